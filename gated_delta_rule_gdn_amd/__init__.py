@@ -11,6 +11,9 @@ are not on a GPU.
     o      = recurrent_fwd(q, k, v, log_alpha, b, w, state, state_idx=None)
                                       # T tokens per sequence against a state pool (fp32/bf16)
 
+The operators around the recurrence (short_conv_fwd and so on) are in ``layer`` and are
+functions of this package too.
+
 Layouts: q, k [B,T,H_k,d_k]; v, w [B,T,H_v,d_v]; log_alpha, b [B,T,H_v,d_k];
 states [N,H_v,d_k,d_v] fp32. ``log_alpha`` is log of the decay (<= 0). Decode inputs drop
 the T axis: q, k [N,H_k,d_k], v, w [N,H_v,d_v], log_alpha, b [N,H_v,d_k].
@@ -97,6 +100,7 @@ def lib() -> ctypes.CDLL:
         L.gdn2_chunk_bwd.argtypes = [vp] * 8 + [i32] + [vp] * 9 + [dp, vp, sz, vp]
         L.gdn2_chunk_bwd_states.restype = i32
         L.gdn2_chunk_bwd_states.argtypes = [vp] * 8 + [i32] + [vp] * 10 + [dp, vp, sz, vp]
+        layer.declare(L)
         _lib = L
     return _lib
 
@@ -619,3 +623,8 @@ def gated_recurrent_fwd(mode: str, q, k, v, log_alpha, beta, state, beta_v=None,
 
 def abi_version() -> int:
     return int(lib().gdn2_abi_version())
+
+
+from . import layer  # noqa: E402  (it uses the helpers above)
+from .layer import (short_conv_bwd, short_conv_bwd_workspace_bytes,  # noqa: E402,F401
+                    short_conv_fwd, short_conv_step)

@@ -116,6 +116,43 @@ struct GateBwdArgs {
     bool bf16;
 };
 
+// The sequences on a token axis of `total` tokens: n of them, packed (offsets cu[n + 1] in
+// device memory) or dense (cu NULL, seqlen tokens each).
+struct SeqMap {
+    const int32_t *cu;
+    int n, seqlen, total;
+};
+
+// The short convolution over prompts (gdn2_short_conv_fwd, gdn2_short_conv_bwd).
+struct ConvArgs {
+    const void *x = nullptr, *dy = nullptr;
+    const float *weight = nullptr, *bias = nullptr, *state0 = nullptr, *dstate_T = nullptr;
+    void *y = nullptr, *dx = nullptr;
+    float *state_T = nullptr, *dstate0 = nullptr, *dweight = nullptr, *dbias = nullptr;
+    float *partial = nullptr;        // [tiles][width + 1][channels] sums of a backward call
+    SeqMap map;
+    int64_t x_stride;                // elements from one token of x to the next
+    int channels, width, tile;
+    bool silu, bf16, grad_bf16 = false;
+};
+int conv_tile(int64_t tokens, int channels);             // tokens a wave takes
+int64_t conv_tiles(int64_t tokens, int tile);            // at least one
+hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t st);
+hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t st);
+
+// The short convolution of single tokens (gdn2_short_conv_step).
+struct ConvStepArgs {
+    const void *x;
+    const float *weight, *bias;
+    float *state;                    // [num_slots][width - 1][channels]
+    const int32_t *idx;
+    void *y;
+    int64_t x_stride;
+    int num_seqs, ntok, num_slots, channels, width;
+    bool silu, bf16;
+};
+hipError_t launch_conv_step(const ConvStepArgs &a, hipStream_t st);
+
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t st);
 hipError_t launch_map_gates(const GateArgs &a, hipStream_t st);
 hipError_t launch_map_gates_bwd(const GateBwdArgs &a, hipStream_t st);

@@ -1,0 +1,181 @@
+// gdn2_layer_api.cpp -- the extern "C" boundary of the operators around the recurrence: argument
+// validation, workspace sizing and dispatch. Every check runs on the host before anything is
+// enqueued, so a rejected call has no effect on the device.
+#include <hip/hip_runtime.h>
+
+#include "gdn2.h"
+#include "gdn2_internal.h"
+
+namespace {
+
+using gdn2::report;
+using gdn2::report_hip;
+
+constexpr int64_t kMaxElems = (int64_t{1} << 40);    // bound on any tensor's element count
+constexpr int64_t kMaxTokens = (int64_t{1} << 30);   // token arithmetic stays in 32 bits
+constexpr int32_t kMaxChannels = 1 << 20;
+
+gdn2_status ok() { return report(GDN2_OK, ""); }
+
+gdn2_status done(hipError_t e, const char *where) {
+    return e == hipSuccess ? ok() : report_hip(e, where);
+}
+
+bool dtype_ok(int32_t t) { return t == GDN2_F32 || t == GDN2_BF16; }
+
+// An output that is the same buffer as an input or as another output. NULLs are not compared.
+template <int NO, int NI>
+bool aliases(const void *const (&outs)[NO], const void *const (&ins)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        if (!outs[i]) continue;
+        for (int j = 0; j < NI; ++j)
+            if (outs[i] == ins[j]) return true;
+        for (int j = i + 1; j < NO; ++j)
+            if (outs[i] == outs[j]) return true;
+    }
+    return false;
+}
+
+// The token layout shared by the prompt calls: dense, or packed with cu_seqlens.
+gdn2_status check_tokens(int32_t batch, int32_t seqlen, int32_t num_seqs, bool packed) {
+    if (seqlen < 0) return report(GDN2_ERR_BAD_SHAPE, "seqlen must be >= 0");
+    if (packed) {
+        if (batch != 1) return report(GDN2_ERR_BAD_SHAPE, "packed batches need batch = 1");
+        if (num_seqs < 1) return report(GDN2_ERR_BAD_SHAPE, "num_seqs must be >= 1");
+    } else if (batch < 1) {
+        return report(GDN2_ERR_BAD_SHAPE, "batch must be >= 1");
+    }
+    if (static_cast<int64_t>(batch) * seqlen > kMaxTokens || num_seqs > kMaxTokens)
+        return report(GDN2_ERR_BAD_SHAPE, "more than 2^30 tokens or sequences");
+    return GDN2_OK;
+}
+
+gdn2::SeqMap seq_map(const int32_t *cu, int32_t batch, int32_t seqlen, int32_t num_seqs) {
+    return gdn2::SeqMap{cu, cu ? num_seqs : batch, seqlen, batch * seqlen};
+}
+
+// A token stride: 0 means contiguous. False if it is too small or the tensor too large.
+bool take_stride(int64_t given, int64_t row, int64_t tokens, int64_t *out) {
+    *out = given == 0 ? row : given;
+    return *out >= row && *out <= kMaxElems && tokens * *out <= kMaxElems;
+}
+
+// ---- short convolution -------------------------------------------------------------------
+
+gdn2_status check_conv(const gdn2_conv_dims *d, bool packed, bool backward) {
+    if (!d) return report(GDN2_ERR_NULL_ARG, "dims is NULL");
+    if (!dtype_ok(d->dtype)) return report(GDN2_ERR_UNSUPPORTED, "dtype must be GDN2_F32 or GDN2_BF16");
+    if (backward && d->grad_dtype != GDN2_F32 && d->grad_dtype != d->dtype)
+        return report(GDN2_ERR_UNSUPPORTED, "grad_dtype must be GDN2_F32 or dtype");
+    if (d->width < 2 || d->width > 4) return report(GDN2_ERR_UNSUPPORTED, "width must be 2, 3 or 4");
+    if (d->channels < 1 || d->channels > kMaxChannels)
+        return report(GDN2_ERR_BAD_SHAPE, "channels must be 1 .. 2^20");
+    const gdn2_status st = check_tokens(d->batch, d->seqlen, d->num_seqs, packed);
+    if (st != GDN2_OK) return st;
+    int64_t s;
+    if (!take_stride(d->x_stride, d->channels, static_cast<int64_t>(d->batch) * d->seqlen, &s))
+        return report(GDN2_ERR_BAD_SHAPE, "x_stride is smaller than channels or the tensor too large");
+    const int64_t nseq = packed ? d->num_seqs : d->batch;
+    if (nseq * d->channels * 3 > kMaxElems) return report(GDN2_ERR_BAD_SHAPE, "state tensor too large");
+    return GDN2_OK;
+}
+
+gdn2::ConvArgs conv_args(const gdn2_conv_dims *d, const void *x, const float *weight,
+                         const float *bias, const float *state0, const int32_t *cu) {
+    gdn2::ConvArgs a;
+    a.x = x; a.weight = weight; a.bias = bias; a.state0 = state0;
+    a.map = seq_map(cu, d->batch, d->seqlen, d->num_seqs);
+    a.x_stride = d->x_stride ? d->x_stride : d->channels;
+    a.channels = d->channels; a.width = d->width;
+    a.tile = gdn2::conv_tile(a.map.total, a.channels);
+    a.silu = d->silu != 0;
+    a.bf16 = d->dtype == GDN2_BF16;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn2_status gdn2_short_conv_fwd(const void *x, const float *weight, const float *bias,
+                                const float *state0, const int32_t *cu_seqlens, void *y,
+                                float *state_T, const gdn2_conv_dims *dims, void *stream) {
+    gdn2_status st = check_conv(dims, cu_seqlens != nullptr, false);
+    if (st != GDN2_OK) return st;
+    const bool tokens = dims->batch > 0 && dims->seqlen > 0;
+    if (!weight || (tokens && (!x || !y)))
+        return report(GDN2_ERR_NULL_ARG, "x, weight and y are required");
+    const void *outs[] = {y, state_T}, *ins[] = {x, weight, bias, state0, cu_seqlens};
+    if (aliases(outs, ins)) return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input or the other output");
+    if (!tokens && !state_T) return ok();
+    gdn2::ConvArgs a = conv_args(dims, x, weight, bias, state0, cu_seqlens);
+    a.y = y; a.state_T = state_T;
+    return done(gdn2::launch_conv_fwd(a, static_cast<hipStream_t>(stream)), "gdn2_short_conv_fwd launch");
+}
+
+size_t gdn2_short_conv_bwd_workspace_bytes(const gdn2_conv_dims *dims) {
+    if (!dims || check_conv(dims, dims->num_seqs > 0 && dims->batch == 1, true) != GDN2_OK) return 0;
+    const int64_t tokens = static_cast<int64_t>(dims->batch) * dims->seqlen;
+    const int64_t tiles = gdn2::conv_tiles(tokens, gdn2::conv_tile(tokens, dims->channels));
+    return static_cast<size_t>(tiles) * (dims->width + 1) * dims->channels * sizeof(float);
+}
+
+gdn2_status gdn2_short_conv_bwd(const void *x, const float *weight, const float *bias,
+                                const float *state0, const int32_t *cu_seqlens, const void *dy,
+                                const float *dstate_T, void *dx, float *dweight, float *dbias,
+                                float *dstate0, const gdn2_conv_dims *dims, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    gdn2_status st = check_conv(dims, cu_seqlens != nullptr, true);
+    if (st != GDN2_OK) return st;
+    const bool tokens = dims->batch > 0 && dims->seqlen > 0;
+    if (!weight || !dweight || (tokens && (!x || !dy || !dx)))
+        return report(GDN2_ERR_NULL_ARG, "x, weight, dy, dx and dweight are required");
+    if (bias && !dbias) return report(GDN2_ERR_NULL_ARG, "a bias needs dbias");
+    const void *outs[] = {dx, dweight, dbias, dstate0};
+    const void *ins[] = {x, weight, bias, state0, cu_seqlens, dy, dstate_T, workspace};
+    if (aliases(outs, ins)) return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input, the workspace or another output");
+    gdn2::ConvArgs a = conv_args(dims, x, weight, bias, state0, cu_seqlens);
+    const size_t need = static_cast<size_t>(gdn2::conv_tiles(a.map.total, a.tile)) * (a.width + 1) *
+                        a.channels * sizeof(float);
+    if (!workspace) return report(GDN2_ERR_WORKSPACE, "workspace is NULL");
+    if (workspace_bytes < need) return report(GDN2_ERR_WORKSPACE, "workspace is too small");
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+        return report(GDN2_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    a.dy = dy; a.dstate_T = dstate_T; a.dx = dx; a.dweight = dweight; a.dbias = dbias; a.dstate0 = dstate0;
+    a.partial = static_cast<float *>(workspace);
+    a.grad_bf16 = dims->grad_dtype == GDN2_BF16;
+    return done(gdn2::launch_conv_bwd(a, static_cast<hipStream_t>(stream)), "gdn2_short_conv_bwd launch");
+}
+
+gdn2_status gdn2_short_conv_step(const void *x, const float *weight, const float *bias,
+                                 float *conv_state, const int32_t *state_idx, int32_t num_slots,
+                                 void *y, const gdn2_conv_dims *dims, void *stream) {
+    if (dims && dims->batch == 0) {     // an empty batch: the other dims still have to be right
+        gdn2_conv_dims one = *dims;
+        one.batch = 1;
+        const gdn2_status st = check_conv(&one, false, false);
+        return st != GDN2_OK ? st : ok();
+    }
+    gdn2_status st = check_conv(dims, false, false);
+    if (st != GDN2_OK) return st;
+    if (dims->seqlen < 1) return report(GDN2_ERR_BAD_SHAPE, "seqlen (tokens per sequence) must be >= 1");
+    if (num_slots < 0) return report(GDN2_ERR_BAD_SHAPE, "num_slots must be >= 0");
+    if (!state_idx && num_slots < dims->batch)
+        return report(GDN2_ERR_BAD_SHAPE, "without state_idx, num_slots must be >= batch");
+    if (static_cast<int64_t>(num_slots) * dims->channels * 3 > kMaxElems)
+        return report(GDN2_ERR_BAD_SHAPE, "state tensor too large");
+    if (!x || !weight || !y || (num_slots > 0 && !conv_state))
+        return report(GDN2_ERR_NULL_ARG, "x, weight, conv_state and y are required");
+    const void *outs[] = {y, conv_state}, *ins[] = {x, weight, bias, state_idx};
+    if (aliases(outs, ins)) return report(GDN2_ERR_BAD_SHAPE, "y or the state aliases an input or the other");
+    gdn2::ConvStepArgs a;
+    a.x = x; a.weight = weight; a.bias = bias; a.state = conv_state; a.idx = state_idx; a.y = y;
+    a.x_stride = dims->x_stride ? dims->x_stride : dims->channels;
+    a.num_seqs = dims->batch; a.ntok = dims->seqlen; a.num_slots = num_slots;
+    a.channels = dims->channels; a.width = dims->width;
+    a.silu = dims->silu != 0;
+    a.bf16 = dims->dtype == GDN2_BF16;
+    return done(gdn2::launch_conv_step(a, static_cast<hipStream_t>(stream)), "gdn2_short_conv_step launch");
+}
+
+}  // extern "C"

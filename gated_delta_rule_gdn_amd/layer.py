@@ -1,0 +1,240 @@
+"""The operators around the recurrence, bound to libgdn2.so: the short causal convolution over
+prompts, its gradients and its form for single tokens.
+
+    y, state_T = short_conv_fwd(x, weight, bias=None, state0=None, cu_seqlens=None, silu=False)
+    grads      = short_conv_bwd(x, weight, dy, ...)
+    y          = short_conv_step(x, weight, conv_state, ...)        # conv_state updated in place
+
+As in the rest of the package, these functions check shapes, allocate outputs and workspaces
+and call the C ABI (``include/gdn2.h``) on the current HIP stream of the tensors' device. Token
+inputs may be column slices of a wider tensor (one stride from token to token); everything else
+is contiguous. Gradients are returned in a dict, ``d`` before each input's name: those of token
+tensors in the type of the incoming gradient, those of parameters and states in fp32.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import _dtype_code, _need_gpu, _ptr, _raise_on, lib
+
+_i32, _i64, _f32, _vp, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p,
+                              ctypes.c_size_t)
+
+
+class ConvDims(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("seqlen", _i32), ("num_seqs", _i32), ("channels", _i32),
+                ("width", _i32), ("dtype", _i32), ("grad_dtype", _i32), ("silu", _i32),
+                ("x_stride", _i64)]
+
+
+def declare(L: ctypes.CDLL) -> None:
+    """Argument types of this module's calls (lib() runs it once)."""
+    cd = ctypes.POINTER(ConvDims)
+    for name, restype, argtypes in (
+            ("gdn2_short_conv_fwd", _i32, [_vp] * 7 + [cd, _vp]),
+            ("gdn2_short_conv_bwd_workspace_bytes", _sz, [cd]),
+            ("gdn2_short_conv_bwd", _i32, [_vp] * 11 + [cd, _vp, _sz, _vp]),
+            ("gdn2_short_conv_step", _i32, [_vp] * 5 + [_i32, _vp, cd, _vp])):
+        f = getattr(L, name)
+        f.restype, f.argtypes = restype, argtypes
+
+
+def _call(dev: torch.device, f, *args) -> None:
+    """f(*args, stream) on the device's current stream, with that device current."""
+    if torch.cuda.current_device() == dev.index:
+        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        _raise_on(st)
+
+
+def _on_gpu(name: str, t: torch.Tensor, dev) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _tokens(name: str, t: torch.Tensor, dev, dtype, lead, inner) -> int:
+    """Checks a token input [*lead, *inner] that may be a column slice. Returns the elements
+    from one token to the next."""
+    _on_gpu(name, t, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != lead + inner:
+        raise ValueError(f"{name} must be {list(lead + inner)}, not {list(t.shape)}")
+    row = 1
+    for n in inner:
+        row *= n
+    if t.is_contiguous():
+        return row
+    want = 1
+    for d in range(t.dim() - 1, 1, -1):
+        if t.shape[d] != 1 and t.stride(d) != want:
+            raise ValueError(f"{name}: every token's values must be contiguous")
+        want *= t.shape[d]
+    B, T = lead
+    if T > 1:
+        step = t.stride(1)
+        if B > 1 and t.stride(0) != T * step:
+            raise ValueError(f"{name}: the sequences must follow each other at one token stride")
+    else:
+        step = t.stride(0) if B > 1 else row
+    if step < row:
+        raise ValueError(f"{name}: tokens overlap (stride {step}, {row} values)")
+    return step
+
+
+def _whole(name: str, t: Optional[torch.Tensor], dev, dtype, shape) -> Optional[int]:
+    """Checks a contiguous tensor of one type and shape (None is let through); its pointer."""
+    if t is None:
+        return None
+    _need_gpu(name, t, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _grad_code(name: str, t: torch.Tensor, dtype) -> int:
+    """The type of a call's token gradients: fp32 or the inputs' own."""
+    if t.dtype != torch.float32 and t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype} or torch.float32")
+    return _dtype_code(t.dtype)
+
+
+def _sequences(cu_seqlens, B: int, dev) -> Tuple[int, int]:
+    """(number of sequences, num_seqs of the dims) of a dense or packed batch."""
+    if cu_seqlens is None:
+        return B, 0
+    _need_gpu("cu_seqlens", cu_seqlens, dev)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
+        raise TypeError("cu_seqlens must be a 1-D int32 tensor")
+    N = cu_seqlens.numel() - 1
+    if N < 1 or B != 1:
+        raise ValueError("a packed batch is [1,T,..] with cu_seqlens of N+1 >= 2 offsets")
+    return N, N
+
+
+def _workspace(workspace, need: int, dev) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _need_gpu("workspace", workspace, dev)
+    return workspace
+
+
+# ---- short convolution -------------------------------------------------------------------
+
+
+def _conv_dims(x, weight, bias, cu_seqlens, silu, grad_code) -> Tuple[ConvDims, int]:
+    """The checked dims of a prompt call, and the number of sequences."""
+    dev = x.device
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,C]")
+    B, T, C = x.shape
+    code = _dtype_code(x.dtype)
+    step = _tokens("x", x, dev, x.dtype, (B, T), (C,))
+    if weight.dim() != 2 or weight.shape[0] != C:
+        raise ValueError(f"weight must be fp32 [{C},W]")
+    _whole("weight", weight, dev, torch.float32, (C, weight.shape[1]))
+    _whole("bias", bias, dev, torch.float32, (C,))
+    N, num_seqs = _sequences(cu_seqlens, B, dev)
+    return ConvDims(B, T, num_seqs, C, weight.shape[1], code, grad_code, 1 if silu else 0, step), N
+
+
+def short_conv_fwd(x, weight, bias: Optional[torch.Tensor] = None,
+                   state0: Optional[torch.Tensor] = None,
+                   cu_seqlens: Optional[torch.Tensor] = None, silu: bool = False,
+                   output_final_state: bool = True, out: Optional[torch.Tensor] = None,
+                   final_state: Optional[torch.Tensor] = None
+                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The short causal depthwise convolution over prompts. x [B,T,C] (may be a column slice);
+    weight fp32 [C,W], W = 2..4, the last tap on the current token; bias fp32 [C]; state0 fp32
+    [N,W-1,C], the inputs before each sequence (None: zeros); cu_seqlens int32 [N+1] for a
+    packed batch. Returns (y [B,T,C], state_T fp32 [N,W-1,C] or None): state_T is what
+    recurrent_fwd and short_conv_step keep in their conv_state. It must not be state0's own
+    buffer."""
+    d, N = _conv_dims(x, weight, bias, cu_seqlens, silu, 0)
+    dev, shape = x.device, tuple(x.shape)
+    f32 = torch.float32
+    st_shape = (N, d.width - 1, d.channels)
+    s0 = _whole("state0", state0, dev, f32, st_shape)
+    y = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
+    py = _whole("out", y, dev, x.dtype, shape)
+    state_T = None
+    if output_final_state:
+        state_T = torch.empty(st_shape, dtype=f32, device=dev) if final_state is None else final_state
+    ps = _whole("final_state", state_T, dev, f32, st_shape)
+    _call(dev, lib().gdn2_short_conv_fwd, x.data_ptr(), weight.data_ptr(), _ptr(bias), s0,
+          _ptr(cu_seqlens), py, ps, ctypes.byref(d))
+    return y, state_T
+
+
+def short_conv_bwd(x, weight, dy, bias: Optional[torch.Tensor] = None,
+                   state0: Optional[torch.Tensor] = None,
+                   cu_seqlens: Optional[torch.Tensor] = None, silu: bool = False,
+                   dstate_T: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of short_conv_fwd given dy = dL/dy [B,T,C] (x's dtype or fp32) and dstate_T =
+    dL/dstate_T (None: zero). Returns dx (dy's dtype), dweight fp32 [C,W], and dbias, dstate0
+    where the call has a bias, a state0."""
+    d, N = _conv_dims(x, weight, bias, cu_seqlens, silu, _grad_code("dy", dy, x.dtype))
+    dev, shape = x.device, tuple(x.shape)
+    f32 = torch.float32
+    st_shape = (N, d.width - 1, d.channels)
+    s0 = _whole("state0", state0, dev, f32, st_shape)
+    pdy = _whole("dy", dy, dev, dy.dtype, shape)
+    pds = _whole("dstate_T", dstate_T, dev, f32, st_shape)
+    out = {"dx": torch.empty(shape, dtype=dy.dtype, device=dev),
+           "dweight": torch.empty(weight.shape, dtype=f32, device=dev)}
+    if bias is not None:
+        out["dbias"] = torch.empty(bias.shape, dtype=f32, device=dev)
+    if state0 is not None:
+        out["dstate0"] = torch.empty(st_shape, dtype=f32, device=dev)
+    ws = _workspace(workspace, lib().gdn2_short_conv_bwd_workspace_bytes(ctypes.byref(d)), dev)
+    _call(dev, lib().gdn2_short_conv_bwd, x.data_ptr(), weight.data_ptr(), _ptr(bias), s0,
+          _ptr(cu_seqlens), pdy, pds, out["dx"].data_ptr(), out["dweight"].data_ptr(),
+          _ptr(out.get("dbias")), _ptr(out.get("dstate0")), ctypes.byref(d), ws.data_ptr(),
+          ws.numel())
+    return out
+
+
+def short_conv_bwd_workspace_bytes(batch: int, seqlen: int, channels: int, width: int,
+                                   dtype: torch.dtype, num_seqs: int = 0) -> int:
+    d = ConvDims(batch, seqlen, num_seqs, channels, width, _dtype_code(dtype), 0, 0, 0)
+    return int(lib().gdn2_short_conv_bwd_workspace_bytes(ctypes.byref(d)))
+
+
+def _state_idx(state_idx, N: int, dev) -> Optional[int]:
+    if state_idx is None:
+        return None
+    _need_gpu("state_idx", state_idx, dev)
+    if state_idx.dtype != torch.int32 or state_idx.shape != (N,):
+        raise ValueError(f"state_idx must be int32 [{N}]")
+    return state_idx.data_ptr()
+
+
+def short_conv_step(x, weight, conv_state, bias: Optional[torch.Tensor] = None,
+                    state_idx: Optional[torch.Tensor] = None, silu: bool = False,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """T tokens of each of N sequences, x [N,T,C], against a pool of conv states fp32
+    [num_slots,W-1,C], updated in place. state_idx int32 [N]: the slot of each sequence (None:
+    slot n); an entry outside the pool marks padding (zero y rows, no state touched). Returns
+    y [N,T,C]."""
+    d, N = _conv_dims(x, weight, bias, None, silu, 0)
+    dev, shape = x.device, tuple(x.shape)
+    if conv_state.dim() != 3:
+        raise ValueError(f"conv_state must be fp32 [num_slots,{d.width - 1},{d.channels}]")
+    slots = conv_state.shape[0]
+    ps = _whole("conv_state", conv_state, dev, torch.float32, (slots, d.width - 1, d.channels))
+    y = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
+    py = _whole("out", y, dev, x.dtype, shape)
+    _call(dev, lib().gdn2_short_conv_step, x.data_ptr(), weight.data_ptr(), _ptr(bias), ps,
+          _state_idx(state_idx, N, dev), slots, py, ctypes.byref(d))
+    return y

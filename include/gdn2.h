@@ -26,7 +26,11 @@
  *                               FG2-GDN, FG2-GDN+) mapped onto these, and their gradients
  *                               mapped back;
  *   - gdn2_chunk_fwd_noalloc    the chunked forward on a static device workspace, for
- *                               callers that cannot allocate.
+ *                               callers that cannot allocate;
+ *   - gdn2_short_conv_fwd, gdn2_short_conv_bwd, gdn2_short_conv_step
+ *                               the short causal convolution before the recurrence, over
+ *                               prompts, its gradients, and for single tokens.
+ * Calls added since version 9 of the ABI change none of its calls, so the number stays.
  *
  * Conventions (the pages are silent on these; this is the reading the library implements):
  *   - o_t reads the state AFTER the update of token t.
@@ -439,6 +443,88 @@ gdn2_status gdn2_map_gates_bwd(int32_t mode, const gdn2_dims *dims, const void *
                                const float *dla_m, const float *db_m, const float *dw_m,
                                float *dq, float *dk, float *dv, float *dlog_alpha,
                                float *dbeta, float *dbeta_v, void *stream);
+
+/*
+ * ---- Around the recurrence ---------------------------------------------------------------
+ *
+ * The calls below share these conventions on top of those at the head of this file:
+ *   - Token tensors are [B, T, ...] (dense) or [1, T, ...] with cu_seqlens (packed). A packed
+ *     batch may end before T (cu_seqlens[N] <= T): rows behind the last sequence are neither
+ *     read nor written. Offsets are held inside [0, T] on the device, so a wrong table gives
+ *     wrong results but no access outside the tensors; it has to be non-decreasing. Empty
+ *     sequences are allowed and hand their initial state on.
+ *   - A stride field gives the elements from one token to the next of an input that is a column
+ *     slice of a wider tensor (a projection's output); 0 means contiguous. The sequences of a
+ *     dense batch follow each other at seqlen times that stride. Outputs are contiguous.
+ *   - grad_dtype is the type of the token gradients that go in and come out: GDN2_F32, or the
+ *     call's dtype. Gradients of parameters and states are fp32.
+ *   - All sums, states and statistics are held in fp32. Every call gives the same bits for the
+ *     same arguments (no atomics).
+ *   - At most 2^30 tokens and 2^20 channels. Outputs must not overlap inputs, the workspace or
+ *     each other (the same pointer twice is refused).
+ */
+
+/*
+ * The short causal depthwise convolution that the burn-gdn2 diagram ("Architecture",
+ * use_short_conv) puts before the recurrence, over whole prompts; gdn2_fusion.conv_weight is
+ * its form inside gdn2_recurrent_fwd, with the same weights and states. With W = width taps:
+ *     a_t[c] = bias[c] + sum_{j < W} weight[c][j] x_{t - W + 1 + j}[c],   y_t = silu(a_t) or a_t
+ * where the W - 1 inputs before a sequence are its rows of state0 (oldest first), or zeros.
+ */
+typedef struct gdn2_conv_dims {
+    int32_t batch, seqlen, num_seqs;   /* as in gdn2_dims */
+    int32_t channels;                  /* C >= 1 */
+    int32_t width;                     /* W: 2, 3 or 4 taps */
+    int32_t dtype;                     /* gdn2_dtype of x and y */
+    int32_t grad_dtype;                /* of dy and dx (backward only) */
+    int32_t silu;                      /* nonzero: y = silu(a) */
+    int64_t x_stride;                  /* elements between tokens of x, >= C, or 0 */
+} gdn2_conv_dims;
+
+/*
+ *   x           device [B, T, C]
+ *   weight      device fp32 [C][W];  bias  device fp32 [C], or NULL
+ *   state0      device fp32 [N][W-1][C], the inputs before each sequence, or NULL for zeros
+ *   cu_seqlens  device int32 [N+1] for a packed batch, or NULL
+ *   y           device [B, T, C]
+ *   state_T     device fp32 [N][W-1][C], the last W-1 inputs of each sequence (of state0 and x
+ *               together, where it is shorter), or NULL. A row of a conv_state pool has this
+ *               layout, so decoding goes on from it.
+ */
+gdn2_status gdn2_short_conv_fwd(const void *x, const float *weight, const float *bias,
+                                const float *state0, const int32_t *cu_seqlens, void *y,
+                                float *state_T, const gdn2_conv_dims *dims, void *stream);
+
+/* Bytes of device workspace gdn2_short_conv_bwd needs, or 0 if the dims are invalid. */
+size_t gdn2_short_conv_bwd_workspace_bytes(const gdn2_conv_dims *dims);
+
+/*
+ * Gradients of gdn2_short_conv_fwd, which is formed again from its inputs.
+ *   dy          device [B, T, C] (grad_dtype): dL/dy
+ *   dstate_T    device fp32 [N][W-1][C]: dL/dstate_T, or NULL for zero
+ *   dx          device [B, T, C] (grad_dtype)
+ *   dweight     device fp32 [C][W];  dbias  device fp32 [C], required with a bias
+ *   dstate0     device fp32 [N][W-1][C], or NULL to skip it
+ *   workspace   at least gdn2_short_conv_bwd_workspace_bytes() bytes, 256-byte aligned
+ */
+gdn2_status gdn2_short_conv_bwd(const void *x, const float *weight, const float *bias,
+                                const float *state0, const int32_t *cu_seqlens, const void *dy,
+                                const float *dstate_T, void *dx, float *dweight, float *dbias,
+                                float *dstate0, const gdn2_conv_dims *dims, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * The convolution of T tokens (seqlen >= 1) of each of N sequences (batch >= 0) against a pool
+ * of conv states, as gdn2_recurrent_fwd runs the recurrence against its pool.
+ *   x, y        device [N, T, C]
+ *   conv_state  device fp32 [num_slots][W-1][C], read and updated in place
+ *   state_idx   device int32 [N], the slot of each sequence, or NULL (slot n). An entry outside
+ *               [0, num_slots) marks a padding sequence: zero y rows, no state touched. The
+ *               valid entries must be distinct.
+ */
+gdn2_status gdn2_short_conv_step(const void *x, const float *weight, const float *bias,
+                                 float *conv_state, const int32_t *state_idx, int32_t num_slots,
+                                 void *y, const gdn2_conv_dims *dims, void *stream);
 
 /*
  * Host helper: checks a HOST copy of cu_seqlens (N+1 entries) against total tokens T.
