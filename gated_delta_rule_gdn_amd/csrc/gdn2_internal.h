@@ -153,6 +153,41 @@ struct ConvStepArgs {
 };
 hipError_t launch_conv_step(const ConvStepArgs &a, hipStream_t st);
 
+// The selective scan over prompts (gdn2_selective_scan_fwd, gdn2_selective_scan_bwd).
+struct ScanArgs {
+    const void *x, *dt, *B, *C, *gate;
+    const float *A, *D, *dt_bias, *S0;
+    void *o = nullptr;
+    float *S_T = nullptr;
+    SeqMap map;
+    int64_t x_stride, dt_stride, b_stride, c_stride, gate_stride;
+    int channels, d_state, groups, tile;
+    bool softplus, bf16;
+    bool chained;                    // sequences reach over tiles: the arrays below are used
+    float *tiles_h = nullptr;        // [tiles][d_state][channels]: states reached, then entering
+    float *tiles_dt = nullptr;       // [tiles][channels]: sums of dt
+    int32_t *tiles_pass = nullptr;   // [tiles]: whether one sequence passes through the whole tile
+};
+int scan_parts(int d_state);                              // lanes that share a channel's states
+int scan_blocks(int channels, int groups, int parts);     // workgroups across the channels
+int scan_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed);
+int scan_tiles(int total, int tile);
+bool scan_chained(int batch, int seqlen, bool packed, int tile);
+hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st);
+
+// The selective scan of single tokens (gdn2_selective_scan_step).
+struct ScanStepArgs {
+    const void *x, *dt, *B, *C, *gate;
+    const float *A, *D, *dt_bias;
+    void *state;                     // [num_slots][channels][d_state], fp32 or bf16
+    const int32_t *idx;
+    void *o;
+    int64_t x_stride, dt_stride, b_stride, c_stride, gate_stride;
+    int num_seqs, ntok, num_slots, channels, d_state, groups;
+    bool softplus, bf16, state_bf16;
+};
+hipError_t launch_scan_step(const ScanStepArgs &a, hipStream_t st);
+
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t st);
 hipError_t launch_map_gates(const GateArgs &a, hipStream_t st);
 hipError_t launch_map_gates_bwd(const GateBwdArgs &a, hipStream_t st);

@@ -93,6 +93,78 @@ gdn2::ConvArgs conv_args(const gdn2_conv_dims *d, const void *x, const float *we
     return a;
 }
 
+// ---- selective scan ----------------------------------------------------------------------
+
+gdn2_status check_scan(const gdn2_scan_dims *d, bool packed, bool backward) {
+    if (!d) return report(GDN2_ERR_NULL_ARG, "dims is NULL");
+    if (!dtype_ok(d->dtype)) return report(GDN2_ERR_UNSUPPORTED, "dtype must be GDN2_F32 or GDN2_BF16");
+    if (backward && d->grad_dtype != GDN2_F32 && d->grad_dtype != d->dtype)
+        return report(GDN2_ERR_UNSUPPORTED, "grad_dtype must be GDN2_F32 or dtype");
+    if (d->channels < 1 || d->channels > kMaxChannels)
+        return report(GDN2_ERR_BAD_SHAPE, "channels must be 1 .. 2^20");
+    if (d->groups < 1 || d->channels % d->groups != 0)
+        return report(GDN2_ERR_BAD_SHAPE, "channels must be a multiple of groups");
+    if (d->d_state < 1) return report(GDN2_ERR_BAD_SHAPE, "d_state must be >= 1");
+    if (d->d_state > 128) return report(GDN2_ERR_UNSUPPORTED, "d_state must be 1 .. 128");
+    const gdn2_status st = check_tokens(d->batch, d->seqlen, d->num_seqs, packed);
+    if (st != GDN2_OK) return st;
+    const int64_t tokens = static_cast<int64_t>(d->batch) * d->seqlen;
+    const int64_t bc = static_cast<int64_t>(d->groups) * d->d_state;
+    int64_t s;
+    if (!take_stride(d->x_stride, d->channels, tokens, &s) ||
+        !take_stride(d->dt_stride, d->channels, tokens, &s) ||
+        !take_stride(d->gate_stride, d->channels, tokens, &s) ||
+        !take_stride(d->b_stride, bc, tokens, &s) || !take_stride(d->c_stride, bc, tokens, &s))
+        return report(GDN2_ERR_BAD_SHAPE, "a stride is smaller than its row or a tensor too large");
+    const int64_t nseq = packed ? d->num_seqs : d->batch;
+    if (nseq * d->channels * d->d_state > kMaxElems)
+        return report(GDN2_ERR_BAD_SHAPE, "state tensor too large");
+    return GDN2_OK;
+}
+
+template <typename Args>
+void scan_inputs(Args *a, const gdn2_scan_dims *d, const void *x, const void *dt, const float *A,
+                 const void *B, const void *C, const float *D, const void *gate, const float *dt_bias) {
+    a->x = x; a->dt = dt; a->A = A; a->B = B; a->C = C; a->D = D; a->gate = gate; a->dt_bias = dt_bias;
+    const int64_t bc = static_cast<int64_t>(d->groups) * d->d_state;
+    a->x_stride = d->x_stride ? d->x_stride : d->channels;
+    a->dt_stride = d->dt_stride ? d->dt_stride : d->channels;
+    a->gate_stride = d->gate_stride ? d->gate_stride : d->channels;
+    a->b_stride = d->b_stride ? d->b_stride : bc;
+    a->c_stride = d->c_stride ? d->c_stride : bc;
+    a->channels = d->channels; a->d_state = d->d_state; a->groups = d->groups;
+    a->softplus = d->dt_softplus != 0;
+    a->bf16 = d->dtype == GDN2_BF16;
+}
+
+constexpr size_t kAlign = 256;
+size_t padded(size_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
+
+// Sizes of the forward's workspace: the tiles' states, sums of dt and pass flags.
+struct ScanPlan {
+    int tile, tiles;
+    bool chained;
+    size_t states, sums, flags;
+    ScanPlan(const gdn2_scan_dims *d, bool packed) {
+        tile = gdn2::scan_tile(d->channels, d->groups, d->d_state, d->batch, d->seqlen, packed);
+        tiles = gdn2::scan_tiles(d->batch * d->seqlen, tile);
+        chained = gdn2::scan_chained(d->batch, d->seqlen, packed, tile);
+        states = padded(static_cast<size_t>(tiles) * d->d_state * d->channels * sizeof(float));
+        sums = padded(static_cast<size_t>(tiles) * d->channels * sizeof(float));
+        flags = padded(static_cast<size_t>(tiles) * sizeof(int32_t));
+    }
+    size_t fwd_bytes() const { return chained ? states + sums + flags : 0; }
+};
+
+gdn2_status check_workspace(const void *ws, size_t bytes, size_t need) {
+    if (need == 0) return GDN2_OK;
+    if (!ws) return report(GDN2_ERR_WORKSPACE, "workspace is NULL");
+    if (bytes < need) return report(GDN2_ERR_WORKSPACE, "workspace is too small");
+    if (reinterpret_cast<uintptr_t>(ws) % kAlign != 0)
+        return report(GDN2_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    return GDN2_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -137,10 +209,8 @@ gdn2_status gdn2_short_conv_bwd(const void *x, const float *weight, const float 
     gdn2::ConvArgs a = conv_args(dims, x, weight, bias, state0, cu_seqlens);
     const size_t need = static_cast<size_t>(gdn2::conv_tiles(a.map.total, a.tile)) * (a.width + 1) *
                         a.channels * sizeof(float);
-    if (!workspace) return report(GDN2_ERR_WORKSPACE, "workspace is NULL");
-    if (workspace_bytes < need) return report(GDN2_ERR_WORKSPACE, "workspace is too small");
-    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
-        return report(GDN2_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    st = check_workspace(workspace, workspace_bytes, need);
+    if (st != GDN2_OK) return st;
     a.dy = dy; a.dstate_T = dstate_T; a.dx = dx; a.dweight = dweight; a.dbias = dbias; a.dstate0 = dstate0;
     a.partial = static_cast<float *>(workspace);
     a.grad_bf16 = dims->grad_dtype == GDN2_BF16;
@@ -176,6 +246,78 @@ gdn2_status gdn2_short_conv_step(const void *x, const float *weight, const float
     a.silu = dims->silu != 0;
     a.bf16 = dims->dtype == GDN2_BF16;
     return done(gdn2::launch_conv_step(a, static_cast<hipStream_t>(stream)), "gdn2_short_conv_step launch");
+}
+
+size_t gdn2_selective_scan_fwd_workspace_bytes(const gdn2_scan_dims *dims) {
+    if (!dims) return 0;
+    const bool packed = dims->num_seqs > 0 && dims->batch == 1;
+    if (check_scan(dims, packed, false) != GDN2_OK) return 0;
+    // sized for whichever layout the caller may use
+    const size_t dense = ScanPlan(dims, false).fwd_bytes(), pk = packed ? ScanPlan(dims, true).fwd_bytes() : 0;
+    return dense > pk ? dense : pk;
+}
+
+gdn2_status gdn2_selective_scan_fwd(const void *x, const void *dt, const float *A, const void *B,
+                                    const void *C, const float *D, const void *gate,
+                                    const float *dt_bias, const float *S0, const int32_t *cu_seqlens,
+                                    void *o, float *S_T, const gdn2_scan_dims *dims, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+    const bool packed = cu_seqlens != nullptr;
+    gdn2_status st = check_scan(dims, packed, false);
+    if (st != GDN2_OK) return st;
+    const bool tokens = dims->batch > 0 && dims->seqlen > 0;
+    if (!A || (tokens && (!x || !dt || !B || !C || !o)))
+        return report(GDN2_ERR_NULL_ARG, "x, dt, A, B, C and o are required");
+    const void *outs[] = {o, S_T};
+    const void *ins[] = {x, dt, A, B, C, D, gate, dt_bias, S0, cu_seqlens, workspace};
+    if (aliases(outs, ins)) return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input, the workspace or the other output");
+    if (!tokens && !S_T) return ok();
+    const ScanPlan p(dims, packed);
+    st = check_workspace(workspace, workspace_bytes, p.fwd_bytes());
+    if (st != GDN2_OK) return st;
+    gdn2::ScanArgs a;
+    scan_inputs(&a, dims, x, dt, A, B, C, D, gate, dt_bias);
+    a.S0 = S0; a.o = o; a.S_T = S_T;
+    a.map = seq_map(cu_seqlens, dims->batch, dims->seqlen, dims->num_seqs);
+    a.tile = p.tile; a.chained = p.chained;
+    if (p.chained) {
+        char *w = static_cast<char *>(workspace);
+        a.tiles_h = reinterpret_cast<float *>(w);
+        a.tiles_dt = reinterpret_cast<float *>(w + p.states);
+        a.tiles_pass = reinterpret_cast<int32_t *>(w + p.states + p.sums);
+    }
+    return done(gdn2::launch_scan_fwd(a, static_cast<hipStream_t>(stream)), "gdn2_selective_scan_fwd launch");
+}
+
+gdn2_status gdn2_selective_scan_step(const void *x, const void *dt, const float *A, const void *B,
+                                     const void *C, const float *D, const void *gate,
+                                     const float *dt_bias, void *state, int32_t state_dtype,
+                                     const int32_t *state_idx, int32_t num_slots, void *o,
+                                     const gdn2_scan_dims *dims, void *stream) {
+    if (!dims) return report(GDN2_ERR_NULL_ARG, "dims is NULL");
+    gdn2_scan_dims d = *dims;
+    if (d.batch == 0) d.batch = 1;      // an empty batch: the other dims still have to be right
+    gdn2_status st = check_scan(&d, false, false);
+    if (st != GDN2_OK) return st;
+    if (state_dtype != GDN2_STATE_F32 && state_dtype != GDN2_STATE_BF16)
+        return report(GDN2_ERR_UNSUPPORTED, "state_dtype must be GDN2_STATE_F32 or GDN2_STATE_BF16");
+    if (dims->batch == 0) return ok();
+    if (d.seqlen < 1) return report(GDN2_ERR_BAD_SHAPE, "seqlen (tokens per sequence) must be >= 1");
+    if (num_slots < 0) return report(GDN2_ERR_BAD_SHAPE, "num_slots must be >= 0");
+    if (!state_idx && num_slots < d.batch)
+        return report(GDN2_ERR_BAD_SHAPE, "without state_idx, num_slots must be >= batch");
+    if (static_cast<int64_t>(num_slots) * d.channels * d.d_state > kMaxElems)
+        return report(GDN2_ERR_BAD_SHAPE, "state tensor too large");
+    if (!x || !dt || !A || !B || !C || !o || (num_slots > 0 && !state))
+        return report(GDN2_ERR_NULL_ARG, "x, dt, A, B, C, the state and o are required");
+    const void *outs[] = {o, state}, *ins[] = {x, dt, A, B, C, D, gate, dt_bias, state_idx};
+    if (aliases(outs, ins)) return report(GDN2_ERR_BAD_SHAPE, "o or the state aliases an input or the other");
+    gdn2::ScanStepArgs a;
+    scan_inputs(&a, dims, x, dt, A, B, C, D, gate, dt_bias);
+    a.state = state; a.idx = state_idx; a.o = o;
+    a.num_seqs = d.batch; a.ntok = d.seqlen; a.num_slots = num_slots;
+    a.state_bf16 = state_dtype == GDN2_STATE_BF16;
+    return done(gdn2::launch_scan_step(a, static_cast<hipStream_t>(stream)), "gdn2_selective_scan_step launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,347 @@
+// gdn2_scan.hip -- the selective state space scan over prompts, and of single tokens against a
+// pool of states.
+//
+// Per channel d and state n, with the step dt_t[d] = softplus(dt_raw + dt_bias) (or their sum):
+//     h_t = exp(dt_t A) h_{t-1} + dt_t B_t[n] x_t,   y_t = sum_n C_t[n] h_t + D x_t,
+//     o_t = y_t silu(gate_t).
+// The recurrence is elementwise in (d, n), with a decay of its own per token, channel and state,
+// so it has no matrix form: its cost is one exp2 and four fp32 operations per (t, d, n) on the
+// vector unit, about four times the time that x, dt, gate and o take from memory at 16 states.
+//
+// A lane owns one channel and up to 16 of its states, which makes the sum over n free of
+// exchanges, and keeps h in registers along the tokens; B and C of eight tokens are staged in LDS
+// for the workgroup's four waves and read by broadcast. Where channels and sequences alone do not
+// fill the chip, the token axis is cut into tiles (packed sequences start and end anywhere in a
+// tile): one pass forms each tile's state from zero and its sum of dt (the decay over a tile is
+// exp(A sum dt)), a second chains the tiles, a third runs them from their true states. That costs
+// the exp2 and three operations once more, so the rule takes it only when it is the faster.
+#include "gdn2_internal.h"
+#include "gdn2_layer.h"
+#include "gdn2_scan.h"
+
+namespace gdn2 {
+
+namespace {
+
+constexpr int kB = 8;        // tokens whose inputs are in flight and whose B and C are staged together
+
+// B (and C) of tokens [t, hi) of a group, staged as fp32 [kB][NP] each, zero where there is none.
+// take() loads this thread's share of a batch into registers, put() writes it to LDS.
+template <typename T, int NP, bool WITH_C>
+struct Stage {
+    static constexpr int ROW = WITH_C ? 2 * NP : NP, PER = (kB * ROW + 255) / 256;
+    float r[PER];
+    __device__ __forceinline__ void take(const ScanArgs &a, int g, int t, int hi) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = threadIdx.x + 256 * i, k = e / ROW, j = e % ROW, n = j % NP;
+            r[i] = 0.f;
+            if (k < kB && t + k < hi && n < a.d_state) {
+                const bool c = WITH_C && j >= NP;
+                const T *p = static_cast<const T *>(c ? a.C : a.B);
+                r[i] = io<T>::ld(p + (t + k) * (c ? a.c_stride : a.b_stride) + g * a.d_state + n);
+            }
+        }
+    }
+    __device__ __forceinline__ void put(float *s) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = threadIdx.x + 256 * i;
+            if (PER * 256 == kB * ROW || e < kB * ROW) s[e] = r[i];
+        }
+    }
+};
+
+// NS floats from LDS, the same address in all lanes of a part.
+template <int NS>
+__device__ __forceinline__ void lds_row(const float *s, float (&v)[NS]) {
+#pragma unroll
+    for (int n = 0; n < NS; n += 4) {
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(s + n);
+        v[n] = x.x; v[n + 1] = x.y; v[n + 2] = x.z; v[n + 3] = x.w;
+    }
+}
+
+// FINAL: runs a tile from its true state and writes o (and S_T). Otherwise: runs it from zero
+// and writes its state, its sum of dt and whether one sequence passes through all of it.
+template <typename T, int NS, int S, bool FINAL>
+__global__ __launch_bounds__(256) void scan_fwd_kernel(ScanArgs a) {
+    using Lane = ScanLane<NS, S>;
+    constexpr int NP = Lane::NP, ROW = FINAL ? 2 * NP : NP;
+    __shared__ __align__(16) float s_bc[2][kB * ROW];
+    const Lane l(a, blockIdx.x);
+    const int64_t tile = blockIdx.y;
+    const int t0 = static_cast<int>(tile * a.tile);
+    const int t1 = a.map.total - t0 < a.tile ? a.map.total : t0 + a.tile;
+    const T *x = static_cast<const T *>(a.x) + l.c, *dt = static_cast<const T *>(a.dt) + l.c;
+    const T *gate = a.gate ? static_cast<const T *>(a.gate) + l.c : nullptr;
+    T *o = static_cast<T *>(a.o) + l.c;
+    float A2[NS], h[NS];
+    load_rates(a, l, A2);
+    const float bias = a.dt_bias ? a.dt_bias[l.c] : 0.f, skip = a.D ? a.D[l.c] : 0.f;
+    float sum = 0.f;
+    bool pass = false;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = 0.f;
+    for_spans(a.map, t0, t1, [&](const Span &s) {
+        if (s.starts) {
+            if (a.S0) load_state(a, l, a.S0, s.i, h);
+            else
+#pragma unroll
+                for (int n = 0; n < NS; ++n) h[n] = 0.f;
+        } else if (FINAL) {
+            load_tile(a, l, a.tiles_h, tile, h);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NS; ++n) h[n] = 0.f;
+        }
+        pass = !s.starts && !s.ends;
+        if (s.lo < s.hi) {
+            Stage<T, NP, FINAL> st;
+            T xr[kB], dr[kB], gr[kB];
+            auto fetch = [&](int t) {
+                st.take(a, l.g, t, s.hi);
+#pragma unroll
+                for (int k = 0; k < kB; ++k)
+                    if (t + k < s.hi) {
+                        xr[k] = x[(t + k) * a.x_stride];
+                        dr[k] = dt[(t + k) * a.dt_stride];
+                        if (FINAL && gate) gr[k] = gate[(t + k) * a.gate_stride];
+                    }
+            };
+            fetch(s.lo);
+            st.put(s_bc[0]);
+            __syncthreads();
+            int buf = 0;
+            for (int t = s.lo; t < s.hi; t += kB, buf ^= 1) {
+                float xv[kB], dv[kB], gv[kB];
+#pragma unroll
+                for (int k = 0; k < kB; ++k) {
+                    xv[k] = io<T>::val(xr[k]);
+                    dv[k] = io<T>::val(dr[k]);
+                    gv[k] = io<T>::val(gr[k]);
+                }
+                const bool more = t + kB < s.hi;
+                if (more) fetch(t + kB);
+                const int m = s.hi - t;
+#pragma unroll
+                for (int k = 0; k < kB; ++k) {
+                    if (k >= m) break;
+                    float d = dv[k] + bias;
+                    if (a.softplus) d = softplus(d);
+                    const float u = d * xv[k];
+                    const float *row = s_bc[buf] + k * ROW + l.n0;
+                    float b[NS];
+                    lds_row<NS>(row, b);
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+                        h[n] = fmaf(__builtin_amdgcn_exp2f(d * A2[n]), h[n], u * b[n]);
+                    if constexpr (FINAL) {
+                        float c[NS];
+                        lds_row<NS>(row + NP, c);
+                        float y = 0.f;
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) y = fmaf(c[n], h[n], y);
+                        y = fmaf(skip, xv[k], sum_parts<S>(y));
+                        if (gate) y *= silu(gv[k]);
+                        if (l.on && l.part == 0)
+                            io<T>::st(o + (t + k) * static_cast<int64_t>(a.channels), y);
+                    } else {
+                        sum += d;
+                    }
+                }
+                if (more) st.put(s_bc[buf ^ 1]);
+                __syncthreads();
+            }
+        }
+        if (FINAL && s.ends && a.S_T) store_state(a, l, a.S_T, s.i, h);
+    });
+    if constexpr (!FINAL) {
+        store_tile(a, l, a.tiles_h, tile, h);
+        if (l.on && l.part == 0) a.tiles_dt[tile * a.channels + l.c] = sum;
+        if (blockIdx.x == 0 && threadIdx.x == 0) a.tiles_pass[tile] = pass ? 1 : 0;
+    }
+}
+
+// Chains the tiles: the state entering tile i replaces the state tile i reached from zero. One
+// thread per (state, channel); sixteen tiles' loads are in flight together.
+__global__ __launch_bounds__(256) void scan_chain_kernel(ScanArgs a, int tiles) {
+    const int64_t col = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
+    const int64_t cols = static_cast<int64_t>(a.d_state) * a.channels;
+    if (col >= cols) return;
+    const int n = static_cast<int>(col / a.channels), c = static_cast<int>(col - static_cast<int64_t>(n) * a.channels);
+    const float A2 = kLog2e * a.A[static_cast<int64_t>(c) * a.d_state + n];
+    float run = 0.f;
+    constexpr int U = 16;
+    for (int i0 = 0; i0 < tiles; i0 += U) {
+        float hl[U], dl[U];
+        int pl[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (i0 + k < tiles) {
+                hl[k] = a.tiles_h[(i0 + k) * cols + col];
+                dl[k] = a.tiles_dt[static_cast<int64_t>(i0 + k) * a.channels + c];
+                pl[k] = a.tiles_pass[i0 + k];
+            }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i0 + k >= tiles) break;
+            a.tiles_h[(i0 + k) * cols + col] = run;
+            run = pl[k] ? fmaf(__builtin_amdgcn_exp2f(A2 * dl[k]), run, hl[k]) : hl[k];
+        }
+    }
+}
+
+// T tokens of every sequence against its slot of a pool [num_slots][channels][d_state]. LP lanes
+// per channel, four consecutive states per lane: a wave reads and writes 1 KiB of states in a
+// row. Bound by that traffic; each state is read once and written once per call.
+template <typename T, typename TS, int LP, bool VEC>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanStepArgs a) {
+    constexpr int PER = 256 / LP;
+    const int part = threadIdx.x & (LP - 1);
+    const int c = blockIdx.x * PER + threadIdx.x / LP;
+    const bool on = c < a.channels;
+    const int cc = on ? c : a.channels - 1;
+    const int n0 = 4 * part, g = cc / (a.channels / a.groups);
+    float A2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        A2[j] = n0 + j < a.d_state ? kLog2e * a.A[static_cast<int64_t>(cc) * a.d_state + n0 + j] : 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[cc] : 0.f, skip = a.D ? a.D[cc] : 0.f;
+    for (int64_t i = blockIdx.y; i < a.num_seqs; i += gridDim.y) {
+        const int slot = a.idx ? a.idx[i] : static_cast<int>(i);
+        T *o = static_cast<T *>(a.o) + i * a.ntok * static_cast<int64_t>(a.channels) + cc;
+        if (slot < 0 || slot >= a.num_slots) {
+            if (on && part == 0)
+                for (int t = 0; t < a.ntok; ++t) io<T>::st(o + t * static_cast<int64_t>(a.channels), 0.f);
+            continue;
+        }
+        TS *st = static_cast<TS *>(a.state) + (static_cast<int64_t>(slot) * a.channels + cc) * a.d_state + n0;
+        float h[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (VEC) {
+            if (n0 < a.d_state) ldv<TS, 4>(st, h);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n0 + j < a.d_state) h[j] = io<TS>::ld(st + j);
+        }
+        for (int t = 0; t < a.ntok; ++t) {
+            const int64_t row = i * a.ntok + t;
+            const float xv = io<T>::ld(static_cast<const T *>(a.x) + row * a.x_stride + cc);
+            float d = io<T>::ld(static_cast<const T *>(a.dt) + row * a.dt_stride + cc) + bias;
+            const float gv = a.gate ? io<T>::ld(static_cast<const T *>(a.gate) + row * a.gate_stride + cc) : 0.f;
+            const T *pb = static_cast<const T *>(a.B) + row * a.b_stride + g * a.d_state + n0;
+            const T *pc = static_cast<const T *>(a.C) + row * a.c_stride + g * a.d_state + n0;
+            float b[4], cv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = n0 + j < a.d_state;
+                b[j] = in ? io<T>::ld(pb + j) : 0.f;
+                cv[j] = in ? io<T>::ld(pc + j) : 0.f;
+            }
+            if (a.softplus) d = softplus(d);
+            const float u = d * xv;
+            float y = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = fmaf(__builtin_amdgcn_exp2f(d * A2[j]), h[j], u * b[j]);
+                y = fmaf(cv[j], h[j], y);
+            }
+#pragma unroll
+            for (int m = 1; m < LP; m <<= 1) y += __shfl_xor(y, m);
+            y = fmaf(skip, xv, y);
+            if (a.gate) y *= silu(gv);
+            if (on && part == 0) io<T>::st(o + t * static_cast<int64_t>(a.channels), y);
+        }
+        if (!on) continue;
+        if constexpr (VEC) {
+            if (n0 < a.d_state) stv<TS, 4>(st, h);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n0 + j < a.d_state) io<TS>::st(st + j, h[j]);
+        }
+    }
+}
+
+template <typename T, int NS, int S>
+hipError_t launch_fwd(const ScanArgs &a, hipStream_t st) {
+    const int tiles = scan_tiles(a.map.total, a.tile);
+    const dim3 grid(scan_blocks(a.channels, a.groups, S), tiles);
+    if (a.chained) {
+        hipLaunchKernelGGL((scan_fwd_kernel<T, NS, S, false>), grid, dim3(256), 0, st, a);
+        const int64_t cols = static_cast<int64_t>(a.d_state) * a.channels;
+        hipLaunchKernelGGL(scan_chain_kernel, dim3(static_cast<unsigned>((cols + 255) / 256)), dim3(256),
+                           0, st, a, tiles);
+    }
+    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, S, true>), grid, dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_fwd_t(const ScanArgs &a, hipStream_t st) {
+    switch (scan_parts(a.d_state)) {
+    case 1: return a.d_state <= 8 ? launch_fwd<T, 8, 1>(a, st) : launch_fwd<T, 16, 1>(a, st);
+    case 2: return launch_fwd<T, 16, 2>(a, st);
+    case 4: return launch_fwd<T, 16, 4>(a, st);
+    default: return launch_fwd<T, 16, 8>(a, st);
+    }
+}
+
+template <typename T, typename TS, int LP>
+hipError_t launch_step(const ScanStepArgs &a, hipStream_t st) {
+    const dim3 grid(static_cast<unsigned>((a.channels + 256 / LP - 1) / (256 / LP)),
+                    static_cast<unsigned>(a.num_seqs < 65535 ? a.num_seqs : 65535));
+    const bool vec = a.d_state % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
+    if (vec) hipLaunchKernelGGL((scan_step_kernel<T, TS, LP, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((scan_step_kernel<T, TS, LP, false>), grid, dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename T, typename TS>
+hipError_t launch_step_t(const ScanStepArgs &a, hipStream_t st) {
+    if (a.d_state <= 8) return launch_step<T, TS, 2>(a, st);
+    if (a.d_state <= 16) return launch_step<T, TS, 4>(a, st);
+    if (a.d_state <= 32) return launch_step<T, TS, 8>(a, st);
+    if (a.d_state <= 64) return launch_step<T, TS, 16>(a, st);
+    return launch_step<T, TS, 32>(a, st);
+}
+
+}  // namespace
+
+int scan_parts(int d_state) { return d_state <= 16 ? 1 : d_state <= 32 ? 2 : d_state <= 64 ? 4 : 8; }
+
+int scan_blocks(int channels, int groups, int parts) {
+    const int per = channels / groups, w = kScanWaves * 64 / parts;
+    return groups * ((per + w - 1) / w);
+}
+
+int scan_tiles(int total, int tile) { return total > tile ? (total + tile - 1) / tile : 1; }
+
+// Tokens per tile. A dense batch whose sequences alone give 1,024 waves (one per SIMD) is not
+// cut: its tile is a sequence. Otherwise about 2,048 waves, 16 tokens at least.
+int scan_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed) {
+    const int64_t total = static_cast<int64_t>(batch) * seqlen;
+    const int64_t waves = static_cast<int64_t>(kScanWaves) * scan_blocks(channels, groups, scan_parts(d_state));
+    if (!packed && batch <= 65535 && (batch * waves >= 1024 || seqlen <= 16)) return seqlen > 0 ? seqlen : 1;
+    int64_t t = (total * waves / 2048 + kB - 1) / kB * kB;
+    if (t < 16) t = 16;
+    while ((total + t - 1) / t > 65535) t *= 2;
+    return static_cast<int>(t);
+}
+
+// Whether some sequence may reach over a tile's end.
+bool scan_chained(int batch, int seqlen, bool packed, int tile) {
+    return static_cast<int64_t>(batch) * seqlen > tile && (packed || tile != seqlen);
+}
+
+hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
+    return a.bf16 ? launch_fwd_t<bf16_t>(a, st) : launch_fwd_t<float>(a, st);
+}
+
+hipError_t launch_scan_step(const ScanStepArgs &a, hipStream_t st) {
+    if (a.bf16) return a.state_bf16 ? launch_step_t<bf16_t, bf16_t>(a, st) : launch_step_t<bf16_t, float>(a, st);
+    return a.state_bf16 ? launch_step_t<float, bf16_t>(a, st) : launch_step_t<float, float>(a, st);
+}
+
+}  // namespace gdn2

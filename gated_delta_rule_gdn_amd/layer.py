@@ -1,9 +1,11 @@
-"""The operators around the recurrence, bound to libgdn2.so: the short causal convolution over
-prompts, its gradients and its form for single tokens.
+"""The operators around the recurrence, bound to libgdn2.so: the short causal convolution and
+the selective state space scan, over prompts, their gradients, and for single tokens.
 
     y, state_T = short_conv_fwd(x, weight, bias=None, state0=None, cu_seqlens=None, silu=False)
     grads      = short_conv_bwd(x, weight, dy, ...)
     y          = short_conv_step(x, weight, conv_state, ...)        # conv_state updated in place
+    o, S_T     = selective_scan_fwd(x, dt, A, B, C, D=None, gate=None, ...)
+    o          = selective_scan_step(x, dt, A, B, C, state, ...)    # state updated in place
 
 As in the rest of the package, these functions check shapes, allocate outputs and workspaces
 and call the C ABI (``include/gdn2.h``) on the current HIP stream of the tensors' device. Token
@@ -30,14 +32,25 @@ class ConvDims(ctypes.Structure):
                 ("x_stride", _i64)]
 
 
+class ScanDims(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("seqlen", _i32), ("num_seqs", _i32), ("channels", _i32),
+                ("d_state", _i32), ("groups", _i32), ("dtype", _i32), ("grad_dtype", _i32),
+                ("dt_softplus", _i32), ("x_stride", _i64), ("dt_stride", _i64),
+                ("b_stride", _i64), ("c_stride", _i64), ("gate_stride", _i64)]
+
+
 def declare(L: ctypes.CDLL) -> None:
     """Argument types of this module's calls (lib() runs it once)."""
-    cd = ctypes.POINTER(ConvDims)
+    cd, sd = ctypes.POINTER(ConvDims), ctypes.POINTER(ScanDims)
     for name, restype, argtypes in (
             ("gdn2_short_conv_fwd", _i32, [_vp] * 7 + [cd, _vp]),
             ("gdn2_short_conv_bwd_workspace_bytes", _sz, [cd]),
             ("gdn2_short_conv_bwd", _i32, [_vp] * 11 + [cd, _vp, _sz, _vp]),
-            ("gdn2_short_conv_step", _i32, [_vp] * 5 + [_i32, _vp, cd, _vp])):
+            ("gdn2_short_conv_step", _i32, [_vp] * 5 + [_i32, _vp, cd, _vp]),
+            ("gdn2_selective_scan_fwd_workspace_bytes", _sz, [sd]),
+            ("gdn2_selective_scan_fwd", _i32, [_vp] * 12 + [sd, _vp, _sz, _vp]),
+            ("gdn2_selective_scan_step", _i32,
+             [_vp] * 9 + [_i32, _vp, _i32, _vp, sd, _vp])):
         f = getattr(L, name)
         f.restype, f.argtypes = restype, argtypes
 
@@ -238,3 +251,100 @@ def short_conv_step(x, weight, conv_state, bias: Optional[torch.Tensor] = None,
     _call(dev, lib().gdn2_short_conv_step, x.data_ptr(), weight.data_ptr(), _ptr(bias), ps,
           _state_idx(state_idx, N, dev), slots, py, ctypes.byref(d))
     return y
+
+
+# ---- selective scan ----------------------------------------------------------------------
+
+
+def _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, num_seqs, grad_code) -> ScanDims:
+    """The checked dims of a scan call."""
+    dev, dtype = x.device, x.dtype
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,channels]")
+    if B.dim() != 4:
+        raise ValueError("B and C must be [B,T,groups,d_state]")
+    lead, ch = tuple(x.shape[:2]), x.shape[2]
+    G, M = B.shape[2], B.shape[3]
+    code = _dtype_code(dtype)
+    strides = [_tokens("x", x, dev, dtype, lead, (ch,)), _tokens("dt", dt, dev, dtype, lead, (ch,)),
+               _tokens("B", B, dev, dtype, lead, (G, M)), _tokens("C", C, dev, dtype, lead, (G, M)),
+               0 if gate is None else _tokens("gate", gate, dev, dtype, lead, (ch,))]
+    f32 = torch.float32
+    _whole("A", A, dev, f32, (ch, M))
+    _whole("D", D, dev, f32, (ch,))
+    _whole("dt_bias", dt_bias, dev, f32, (ch,))
+    return ScanDims(lead[0], lead[1], num_seqs, ch, M, G, code, grad_code, 1 if dt_softplus else 0,
+                    *strides)
+
+
+def _scan_ptrs(x, dt, A, B, C, D, gate, dt_bias):
+    return (x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
+            _ptr(gate), _ptr(dt_bias))
+
+
+def selective_scan_fwd(x, dt, A, B, C, D: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None,
+                       dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False,
+                       S0: Optional[torch.Tensor] = None,
+                       cu_seqlens: Optional[torch.Tensor] = None,
+                       output_final_state: bool = True, workspace: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None,
+                       final_state: Optional[torch.Tensor] = None
+                       ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The selective state space scan over prompts:
+        h_t = exp(dt_t A) h_{t-1} + dt_t B_t x_t,  y_t = sum_n C_t h_t + D x_t,  o = y silu(gate)
+    x, dt, gate [B,T,channels]; B, C [B,T,groups,d_state] (these five in one dtype, each may be
+    a column slice); A fp32 [channels,d_state]; D, dt_bias fp32 [channels]; dt_softplus: the
+    step is softplus(dt + dt_bias); S0 fp32 [N,channels,d_state]; cu_seqlens int32 [N+1] for a
+    packed batch. Returns (o [B,T,channels], S_T fp32 [N,channels,d_state] or None)."""
+    N, num_seqs = _sequences(cu_seqlens, x.shape[0], x.device)
+    d = _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, num_seqs, 0)
+    dev, shape, f32 = x.device, tuple(x.shape), torch.float32
+    st_shape = (N, d.channels, d.d_state)
+    s0 = _whole("S0", S0, dev, f32, st_shape)
+    o = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
+    po = _whole("out", o, dev, x.dtype, shape)
+    S_T = None
+    if output_final_state:
+        S_T = torch.empty(st_shape, dtype=f32, device=dev) if final_state is None else final_state
+    ps = _whole("final_state", S_T, dev, f32, st_shape)
+    if workspace is None:
+        need = lib().gdn2_selective_scan_fwd_workspace_bytes(ctypes.byref(d))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _need_gpu("workspace", workspace, dev)
+    pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _call(dev, lib().gdn2_selective_scan_fwd, *_scan_ptrs(x, dt, A, B, C, D, gate, dt_bias), s0,
+          _ptr(cu_seqlens), po, ps, ctypes.byref(d), pw, nw)
+    return o, S_T
+
+
+def selective_scan_fwd_workspace_bytes(batch: int, seqlen: int, channels: int, d_state: int,
+                                       groups: int, dtype: torch.dtype, num_seqs: int = 0) -> int:
+    d = ScanDims(batch, seqlen, num_seqs, channels, d_state, groups, _dtype_code(dtype))
+    return int(lib().gdn2_selective_scan_fwd_workspace_bytes(ctypes.byref(d)))
+
+
+def selective_scan_step(x, dt, A, B, C, state, D: Optional[torch.Tensor] = None,
+                        gate: Optional[torch.Tensor] = None,
+                        dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False,
+                        state_idx: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """T tokens of each of N sequences (x [N,T,channels], the other inputs as in
+    selective_scan_fwd) against a pool of states [num_slots,channels,d_state], fp32 or bf16,
+    updated in place. state_idx int32 [N]: the slot of each sequence (None: slot n); an entry
+    outside the pool marks padding (zero o rows, no state touched). Returns o [N,T,channels]."""
+    d = _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, 0, 0)
+    dev, shape = x.device, tuple(x.shape)
+    if state.dim() != 3:
+        raise ValueError(f"state must be [num_slots,{d.channels},{d.d_state}]")
+    if state.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("state must be float32 or bfloat16")
+    slots = state.shape[0]
+    ps = _whole("state", state, dev, state.dtype, (slots, d.channels, d.d_state))
+    o = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
+    po = _whole("out", o, dev, x.dtype, shape)
+    _call(dev, lib().gdn2_selective_scan_step, *_scan_ptrs(x, dt, A, B, C, D, gate, dt_bias), ps,
+          0 if state.dtype == torch.float32 else 1, _state_idx(state_idx, shape[0], dev), slots,
+          po, ctypes.byref(d))
+    return o

@@ -29,7 +29,11 @@
  *                               callers that cannot allocate;
  *   - gdn2_short_conv_fwd, gdn2_short_conv_bwd, gdn2_short_conv_step
  *                               the short causal convolution before the recurrence, over
- *                               prompts, its gradients, and for single tokens.
+ *                               prompts, its gradients, and for single tokens;
+ *   - gdn2_selective_scan_fwd, gdn2_selective_scan_step
+ *                               the selective state space scan, the other linear recurrence
+ *                               of hybrid layers (a decay per channel and state), over
+ *                               prompts and for single tokens.
  * Calls added since version 9 of the ABI change none of its calls, so the number stays.
  *
  * Conventions (the pages are silent on these; this is the reading the library implements):
@@ -525,6 +529,66 @@ gdn2_status gdn2_short_conv_bwd(const void *x, const float *weight, const float 
 gdn2_status gdn2_short_conv_step(const void *x, const float *weight, const float *bias,
                                  float *conv_state, const int32_t *state_idx, int32_t num_slots,
                                  void *y, const gdn2_conv_dims *dims, void *stream);
+
+/*
+ * The selective state space scan. Where the delta rule keeps a matrix per head, it keeps
+ * d_state values per channel, each with a decay of its own that follows the token's step:
+ *     dt_t[d]   = softplus(dt[t][d] + dt_bias[d])         (or the sum alone)
+ *     h_t[d][n] = exp(dt_t[d] A[d][n]) h_{t-1}[d][n] + dt_t[d] B_t[g][n] x_t[d]
+ *     y_t[d]    = sum_n C_t[g][n] h_t[d][n] + D[d] x_t[d]
+ *     o_t[d]    = y_t[d] silu(gate_t[d])                  (without a gate: y_t)
+ * Channel d reads group g = d / (channels / groups) of B and C.
+ */
+typedef struct gdn2_scan_dims {
+    int32_t batch, seqlen, num_seqs;   /* as in gdn2_dims */
+    int32_t channels;                  /* >= 1 */
+    int32_t d_state;                   /* states per channel: 1 .. 128 */
+    int32_t groups;                    /* of B and C; channels is a multiple of it */
+    int32_t dtype;                     /* gdn2_dtype of x, dt, B, C, gate and o */
+    int32_t grad_dtype;                /* of the token gradients (backward only) */
+    int32_t dt_softplus;               /* nonzero: softplus of dt + dt_bias */
+    /* elements between tokens, or 0: */
+    int64_t x_stride, dt_stride, b_stride, c_stride, gate_stride;
+} gdn2_scan_dims;
+
+/*
+ * Bytes of device workspace gdn2_selective_scan_fwd needs for these dims (0 too where it needs
+ * none, and if the dims are invalid).
+ */
+size_t gdn2_selective_scan_fwd_workspace_bytes(const gdn2_scan_dims *dims);
+
+/*
+ *   x, dt, gate  device [B, T, channels];  gate may be NULL
+ *   A            device fp32 [channels][d_state], the rates (<= 0 for a stable state)
+ *   B, C         device [B, T, groups, d_state]
+ *   D, dt_bias   device fp32 [channels], each may be NULL (zero)
+ *   S0           device fp32 [N][channels][d_state] initial states, or NULL for zeros
+ *   cu_seqlens   device int32 [N+1] for a packed batch, or NULL
+ *   o            device [B, T, channels]
+ *   S_T          device fp32 [N][channels][d_state] final states, or NULL. Not S0's buffer.
+ *   workspace    at least gdn2_selective_scan_fwd_workspace_bytes() bytes, 256-byte aligned
+ */
+gdn2_status gdn2_selective_scan_fwd(const void *x, const void *dt, const float *A, const void *B,
+                                    const void *C, const float *D, const void *gate,
+                                    const float *dt_bias, const float *S0, const int32_t *cu_seqlens,
+                                    void *o, float *S_T, const gdn2_scan_dims *dims, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * The scan of T tokens (seqlen >= 1) of each of N sequences (batch >= 0) against a pool of
+ * states, as gdn2_recurrent_fwd runs the delta rule against its pool.
+ *   state        device [num_slots][channels][d_state] in state_dtype (gdn2_state_dtype), read
+ *                once and written once per call
+ *   state_idx    device int32 [N], the slot of each sequence, or NULL (slot n). An entry outside
+ *                [0, num_slots) marks a padding sequence: zero o rows, no state touched. The
+ *                valid entries must be distinct.
+ *   o            device [N, T, channels]
+ */
+gdn2_status gdn2_selective_scan_step(const void *x, const void *dt, const float *A, const void *B,
+                                     const void *C, const float *D, const void *gate,
+                                     const float *dt_bias, void *state, int32_t state_dtype,
+                                     const int32_t *state_idx, int32_t num_slots, void *o,
+                                     const gdn2_scan_dims *dims, void *stream);
 
 /*
  * Host helper: checks a HOST copy of cu_seqlens (N+1 entries) against total tokens T.

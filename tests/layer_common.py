@@ -98,3 +98,51 @@ def conv_ref(x, weight, bias, state0, lens, silu, dy=None, dstate_T=None):
             r["dstate0"][n], r["dstate0_b"][n] = d_seen[:W - 1], d_b[:W - 1]
             r["dx"][lo:hi], r["dx_b"][lo:hi] = d_seen[W - 1:], d_b[W - 1:]
     return r
+
+
+# ---- selective scan ----------------------------------------------------------------------
+
+
+def scan_ref(x, dt, A, B, C, D, gate, dt_bias, softplus, S0, lens, tile=128):
+    """x, dt, gate [T, ch]; B, C [T, G, M]; A [ch, M]; flat, in fp64. Returns o, S_T and their
+    bounds. The bounds follow the recurrence: `m` holds the magnitudes behind the state, `e` the
+    error of the state."""
+    T, ch = x.shape
+    G, M = B.shape[1:]
+    rep = ch // G
+    cu = offsets(lens)
+    raw = dt + (0.0 if dt_bias is None else dt_bias)
+    step = np.logaddexp(0.0, raw) if softplus else raw
+    # the sum dt + dt_bias, the rounded exponent of e^-|raw|, and a dozen operations of softplus
+    rel = U * ((3 * np.abs(raw) + 24) if softplus else 1.0)
+    r = {"o": np.zeros((T, ch)), "o_b": np.zeros((T, ch)),
+         "S_T": np.zeros((len(lens), ch, M)), "S_T_b": np.zeros((len(lens), ch, M))}
+    for n in range(len(lens)):
+        h = np.zeros((ch, M)) if S0 is None else S0[n].copy()
+        m, e = np.abs(h), np.zeros((ch, M))
+        for t in range(cu[n], cu[n + 1]):
+            z = step[t][:, None] * A
+            a = np.exp(z)
+            b = (step[t] * x[t])[:, None] * np.repeat(B[t], rep, 0)
+            er = (rel[t] if softplus else rel)
+            er = np.broadcast_to(er, (ch,))[:, None]
+            da = a * (np.abs(z) * (er + 3 * U) + 2 * U)
+            e = a * e + da * m + np.abs(b) * (er + 4 * U)
+            h, m = a * h + b, a * m + np.abs(b)
+            e += 2 * U * m
+            c = np.repeat(C[t], rep, 0)
+            # a tile's decay comes from its summed dt: an error of the sum's rounding, at most
+            # tile U of it, times z e^-z <= 0.4
+            et = e + 0.4 * tile * U * m
+            y = (c * h).sum(-1)
+            ye = (np.abs(c) * (et + (M + 3) * U * m)).sum(-1)
+            if D is not None:
+                y = y + D * x[t]
+                ye = ye + 2 * U * np.abs(D * x[t])
+            if gate is not None:
+                s = gate[t] * sigmoid(gate[t])
+                ye = np.abs(s) * ye + np.abs(y * s) * (np.abs(gate[t]) + 8) * 2 * U
+                y = y * s
+            r["o"][t], r["o_b"][t] = y, ye
+        r["S_T"][n], r["S_T_b"][n] = h, e + 0.4 * tile * U * m
+    return r

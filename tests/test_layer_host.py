@@ -6,7 +6,7 @@ import os
 import pytest
 
 import gated_delta_rule_gdn_amd as g
-from gated_delta_rule_gdn_amd.layer import ConvDims
+from gated_delta_rule_gdn_amd.layer import ConvDims, ScanDims
 
 
 def P(i):
@@ -92,3 +92,52 @@ def test_short_conv_step_refusals(L):
     assert conv_step(L, y=None) == NULL
     assert conv_step(L, width=9, batch=0) == UNSUPPORTED
     assert conv_step(L, batch=0) == 0                                # an empty batch
+
+
+SCAN = dict(batch=2, seqlen=300, num_seqs=0, channels=64, d_state=16, groups=2, dtype=1, grad_dtype=1,
+            dt_softplus=1, x_stride=0, dt_stride=0, b_stride=0, c_stride=0, gate_stride=0)
+
+
+def scan_fwd(L, cu=None, o=P(1), S0=None, S_T=None, ws=P(16), nbytes=1 << 30, x=P(1), null=False, **kw):
+    # o defaults to x's pointer: a call that passed every other check is still refused
+    return L.gdn2_selective_scan_fwd(x, P(2), P(3), P(4), P(5), None, None, None, S0, cu, o, S_T,
+                                     None if null else dims(ScanDims, SCAN, **kw), ws, nbytes, None)
+
+
+def test_selective_scan_forward_refusals(L):
+    assert scan_fwd(L, null=True) == NULL
+    assert scan_fwd(L, dtype=5) == UNSUPPORTED
+    assert scan_fwd(L, d_state=0) == SHAPE and scan_fwd(L, d_state=129) == UNSUPPORTED
+    assert scan_fwd(L, groups=0) == SHAPE and scan_fwd(L, groups=3) == SHAPE
+    assert scan_fwd(L, channels=0) == SHAPE
+    assert scan_fwd(L, batch=1 << 20, seqlen=1 << 12) == SHAPE
+    assert scan_fwd(L, b_stride=31) == SHAPE and scan_fwd(L, gate_stride=-1) == SHAPE
+    assert scan_fwd(L, cu=P(9)) == SHAPE
+    assert scan_fwd(L, x=None) == NULL and scan_fwd(L, o=None) == NULL
+    assert scan_fwd(L) == SHAPE and b"alias" in L.gdn2_last_error()
+    assert scan_fwd(L, o=P(6), S0=P(7), S_T=P(7)) == SHAPE
+    need = L.gdn2_selective_scan_fwd_workspace_bytes(dims(ScanDims, SCAN))
+    assert need > 0
+    assert scan_fwd(L, o=P(6), ws=None) == WORKSPACE
+    assert scan_fwd(L, o=P(6), nbytes=need - 1) == WORKSPACE
+    assert scan_fwd(L, o=P(6), ws=ctypes.c_void_p(0x10010)) == WORKSPACE
+    assert scan_fwd(L, seqlen=0, x=None, o=None) == 0
+    assert L.gdn2_selective_scan_fwd_workspace_bytes(dims(ScanDims, SCAN, groups=3)) == 0
+    # one sequence per tile, or one tile: no workspace
+    assert L.gdn2_selective_scan_fwd_workspace_bytes(dims(ScanDims, SCAN, batch=1024)) == 0
+    assert L.gdn2_selective_scan_fwd_workspace_bytes(dims(ScanDims, SCAN, batch=1, seqlen=9)) == 0
+
+
+def scan_step(L, o=P(1), st=P(6), sdt=0, slots=8, idx=None, **kw):
+    return L.gdn2_selective_scan_step(P(1), P(2), P(3), P(4), P(5), None, None, None, st, sdt, idx,
+                                      slots, o, dims(ScanDims, {**SCAN, "seqlen": 1}, **kw), None)
+
+
+def test_selective_scan_step_refusals(L):
+    assert scan_step(L) == SHAPE and scan_step(L, o=P(6)) == SHAPE
+    assert scan_step(L, o=P(7), sdt=2) == UNSUPPORTED
+    assert scan_step(L, o=P(7), seqlen=0) == SHAPE
+    assert scan_step(L, o=P(7), slots=1) == SHAPE
+    assert scan_step(L, o=P(7), st=None) == NULL
+    assert scan_step(L, batch=0, groups=5) == SHAPE
+    assert scan_step(L, batch=0) == 0
