@@ -188,6 +188,25 @@ struct ScanStepArgs {
 };
 hipError_t launch_scan_step(const ScanStepArgs &a, hipStream_t st);
 
+// The norms around a block (gdn2_block_norm_fwd, gdn2_block_norm_bwd).
+struct NormArgs {
+    const void *x, *gate, *residual;
+    const float *norm_weight, *scale, *next_weight;
+    void *h = nullptr, *y = nullptr;
+    const void *dh = nullptr, *dy = nullptr;
+    void *dx = nullptr, *dgate = nullptr, *dresidual = nullptr;
+    float *dnorm_weight = nullptr, *dscale = nullptr, *dnext_weight = nullptr;
+    float *partial = nullptr;        // [norm_parts()][3][d] sums of a backward call
+    int64_t rows, x_stride, gate_stride;
+    int d;
+    float eps;
+    bool bf16, residual_f32, grad_bf16 = false;
+};
+int norm_lanes(int d);                        // lanes that hold a row
+int64_t norm_sets(int64_t rows, int d);       // workgroups that hold all rows
+int64_t norm_parts(int64_t rows, int d);      // rows of the partial sums
+hipError_t launch_norm(const NormArgs &a, bool backward, hipStream_t st);
+
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t st);
 hipError_t launch_map_gates(const GateArgs &a, hipStream_t st);
 hipError_t launch_map_gates_bwd(const GateBwdArgs &a, hipStream_t st);

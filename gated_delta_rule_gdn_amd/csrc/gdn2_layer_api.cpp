@@ -165,6 +165,39 @@ gdn2_status check_workspace(const void *ws, size_t bytes, size_t need) {
     return GDN2_OK;
 }
 
+// ---- block norm --------------------------------------------------------------------------
+
+gdn2_status check_norm(const gdn2_norm_dims *d, bool backward) {
+    if (!d) return report(GDN2_ERR_NULL_ARG, "dims is NULL");
+    if (!dtype_ok(d->dtype)) return report(GDN2_ERR_UNSUPPORTED, "dtype must be GDN2_F32 or GDN2_BF16");
+    if (d->residual_dtype != GDN2_F32 && d->residual_dtype != d->dtype)
+        return report(GDN2_ERR_UNSUPPORTED, "residual_dtype must be GDN2_F32 or dtype");
+    if (backward && d->grad_dtype != GDN2_F32 && d->grad_dtype != d->dtype)
+        return report(GDN2_ERR_UNSUPPORTED, "grad_dtype must be GDN2_F32 or dtype");
+    if (d->d < 1) return report(GDN2_ERR_BAD_SHAPE, "d must be >= 1");
+    if (d->d > 16384) return report(GDN2_ERR_UNSUPPORTED, "d must be 1 .. 16384");
+    if (d->rows < 0 || d->rows > INT32_MAX) return report(GDN2_ERR_BAD_SHAPE, "rows must be 0 .. 2^31-1");
+    if (!(d->eps >= 0.f && d->eps <= 1e30f)) return report(GDN2_ERR_BAD_SHAPE, "eps must be finite and >= 0");
+    int64_t s;
+    if (!take_stride(d->x_stride, d->d, d->rows, &s) || !take_stride(d->gate_stride, d->d, d->rows, &s))
+        return report(GDN2_ERR_BAD_SHAPE, "a stride is smaller than d or a tensor too large");
+    return GDN2_OK;
+}
+
+gdn2::NormArgs norm_args(const gdn2_norm_dims *d, const void *x, const void *gate, const void *residual,
+                         const float *norm_weight, const float *scale, const float *next_weight) {
+    gdn2::NormArgs a;
+    a.x = x; a.gate = gate; a.residual = residual;
+    a.norm_weight = norm_weight; a.scale = scale; a.next_weight = next_weight;
+    a.rows = d->rows; a.d = d->d; a.eps = d->eps;
+    a.x_stride = d->x_stride ? d->x_stride : d->d;
+    a.gate_stride = d->gate_stride ? d->gate_stride : d->d;
+    a.bf16 = d->dtype == GDN2_BF16;
+    a.residual_f32 = a.bf16 && d->residual_dtype == GDN2_F32;
+    a.grad_bf16 = d->grad_dtype == GDN2_BF16;
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -318,6 +351,60 @@ gdn2_status gdn2_selective_scan_step(const void *x, const void *dt, const float 
     a.num_seqs = d.batch; a.ntok = d.seqlen; a.num_slots = num_slots;
     a.state_bf16 = state_dtype == GDN2_STATE_BF16;
     return done(gdn2::launch_scan_step(a, static_cast<hipStream_t>(stream)), "gdn2_selective_scan_step launch");
+}
+
+gdn2_status gdn2_block_norm_fwd(const void *x, const void *gate, const void *residual,
+                                const float *norm_weight, const float *scale,
+                                const float *next_weight, void *h, void *y,
+                                const gdn2_norm_dims *dims, void *stream) {
+    gdn2_status st = check_norm(dims, false);
+    if (st != GDN2_OK) return st;
+    if (dims->rows == 0) return ok();
+    if (!x || !h) return report(GDN2_ERR_NULL_ARG, "x and h are required");
+    if (next_weight && !y) return report(GDN2_ERR_NULL_ARG, "next_weight needs y");
+    // h may be the residual's own buffer: every value is read before its place is written
+    const void *outs[] = {h, next_weight ? y : nullptr}, *ins[] = {x, gate, norm_weight, scale, next_weight};
+    if (aliases(outs, ins) || (outs[1] && y == residual))
+        return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input or the other output");
+    gdn2::NormArgs a = norm_args(dims, x, gate, residual, norm_weight, scale, next_weight);
+    a.h = h; a.y = y;
+    return done(gdn2::launch_norm(a, false, static_cast<hipStream_t>(stream)), "gdn2_block_norm_fwd launch");
+}
+
+size_t gdn2_block_norm_bwd_workspace_bytes(const gdn2_norm_dims *dims) {
+    if (check_norm(dims, true) != GDN2_OK) return 0;
+    return static_cast<size_t>(gdn2::norm_parts(dims->rows, dims->d)) * 3 * dims->d * sizeof(float);
+}
+
+gdn2_status gdn2_block_norm_bwd(const void *x, const void *gate, const void *residual,
+                                const float *norm_weight, const float *scale,
+                                const float *next_weight, const void *dh, const void *dy, void *dx,
+                                void *dgate, void *dresidual, float *dnorm_weight, float *dscale,
+                                float *dnext_weight, const gdn2_norm_dims *dims, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    gdn2_status st = check_norm(dims, true);
+    if (st != GDN2_OK) return st;
+    const bool rows = dims->rows > 0;
+    if (rows && (!x || !dx)) return report(GDN2_ERR_NULL_ARG, "x and dx are required");
+    if (rows && next_weight && !dy) return report(GDN2_ERR_NULL_ARG, "next_weight needs dy");
+    if (rows && !dh && !next_weight) return report(GDN2_ERR_NULL_ARG, "without next_weight, dh is required");
+    if (rows && ((gate && !dgate) || (residual && !dresidual)))
+        return report(GDN2_ERR_NULL_ARG, "a gate needs dgate and a residual dresidual");
+    if ((norm_weight && !dnorm_weight) || (scale && !dscale) || (next_weight && !dnext_weight))
+        return report(GDN2_ERR_NULL_ARG, "every weight and scale needs its gradient");
+    const void *outs[] = {dx, dgate, dresidual, dnorm_weight, dscale, dnext_weight};
+    const void *ins[] = {x, gate, residual, norm_weight, scale, next_weight, dh, dy, workspace};
+    if (aliases(outs, ins)) return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input, the workspace or another output");
+    const bool params = norm_weight || scale || next_weight;
+    st = check_workspace(workspace, workspace_bytes,
+                         params ? static_cast<size_t>(gdn2::norm_parts(dims->rows, dims->d)) * 3 * dims->d * sizeof(float) : 0);
+    if (st != GDN2_OK) return st;
+    if (!rows && !params) return ok();
+    gdn2::NormArgs a = norm_args(dims, x, gate, residual, norm_weight, scale, next_weight);
+    a.dh = dh; a.dy = dy; a.dx = dx; a.dgate = dgate; a.dresidual = residual ? dresidual : nullptr;
+    a.dnorm_weight = dnorm_weight; a.dscale = dscale; a.dnext_weight = dnext_weight;
+    a.partial = static_cast<float *>(workspace);
+    return done(gdn2::launch_norm(a, true, static_cast<hipStream_t>(stream)), "gdn2_block_norm_bwd launch");
 }
 
 }  // extern "C"

@@ -1,11 +1,14 @@
 """The operators around the recurrence, bound to libgdn2.so: the short causal convolution and
-the selective state space scan, over prompts, their gradients, and for single tokens.
+the selective state space scan, over prompts, their gradients, and for single tokens, and the
+norms around a block.
 
     y, state_T = short_conv_fwd(x, weight, bias=None, state0=None, cu_seqlens=None, silu=False)
     grads      = short_conv_bwd(x, weight, dy, ...)
     y          = short_conv_step(x, weight, conv_state, ...)        # conv_state updated in place
     o, S_T     = selective_scan_fwd(x, dt, A, B, C, D=None, gate=None, ...)
     o          = selective_scan_step(x, dt, A, B, C, state, ...)    # state updated in place
+    h, y       = block_norm_fwd(x, norm_weight, gate, residual, scale, next_weight)
+    grads      = block_norm_bwd(x, dh, dy, ...)
 
 As in the rest of the package, these functions check shapes, allocate outputs and workspaces
 and call the C ABI (``include/gdn2.h``) on the current HIP stream of the tensors' device. Token
@@ -39,9 +42,14 @@ class ScanDims(ctypes.Structure):
                 ("b_stride", _i64), ("c_stride", _i64), ("gate_stride", _i64)]
 
 
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("d", _i32), ("dtype", _i32), ("residual_dtype", _i32),
+                ("grad_dtype", _i32), ("eps", _f32), ("x_stride", _i64), ("gate_stride", _i64)]
+
+
 def declare(L: ctypes.CDLL) -> None:
     """Argument types of this module's calls (lib() runs it once)."""
-    cd, sd = ctypes.POINTER(ConvDims), ctypes.POINTER(ScanDims)
+    cd, sd, nd = (ctypes.POINTER(t) for t in (ConvDims, ScanDims, NormDims))
     for name, restype, argtypes in (
             ("gdn2_short_conv_fwd", _i32, [_vp] * 7 + [cd, _vp]),
             ("gdn2_short_conv_bwd_workspace_bytes", _sz, [cd]),
@@ -50,7 +58,10 @@ def declare(L: ctypes.CDLL) -> None:
             ("gdn2_selective_scan_fwd_workspace_bytes", _sz, [sd]),
             ("gdn2_selective_scan_fwd", _i32, [_vp] * 12 + [sd, _vp, _sz, _vp]),
             ("gdn2_selective_scan_step", _i32,
-             [_vp] * 9 + [_i32, _vp, _i32, _vp, sd, _vp])):
+             [_vp] * 9 + [_i32, _vp, _i32, _vp, sd, _vp]),
+            ("gdn2_block_norm_fwd", _i32, [_vp] * 8 + [nd, _vp]),
+            ("gdn2_block_norm_bwd_workspace_bytes", _sz, [nd]),
+            ("gdn2_block_norm_bwd", _i32, [_vp] * 14 + [nd, _vp, _sz, _vp])):
         f = getattr(L, name)
         f.restype, f.argtypes = restype, argtypes
 
@@ -348,3 +359,124 @@ def selective_scan_step(x, dt, A, B, C, state, D: Optional[torch.Tensor] = None,
           0 if state.dtype == torch.float32 else 1, _state_idx(state_idx, shape[0], dev), slots,
           po, ctypes.byref(d))
     return o
+
+
+# ---- block norm --------------------------------------------------------------------------
+
+
+def _rows(name: str, t: torch.Tensor, dev, dtype, shape) -> int:
+    """Checks an input of rows that may be a column slice. Returns the elements between rows."""
+    _on_gpu(name, t, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    d = shape[-1]
+    if t.is_contiguous():
+        return d
+    if d > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: every row's values must be contiguous")
+    step, rows = None, 1
+    for i in range(t.dim() - 2, -1, -1):
+        if t.shape[i] == 1:
+            continue
+        if step is None:
+            step = t.stride(i)
+        elif t.stride(i) != rows * step:
+            raise ValueError(f"{name}: the rows must follow each other at one stride")
+        rows *= t.shape[i]
+    step = d if step is None else step
+    if step < d:
+        raise ValueError(f"{name}: rows overlap (stride {step}, {d} values)")
+    return step
+
+
+def _norm_dims(x, gate, residual, norm_weight, scale, next_weight, eps, grad_code) -> NormDims:
+    """The checked dims of a block norm call."""
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    if x.dim() < 1:
+        raise ValueError("x must be [*rows,d]")
+    d = shape[-1]
+    code = _dtype_code(dtype)
+    xs = _rows("x", x, dev, dtype, shape)
+    gs = 0 if gate is None else _rows("gate", gate, dev, dtype, shape)
+    rcode = code
+    if residual is not None:
+        rcode = _dtype_code(residual.dtype)
+        if residual.dtype not in (dtype, torch.float32):
+            raise TypeError(f"residual has dtype {residual.dtype}, expected {dtype} or torch.float32")
+        _whole("residual", residual, dev, residual.dtype, tuple(shape))
+    for name, t in (("norm_weight", norm_weight), ("scale", scale), ("next_weight", next_weight)):
+        _whole(name, t, dev, torch.float32, (d,))
+    rows = x.numel() // d if d else 0
+    return NormDims(rows, d, code, rcode, grad_code, eps, xs, gs)
+
+
+def block_norm_fwd(x, norm_weight: Optional[torch.Tensor] = None,
+                   gate: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                   scale: Optional[torch.Tensor] = None,
+                   next_weight: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   out: Optional[torch.Tensor] = None, next_out: Optional[torch.Tensor] = None
+                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The norms after and before a block, with its gate, residual and scale:
+        h = residual + scale (rms(x) norm_weight silu(gate)),   y = rms(h) next_weight
+    where every stage but h is taken only if its argument is given. x, gate [*rows,d] (each may
+    be a column slice); residual [*rows,d] in x's dtype or fp32; norm_weight, scale, next_weight
+    fp32 [d]. Returns (h in residual's dtype, y in x's dtype or None). out may be residual."""
+    d = _norm_dims(x, gate, residual, norm_weight, scale, next_weight, eps, 0)
+    dev, shape = x.device, tuple(x.shape)
+    ht = x.dtype if residual is None else residual.dtype
+    h = torch.empty(shape, dtype=ht, device=dev) if out is None else out
+    ph = _whole("out", h, dev, ht, shape)
+    y = None
+    if next_weight is not None:
+        y = torch.empty(shape, dtype=x.dtype, device=dev) if next_out is None else next_out
+    py = _whole("next_out", y, dev, x.dtype, shape)
+    _call(dev, lib().gdn2_block_norm_fwd, x.data_ptr(), _ptr(gate), _ptr(residual),
+          _ptr(norm_weight), _ptr(scale), _ptr(next_weight), ph, py, ctypes.byref(d))
+    return h, y
+
+
+def block_norm_bwd(x, dh: Optional[torch.Tensor] = None, dy: Optional[torch.Tensor] = None,
+                   norm_weight: Optional[torch.Tensor] = None,
+                   gate: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                   scale: Optional[torch.Tensor] = None,
+                   next_weight: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                   grad_dtype: Optional[torch.dtype] = None,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of block_norm_fwd given dh = dL/dh (None: zero, with next_weight only) and dy =
+    dL/dy (with next_weight). grad_dtype, the type of the token gradients in and out, is x's or
+    fp32 (None: dy's, else dh's, else x's); dh and dresidual have it too, and are fp32 with an
+    fp32 residual. Returns dx, and dgate, dresidual, dnorm_weight,
+    dscale, dnext_weight for the arguments given."""
+    if (dy is None) != (next_weight is None):
+        raise ValueError("dy and next_weight go together")
+    if dh is None and dy is None:
+        raise ValueError("without next_weight, dh is required")
+    dev, shape = x.device, tuple(x.shape)
+    wide = residual is not None and residual.dtype == torch.float32 and x.dtype != torch.float32
+    gt = grad_dtype
+    if gt is None:      # with an fp32 residual dh says nothing about the other gradients' type
+        gt = dy.dtype if dy is not None else x.dtype if wide else dh.dtype
+    if gt not in (x.dtype, torch.float32):
+        raise TypeError(f"gradients have dtype {gt}, expected {x.dtype} or torch.float32")
+    d = _norm_dims(x, gate, residual, norm_weight, scale, next_weight, eps, _dtype_code(gt))
+    ht = torch.float32 if wide else gt
+    pdh = _whole("dh", dh, dev, ht, shape)
+    pdy = _whole("dy", dy, dev, gt, shape)
+    new = lambda like, dtype: None if like is None else torch.empty(  # noqa: E731
+        like.shape, dtype=dtype, device=dev)
+    f32 = torch.float32
+    out = {"dx": new(x, gt), "dgate": new(gate, gt), "dresidual": new(residual, ht),
+           "dnorm_weight": new(norm_weight, f32), "dscale": new(scale, f32),
+           "dnext_weight": new(next_weight, f32)}
+    ws = _workspace(workspace, lib().gdn2_block_norm_bwd_workspace_bytes(ctypes.byref(d)), dev)
+    _call(dev, lib().gdn2_block_norm_bwd, x.data_ptr(), _ptr(gate), _ptr(residual),
+          _ptr(norm_weight), _ptr(scale), _ptr(next_weight), pdh, pdy,
+          *(_ptr(t) for t in out.values()), ctypes.byref(d), ws.data_ptr(), ws.numel())
+    return {n: t for n, t in out.items() if t is not None}
+
+
+def block_norm_bwd_workspace_bytes(rows: int, d: int) -> int:
+    n = NormDims(rows, d, 0, 0, 0, 0.0, 0, 0)
+    return int(lib().gdn2_block_norm_bwd_workspace_bytes(ctypes.byref(n)))

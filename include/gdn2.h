@@ -33,7 +33,10 @@
  *   - gdn2_selective_scan_fwd, gdn2_selective_scan_step
  *                               the selective state space scan, the other linear recurrence
  *                               of hybrid layers (a decay per channel and state), over
- *                               prompts and for single tokens.
+ *                               prompts and for single tokens;
+ *   - gdn2_block_norm_fwd, gdn2_block_norm_bwd
+ *                               the norms after and before a block, fused with its gate, the
+ *                               residual and its scale, and their gradients.
  * Calls added since version 9 of the ABI change none of its calls, so the number stays.
  *
  * Conventions (the pages are silent on these; this is the reading the library implements):
@@ -589,6 +592,58 @@ gdn2_status gdn2_selective_scan_step(const void *x, const void *dt, const float 
                                      const float *dt_bias, void *state, int32_t state_dtype,
                                      const int32_t *state_idx, int32_t num_slots, void *o,
                                      const gdn2_scan_dims *dims, void *stream);
+
+/*
+ * The norms after and before a block, fused with the block's gate, the residual and its scale.
+ * Per row, rms(v) = v / sqrt(mean(v^2) + eps), and each stage but the last only where its
+ * argument is given:
+ *     p = rms(x) norm_weight,  u = p silu(gate),  h = residual + scale u,  y = rms(h) next_weight
+ * With norm_weight and gate alone this is the gated output norm that gdn2_fusion.gate fuses
+ * into the recurrence (x its o, one row per token and value head), with gradients; with all of
+ * them it is the whole boundary between two blocks. Both norms are taken of fp32 values (y of h
+ * before it is rounded to its type).
+ */
+typedef struct gdn2_norm_dims {
+    int64_t rows;                      /* 0 .. 2^31-1 */
+    int32_t d;                         /* columns: 1 .. 16384 */
+    int32_t dtype;                     /* gdn2_dtype of x, gate and y */
+    int32_t residual_dtype;            /* of residual and h: GDN2_F32 or dtype */
+    int32_t grad_dtype;                /* of dy, dx, dgate (backward only). dh and dresidual have
+                                          it too, and GDN2_F32 with a GDN2_F32 residual */
+    float eps;                         /* >= 0 */
+    int64_t x_stride, gate_stride;     /* elements between rows, >= d, or 0 */
+} gdn2_norm_dims;
+
+/*
+ *   x, gate, residual                 device [rows, d];  gate and residual may be NULL
+ *   norm_weight, scale, next_weight   device fp32 [d], each may be NULL
+ *   h            device [rows, d]; may be residual's own buffer
+ *   y            device [rows, d], written (and required) with next_weight only
+ */
+gdn2_status gdn2_block_norm_fwd(const void *x, const void *gate, const void *residual,
+                                const float *norm_weight, const float *scale,
+                                const float *next_weight, void *h, void *y,
+                                const gdn2_norm_dims *dims, void *stream);
+
+/* Bytes of device workspace gdn2_block_norm_bwd needs, or 0 if the dims are invalid. */
+size_t gdn2_block_norm_bwd_workspace_bytes(const gdn2_norm_dims *dims);
+
+/*
+ * Gradients of gdn2_block_norm_fwd, which is formed again from its inputs.
+ *   x .. next_weight    the forward's inputs
+ *   dh           device [rows, d]: dL/dh, or NULL for zero (with next_weight only)
+ *   dy           device [rows, d]: dL/dy, required with next_weight
+ *   dx, dgate, dresidual              device [rows, d], the last two for a gate, a residual
+ *   dnorm_weight, dscale, dnext_weight   device fp32 [d], each required with its input
+ *   workspace    at least gdn2_block_norm_bwd_workspace_bytes() bytes, 256-byte aligned; not
+ *                needed without norm_weight, scale and next_weight
+ */
+gdn2_status gdn2_block_norm_bwd(const void *x, const void *gate, const void *residual,
+                                const float *norm_weight, const float *scale,
+                                const float *next_weight, const void *dh, const void *dy, void *dx,
+                                void *dgate, void *dresidual, float *dnorm_weight, float *dscale,
+                                float *dnext_weight, const gdn2_norm_dims *dims, void *workspace,
+                                size_t workspace_bytes, void *stream);
 
 /*
  * Host helper: checks a HOST copy of cu_seqlens (N+1 entries) against total tokens T.

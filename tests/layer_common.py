@@ -146,3 +146,73 @@ def scan_ref(x, dt, A, B, C, D, gate, dt_bias, softplus, S0, lens, tile=128):
             r["o"][t], r["o_b"][t] = y, ye
         r["S_T"][n], r["S_T_b"][n] = h, e + 0.4 * tile * U * m
     return r
+
+
+# ---- block norm --------------------------------------------------------------------------
+
+
+def norm_ref(x, nw, gate, res, scale, nxt, eps, dh=None, dy=None):
+    """Rows in fp64. Returns h, y and, with dh or dy, the gradients, each with its bound. Errors
+    of row statistics are relative: a sum of d squares over 8 or 16 values and up to ten
+    exchanges, a division, rsqrt and a product come to at most 32 U of rstd."""
+    R = 32 * U
+    rows, d = x.shape
+    rx = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    p = x if nw is None else x * rx * nw
+    pe = 0.0 if nw is None else np.abs(p) * R
+    if gate is not None:
+        s = sigmoid(gate)
+        sl, se = gate * s, (np.abs(gate) + 8) * 2 * U * np.abs(gate * s)
+        u, ue = p * sl, np.abs(sl) * pe + np.abs(p) * se + U * np.abs(p * sl)
+    else:
+        u, ue = p, pe
+    sc = 1.0 if scale is None else scale
+    r0 = 0.0 if res is None else res
+    h = r0 + sc * u
+    he = np.abs(sc) * ue + 2 * U * (np.abs(sc * u) + np.abs(r0))
+    rh = 1 / np.sqrt((h * h).mean(-1, keepdims=True) + eps)
+    # rstd(h) moves by rh^2 |h| he / |h| at most, relative
+    rhe = R + rh * rh * (np.abs(h) * he).mean(-1, keepdims=True)
+    out = {"h": h, "h_b": he + 0 * h}
+    if nxt is not None:
+        out["y"] = h * rh * nxt
+        out["y_b"] = np.abs(rh * nxt) * he + np.abs(out["y"]) * (rhe + 2 * U)
+    if dh is None and dy is None:
+        return out
+    g = np.zeros_like(x) if dh is None else dh.copy()
+    ge = np.zeros_like(x)
+    # sums over rows: a workgroup's rows in a lane, then its partial sums in 16 waves
+    grow = (rows / 512 + rows / 16 + 24) * U
+    col = lambda v, e: (v.sum(0), (e + grow * np.abs(v)).sum(0))  # noqa: E731
+    if nxt is not None:
+        v = dy * h * rh
+        out["dnext_weight"], out["dnext_weight_b"] = col(v, np.abs(v) * (rhe + 2 * U) + np.abs(dy * rh) * he)
+        w = dy * nxt
+        m = rh * rh * (w * h).mean(-1, keepdims=True)
+        me = rh * rh * (np.abs(w) * (he + 32 * U * np.abs(h))).mean(-1, keepdims=True) + 2 * rhe * np.abs(m)
+        inner = w - h * m
+        g = g + rh * inner
+        ge = rh * (np.abs(h) * me + he * np.abs(m) + 3 * U * (np.abs(w) + np.abs(h * m))) \
+            + np.abs(rh * inner) * rhe + 2 * U * (np.abs(g) + np.abs(rh * inner))
+    if res is not None:
+        out["dresidual"], out["dresidual_b"] = g, ge
+    if scale is not None:
+        v = g * u
+        out["dscale"], out["dscale_b"] = col(v, np.abs(u) * ge + np.abs(g) * ue + U * np.abs(v))
+        g, ge = g * scale, np.abs(scale) * ge + U * np.abs(g * scale)
+    if gate is not None:
+        slope = s * (1 + gate * (1 - s))
+        out["dgate"] = g * p * slope
+        out["dgate_b"] = np.abs(p * slope) * ge + np.abs(g * slope) * pe + np.abs(g * p) * slope_err(gate, 0.0) \
+            + 3 * U * np.abs(out["dgate"])
+        g, ge = g * sl, np.abs(sl) * ge + np.abs(g) * se + U * np.abs(g * sl)
+    if nw is not None:
+        v = g * x * rx
+        out["dnorm_weight"], out["dnorm_weight_b"] = col(v, np.abs(x * rx) * ge + np.abs(v) * (R + 2 * U))
+        w, we = g * nw, np.abs(nw) * ge + U * np.abs(g * nw)
+        m = rx * rx * (w * x).mean(-1, keepdims=True)
+        me = rx * rx * (np.abs(x) * (we + 32 * U * np.abs(w))).mean(-1, keepdims=True) + 2 * R * np.abs(m)
+        g = rx * (w - x * m)
+        ge = rx * (we + np.abs(x) * me + 3 * U * (np.abs(w) + np.abs(x * m))) + np.abs(g) * R
+    out["dx"], out["dx_b"] = g, ge
+    return out

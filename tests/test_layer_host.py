@@ -6,7 +6,7 @@ import os
 import pytest
 
 import gated_delta_rule_gdn_amd as g
-from gated_delta_rule_gdn_amd.layer import ConvDims, ScanDims
+from gated_delta_rule_gdn_amd.layer import ConvDims, NormDims, ScanDims
 
 
 def P(i):
@@ -141,3 +141,46 @@ def test_selective_scan_step_refusals(L):
     assert scan_step(L, o=P(7), st=None) == NULL
     assert scan_step(L, batch=0, groups=5) == SHAPE
     assert scan_step(L, batch=0) == 0
+
+
+NORM = dict(rows=10, d=64, dtype=1, residual_dtype=1, grad_dtype=1, eps=1e-5, x_stride=0, gate_stride=0)
+
+
+def norm_fwd(L, x=P(1), h=P(1), res=None, nxt=None, y=None, **kw):
+    # h defaults to x's pointer: a call that passed every other check is still refused
+    return L.gdn2_block_norm_fwd(x, None, res, None, None, nxt, h, y, dims(NormDims, NORM, **kw), None)
+
+
+def test_block_norm_forward_refusals(L):
+    assert L.gdn2_block_norm_fwd(*[P(1)] * 8, None, None) == NULL
+    assert norm_fwd(L, dtype=3) == UNSUPPORTED
+    assert norm_fwd(L, dtype=0) == UNSUPPORTED                       # fp32 x, bf16 residual
+    assert norm_fwd(L, residual_dtype=2) == UNSUPPORTED
+    assert norm_fwd(L, d=0) == SHAPE and norm_fwd(L, d=16385) == UNSUPPORTED
+    assert norm_fwd(L, rows=-1) == SHAPE and norm_fwd(L, rows=1 << 31) == SHAPE
+    assert norm_fwd(L, eps=-1.0) == SHAPE and norm_fwd(L, eps=float("nan")) == SHAPE
+    assert norm_fwd(L, x_stride=63) == SHAPE and norm_fwd(L, gate_stride=-1) == SHAPE
+    assert norm_fwd(L, x=None) == NULL and norm_fwd(L, h=None) == NULL
+    assert norm_fwd(L, h=P(2), nxt=P(3)) == NULL                     # y is missing
+    assert norm_fwd(L) == SHAPE
+    assert norm_fwd(L, h=P(2), res=P(4), nxt=P(3), y=P(4)) == SHAPE  # y over the residual
+    assert norm_fwd(L, rows=0) == 0
+
+
+def norm_bwd(L, dx=P(1), dh=P(9), nw=P(2), dnw=P(3), nxt=None, dy=None, gate=None, ws=P(16), nbytes=1 << 30, **kw):
+    return L.gdn2_block_norm_bwd(P(1), gate, None, nw, None, nxt, dh, dy, dx, None, None, dnw, None, None,
+                                 dims(NormDims, NORM, **kw), ws, nbytes, None)
+
+
+def test_block_norm_backward_refusals(L):
+    need = L.gdn2_block_norm_bwd_workspace_bytes(dims(NormDims, NORM))
+    assert need > 0 and L.gdn2_block_norm_bwd_workspace_bytes(dims(NormDims, NORM, d=0)) == 0
+    assert norm_bwd(L, grad_dtype=2) == UNSUPPORTED
+    assert norm_bwd(L) == SHAPE                                      # dx aliases x
+    assert norm_bwd(L, dx=None) == NULL and norm_bwd(L, dx=P(8), dh=None) == NULL
+    assert norm_bwd(L, dx=P(8), nxt=P(5)) == NULL                    # dy is missing
+    assert norm_bwd(L, dx=P(8), gate=P(5)) == NULL                   # dgate is missing
+    assert norm_bwd(L, dx=P(8), dnw=None) == NULL
+    assert norm_bwd(L, dx=P(8), ws=None) == WORKSPACE
+    assert norm_bwd(L, dx=P(8), nbytes=need - 1) == WORKSPACE
+    assert norm_bwd(L, dx=P(8), ws=ctypes.c_void_p(0x10040)) == WORKSPACE
