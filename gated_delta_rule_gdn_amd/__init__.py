@@ -627,6 +627,7 @@ def abi_version() -> int:
 
 from . import layer  # noqa: E402  (it uses the helpers above)
 from .layer import (block_norm_bwd, block_norm_bwd_workspace_bytes, block_norm_fwd,  # noqa: E402,F401
+                    selective_scan_bwd, selective_scan_bwd_workspace_bytes,
                     selective_scan_fwd, selective_scan_fwd_workspace_bytes,
                     selective_scan_step, short_conv_bwd, short_conv_bwd_workspace_bytes,
                     short_conv_fwd, short_conv_step)

@@ -167,13 +167,25 @@ struct ScanArgs {
     float *tiles_h = nullptr;        // [tiles][d_state][channels]: states reached, then entering
     float *tiles_dt = nullptr;       // [tiles][channels]: sums of dt
     int32_t *tiles_pass = nullptr;   // [tiles]: whether one sequence passes through the whole tile
+    // the backward: gradients in and out, and its own workspace
+    const void *dO = nullptr;
+    const float *dS_T = nullptr;
+    void *dx = nullptr, *ddt = nullptr, *dB = nullptr, *dC = nullptr, *dgate = nullptr;
+    float *dA = nullptr, *dD = nullptr, *ddt_bias = nullptr, *dS0 = nullptr;
+    bool grad_bf16 = false;
+    float *tiles_g = nullptr;        // as tiles_h, of the states' gradients from the back
+    float *tiles_db = nullptr;       // [tiles][channels]: sums for ddt_bias
+    float *part_bc = nullptr;        // [workgroups across channels][tokens][2][d_state]
 };
+constexpr int kScanMaxBwdTile = 32;  // tokens of a tile of the backward, which LDS holds whole
 int scan_parts(int d_state);                              // lanes that share a channel's states
 int scan_blocks(int channels, int groups, int parts);     // workgroups across the channels
 int scan_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed);
 int scan_tiles(int total, int tile);
 bool scan_chained(int batch, int seqlen, bool packed, int tile);
+int scan_bwd_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed);
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st);
+hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st);
 
 // The selective scan of single tokens (gdn2_selective_scan_step).
 struct ScanStepArgs {

@@ -140,20 +140,25 @@ void scan_inputs(Args *a, const gdn2_scan_dims *d, const void *x, const void *dt
 constexpr size_t kAlign = 256;
 size_t padded(size_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
-// Sizes of the forward's workspace: the tiles' states, sums of dt and pass flags.
+// Sizes of the workspace: the tiles' states, sums and pass flags; backward also the states'
+// gradients, a second array of sums, and the workgroups' shares of dB and dC.
 struct ScanPlan {
     int tile, tiles;
     bool chained;
-    size_t states, sums, flags;
-    ScanPlan(const gdn2_scan_dims *d, bool packed) {
-        tile = gdn2::scan_tile(d->channels, d->groups, d->d_state, d->batch, d->seqlen, packed);
+    size_t states, sums, flags, shares;
+    ScanPlan(const gdn2_scan_dims *d, bool packed, bool backward = false) {
+        tile = backward ? gdn2::scan_bwd_tile(d->channels, d->groups, d->d_state, d->batch, d->seqlen, packed)
+                        : gdn2::scan_tile(d->channels, d->groups, d->d_state, d->batch, d->seqlen, packed);
         tiles = gdn2::scan_tiles(d->batch * d->seqlen, tile);
         chained = gdn2::scan_chained(d->batch, d->seqlen, packed, tile);
         states = padded(static_cast<size_t>(tiles) * d->d_state * d->channels * sizeof(float));
         sums = padded(static_cast<size_t>(tiles) * d->channels * sizeof(float));
         flags = padded(static_cast<size_t>(tiles) * sizeof(int32_t));
+        shares = padded(static_cast<size_t>(gdn2::scan_blocks(d->channels, d->groups, gdn2::scan_parts(d->d_state))) *
+                        d->batch * d->seqlen * 2 * d->d_state * sizeof(float));
     }
     size_t fwd_bytes() const { return chained ? states + sums + flags : 0; }
+    size_t bwd_bytes() const { return 2 * states + 2 * sums + flags + shares; }
 };
 
 gdn2_status check_workspace(const void *ws, size_t bytes, size_t need) {
@@ -320,6 +325,54 @@ gdn2_status gdn2_selective_scan_fwd(const void *x, const void *dt, const float *
         a.tiles_pass = reinterpret_cast<int32_t *>(w + p.states + p.sums);
     }
     return done(gdn2::launch_scan_fwd(a, static_cast<hipStream_t>(stream)), "gdn2_selective_scan_fwd launch");
+}
+
+size_t gdn2_selective_scan_bwd_workspace_bytes(const gdn2_scan_dims *dims) {
+    if (!dims) return 0;
+    const bool packed = dims->num_seqs > 0 && dims->batch == 1;
+    if (check_scan(dims, packed, true) != GDN2_OK) return 0;
+    const size_t dense = ScanPlan(dims, false, true).bwd_bytes();
+    const size_t pk = packed ? ScanPlan(dims, true, true).bwd_bytes() : 0;
+    return dense > pk ? dense : pk;
+}
+
+gdn2_status gdn2_selective_scan_bwd(const void *x, const void *dt, const float *A, const void *B,
+                                    const void *C, const float *D, const void *gate,
+                                    const float *dt_bias, const float *S0, const int32_t *cu_seqlens,
+                                    const void *dO, const float *dS_T, void *dx, void *ddt, float *dA,
+                                    void *dB, void *dC, float *dD, void *dgate, float *ddt_bias,
+                                    float *dS0, const gdn2_scan_dims *dims, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+    const bool packed = cu_seqlens != nullptr;
+    gdn2_status st = check_scan(dims, packed, true);
+    if (st != GDN2_OK) return st;
+    const bool tokens = dims->batch > 0 && dims->seqlen > 0;
+    if (!A || !dA || (tokens && (!x || !dt || !B || !C || !dO || !dx || !ddt || !dB || !dC)))
+        return report(GDN2_ERR_NULL_ARG, "the inputs, dO, dx, ddt, dA, dB and dC are required");
+    if ((D && !dD) || (dt_bias && !ddt_bias) || (tokens && gate && !dgate))
+        return report(GDN2_ERR_NULL_ARG, "D, dt_bias and a gate need their gradients");
+    const void *outs[] = {dx, ddt, dA, dB, dC, dD, dgate, ddt_bias, dS0};
+    const void *ins[] = {x, dt, A, B, C, D, gate, dt_bias, S0, cu_seqlens, dO, dS_T, workspace};
+    if (aliases(outs, ins)) return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input, the workspace or another output");
+    const ScanPlan p(dims, packed, true);
+    st = check_workspace(workspace, workspace_bytes, p.bwd_bytes());
+    if (st != GDN2_OK) return st;
+    gdn2::ScanArgs a;
+    scan_inputs(&a, dims, x, dt, A, B, C, D, gate, dt_bias);
+    a.S0 = S0; a.dO = dO; a.dS_T = dS_T;
+    a.dx = dx; a.ddt = ddt; a.dA = dA; a.dB = dB; a.dC = dC; a.dS0 = dS0;
+    a.dD = D ? dD : nullptr; a.dgate = gate ? dgate : nullptr; a.ddt_bias = dt_bias ? ddt_bias : nullptr;
+    a.map = seq_map(cu_seqlens, dims->batch, dims->seqlen, dims->num_seqs);
+    a.tile = p.tile; a.chained = p.chained;
+    a.grad_bf16 = dims->grad_dtype == GDN2_BF16;
+    char *w = static_cast<char *>(workspace);
+    a.tiles_h = reinterpret_cast<float *>(w);
+    a.tiles_g = reinterpret_cast<float *>(w + p.states);
+    a.tiles_dt = reinterpret_cast<float *>(w + 2 * p.states);
+    a.tiles_db = reinterpret_cast<float *>(w + 2 * p.states + p.sums);
+    a.tiles_pass = reinterpret_cast<int32_t *>(w + 2 * p.states + 2 * p.sums);
+    a.part_bc = reinterpret_cast<float *>(w + 2 * p.states + 2 * p.sums + p.flags);
+    return done(gdn2::launch_scan_bwd(a, static_cast<hipStream_t>(stream)), "gdn2_selective_scan_bwd launch");
 }
 
 gdn2_status gdn2_selective_scan_step(const void *x, const void *dt, const float *A, const void *B,

@@ -104,4 +104,87 @@ __device__ __forceinline__ void store_tile(const ScanArgs &a, const ScanLane<NS,
         if (l.on && l.n0 + n < a.d_state) p[static_cast<int64_t>(l.n0 + n) * a.channels] = h[n];
 }
 
+constexpr int kB = 8;        // tokens whose inputs are in flight and whose B and C are staged together
+
+// B (and C) of tokens [t, hi) of a group, staged as fp32 [kB][NP] each, zero where there is none.
+// take() loads this thread's share of a batch into registers, put() writes it to LDS.
+template <typename T, int NP, bool WITH_C>
+struct Stage {
+    static constexpr int ROW = WITH_C ? 2 * NP : NP, PER = (kB * ROW + 255) / 256;
+    float r[PER];
+    __device__ __forceinline__ void take(const ScanArgs &a, int g, int t, int hi) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = threadIdx.x + 256 * i, k = e / ROW, j = e % ROW, n = j % NP;
+            r[i] = 0.f;
+            if (k < kB && t + k < hi && n < a.d_state) {
+                const bool c = WITH_C && j >= NP;
+                const T *p = static_cast<const T *>(c ? a.C : a.B);
+                r[i] = io<T>::ld(p + (t + k) * (c ? a.c_stride : a.b_stride) + g * a.d_state + n);
+            }
+        }
+    }
+    __device__ __forceinline__ void put(float *s) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = threadIdx.x + 256 * i;
+            if (PER * 256 == kB * ROW || e < kB * ROW) s[e] = r[i];
+        }
+    }
+};
+
+// NS floats from LDS, the same address in all lanes of a part.
+template <int NS>
+__device__ __forceinline__ void lds_row(const float *s, float (&v)[NS]) {
+#pragma unroll
+    for (int n = 0; n < NS; n += 4) {
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(s + n);
+        v[n] = x.x; v[n + 1] = x.y; v[n + 2] = x.z; v[n + 3] = x.w;
+    }
+}
+
+// Tiles are spread over the grid's second and third dimension.
+inline dim3 scan_grid(int blocks, int tiles) {
+    const int y = tiles < 32768 ? tiles : 32768;
+    return dim3(blocks, y, (tiles + y - 1) / y);
+}
+__device__ __forceinline__ int64_t tile_index() {
+    return static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
+}
+
+// Chains the tiles, from the front (DIR 1) or the back (DIR -1): what comes into tile i from the
+// tile before it replaces what tile i reached from zero. One thread per (state, channel), sixteen
+// tiles' loads in flight together.
+template <int DIR>
+__device__ __forceinline__ void chain_tiles(const ScanArgs &a, float *states, int tiles) {
+    const int64_t col = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
+    const int64_t cols = static_cast<int64_t>(a.d_state) * a.channels;
+    if (col >= cols) return;
+    const int n = static_cast<int>(col / a.channels);
+    const int c = static_cast<int>(col - static_cast<int64_t>(n) * a.channels);
+    const float A2 = kLog2e * a.A[static_cast<int64_t>(c) * a.d_state + n];
+    float run = 0.f;
+    constexpr int U = 16;
+    for (int i0 = 0; i0 < tiles; i0 += U) {
+        float hl[U], dl[U];
+        int pl[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (i0 + k < tiles) {
+                const int64_t i = DIR > 0 ? i0 + k : tiles - 1 - i0 - k;
+                hl[k] = states[i * cols + col];
+                dl[k] = a.tiles_dt[i * a.channels + c];
+                pl[k] = a.tiles_pass[i];
+            }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i0 + k < tiles) {
+                const int64_t i = DIR > 0 ? i0 + k : tiles - 1 - i0 - k;
+                states[i * cols + col] = run;
+                run = pl[k] ? fmaf(__builtin_amdgcn_exp2f(A2 * dl[k]), run, hl[k]) : hl[k];
+            }
+        }
+    }
+}
+
 }  // namespace gdn2

@@ -23,45 +23,6 @@ namespace gdn2 {
 
 namespace {
 
-constexpr int kB = 8;        // tokens whose inputs are in flight and whose B and C are staged together
-
-// B (and C) of tokens [t, hi) of a group, staged as fp32 [kB][NP] each, zero where there is none.
-// take() loads this thread's share of a batch into registers, put() writes it to LDS.
-template <typename T, int NP, bool WITH_C>
-struct Stage {
-    static constexpr int ROW = WITH_C ? 2 * NP : NP, PER = (kB * ROW + 255) / 256;
-    float r[PER];
-    __device__ __forceinline__ void take(const ScanArgs &a, int g, int t, int hi) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = threadIdx.x + 256 * i, k = e / ROW, j = e % ROW, n = j % NP;
-            r[i] = 0.f;
-            if (k < kB && t + k < hi && n < a.d_state) {
-                const bool c = WITH_C && j >= NP;
-                const T *p = static_cast<const T *>(c ? a.C : a.B);
-                r[i] = io<T>::ld(p + (t + k) * (c ? a.c_stride : a.b_stride) + g * a.d_state + n);
-            }
-        }
-    }
-    __device__ __forceinline__ void put(float *s) const {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = threadIdx.x + 256 * i;
-            if (PER * 256 == kB * ROW || e < kB * ROW) s[e] = r[i];
-        }
-    }
-};
-
-// NS floats from LDS, the same address in all lanes of a part.
-template <int NS>
-__device__ __forceinline__ void lds_row(const float *s, float (&v)[NS]) {
-#pragma unroll
-    for (int n = 0; n < NS; n += 4) {
-        const f32x4 x = *reinterpret_cast<const f32x4 *>(s + n);
-        v[n] = x.x; v[n + 1] = x.y; v[n + 2] = x.z; v[n + 3] = x.w;
-    }
-}
-
 // FINAL: runs a tile from its true state and writes o (and S_T). Otherwise: runs it from zero
 // and writes its state, its sum of dt and whether one sequence passes through all of it.
 template <typename T, int NS, int S, bool FINAL>
@@ -70,7 +31,8 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanArgs a) {
     constexpr int NP = Lane::NP, ROW = FINAL ? 2 * NP : NP;
     __shared__ __align__(16) float s_bc[2][kB * ROW];
     const Lane l(a, blockIdx.x);
-    const int64_t tile = blockIdx.y;
+    const int64_t tile = tile_index();
+    if (tile * a.tile >= a.map.total && tile > 0) return;      // the whole workgroup
     const int t0 = static_cast<int>(tile * a.tile);
     const int t1 = a.map.total - t0 < a.tile ? a.map.total : t0 + a.tile;
     const T *x = static_cast<const T *>(a.x) + l.c, *dt = static_cast<const T *>(a.dt) + l.c;
@@ -163,33 +125,9 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanArgs a) {
     }
 }
 
-// Chains the tiles: the state entering tile i replaces the state tile i reached from zero. One
-// thread per (state, channel); sixteen tiles' loads are in flight together.
+// Chains the tiles: one thread per (state, channel).
 __global__ __launch_bounds__(256) void scan_chain_kernel(ScanArgs a, int tiles) {
-    const int64_t col = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
-    const int64_t cols = static_cast<int64_t>(a.d_state) * a.channels;
-    if (col >= cols) return;
-    const int n = static_cast<int>(col / a.channels), c = static_cast<int>(col - static_cast<int64_t>(n) * a.channels);
-    const float A2 = kLog2e * a.A[static_cast<int64_t>(c) * a.d_state + n];
-    float run = 0.f;
-    constexpr int U = 16;
-    for (int i0 = 0; i0 < tiles; i0 += U) {
-        float hl[U], dl[U];
-        int pl[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (i0 + k < tiles) {
-                hl[k] = a.tiles_h[(i0 + k) * cols + col];
-                dl[k] = a.tiles_dt[static_cast<int64_t>(i0 + k) * a.channels + c];
-                pl[k] = a.tiles_pass[i0 + k];
-            }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (i0 + k >= tiles) break;
-            a.tiles_h[(i0 + k) * cols + col] = run;
-            run = pl[k] ? fmaf(__builtin_amdgcn_exp2f(A2 * dl[k]), run, hl[k]) : hl[k];
-        }
-    }
+    chain_tiles<1>(a, a.tiles_h, tiles);
 }
 
 // T tokens of every sequence against its slot of a pool [num_slots][channels][d_state]. LP lanes
@@ -267,7 +205,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepArgs a) {
 template <typename T, int NS, int S>
 hipError_t launch_fwd(const ScanArgs &a, hipStream_t st) {
     const int tiles = scan_tiles(a.map.total, a.tile);
-    const dim3 grid(scan_blocks(a.channels, a.groups, S), tiles);
+    const dim3 grid = scan_grid(scan_blocks(a.channels, a.groups, S), tiles);
     if (a.chained) {
         hipLaunchKernelGGL((scan_fwd_kernel<T, NS, S, false>), grid, dim3(256), 0, st, a);
         const int64_t cols = static_cast<int64_t>(a.d_state) * a.channels;
@@ -323,11 +261,9 @@ int scan_tiles(int total, int tile) { return total > tile ? (total + tile - 1) /
 int scan_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed) {
     const int64_t total = static_cast<int64_t>(batch) * seqlen;
     const int64_t waves = static_cast<int64_t>(kScanWaves) * scan_blocks(channels, groups, scan_parts(d_state));
-    if (!packed && batch <= 65535 && (batch * waves >= 1024 || seqlen <= 16)) return seqlen > 0 ? seqlen : 1;
-    int64_t t = (total * waves / 2048 + kB - 1) / kB * kB;
-    if (t < 16) t = 16;
-    while ((total + t - 1) / t > 65535) t *= 2;
-    return static_cast<int>(t);
+    if (!packed && (batch * waves >= 1024 || seqlen <= 16)) return seqlen > 0 ? seqlen : 1;
+    const int64_t t = (total * waves / 2048 + kB - 1) / kB * kB;
+    return t < 16 ? 16 : static_cast<int>(t);
 }
 
 // Whether some sequence may reach over a tile's end.

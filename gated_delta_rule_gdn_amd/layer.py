@@ -6,6 +6,7 @@ norms around a block.
     grads      = short_conv_bwd(x, weight, dy, ...)
     y          = short_conv_step(x, weight, conv_state, ...)        # conv_state updated in place
     o, S_T     = selective_scan_fwd(x, dt, A, B, C, D=None, gate=None, ...)
+    grads      = selective_scan_bwd(x, dt, A, B, C, dO, ...)
     o          = selective_scan_step(x, dt, A, B, C, state, ...)    # state updated in place
     h, y       = block_norm_fwd(x, norm_weight, gate, residual, scale, next_weight)
     grads      = block_norm_bwd(x, dh, dy, ...)
@@ -57,6 +58,8 @@ def declare(L: ctypes.CDLL) -> None:
             ("gdn2_short_conv_step", _i32, [_vp] * 5 + [_i32, _vp, cd, _vp]),
             ("gdn2_selective_scan_fwd_workspace_bytes", _sz, [sd]),
             ("gdn2_selective_scan_fwd", _i32, [_vp] * 12 + [sd, _vp, _sz, _vp]),
+            ("gdn2_selective_scan_bwd_workspace_bytes", _sz, [sd]),
+            ("gdn2_selective_scan_bwd", _i32, [_vp] * 21 + [sd, _vp, _sz, _vp]),
             ("gdn2_selective_scan_step", _i32,
              [_vp] * 9 + [_i32, _vp, _i32, _vp, sd, _vp]),
             ("gdn2_block_norm_fwd", _i32, [_vp] * 8 + [nd, _vp]),
@@ -334,6 +337,43 @@ def selective_scan_fwd_workspace_bytes(batch: int, seqlen: int, channels: int, d
                                        groups: int, dtype: torch.dtype, num_seqs: int = 0) -> int:
     d = ScanDims(batch, seqlen, num_seqs, channels, d_state, groups, _dtype_code(dtype))
     return int(lib().gdn2_selective_scan_fwd_workspace_bytes(ctypes.byref(d)))
+
+
+def selective_scan_bwd(x, dt, A, B, C, dO, D: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None,
+                       dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False,
+                       S0: Optional[torch.Tensor] = None,
+                       cu_seqlens: Optional[torch.Tensor] = None,
+                       dS_T: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of selective_scan_fwd given dO = dL/do [B,T,channels] (x's dtype or fp32) and
+    dS_T = dL/dS_T (None: zero). Returns dx, ddt, dB, dC (and dgate) in dO's dtype, dA (and dD,
+    ddt_bias, dS0) in fp32, each optional one for the argument given."""
+    N, num_seqs = _sequences(cu_seqlens, x.shape[0], x.device)
+    d = _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, num_seqs,
+                   _grad_code("dO", dO, x.dtype))
+    dev, shape, f32 = x.device, tuple(x.shape), torch.float32
+    st_shape = (N, d.channels, d.d_state)
+    s0 = _whole("S0", S0, dev, f32, st_shape)
+    pdo = _whole("dO", dO, dev, dO.dtype, shape)
+    pds = _whole("dS_T", dS_T, dev, f32, st_shape)
+    new = lambda like, dtype: None if like is None else torch.empty(  # noqa: E731
+        like.shape, dtype=dtype, device=dev)
+    gt = dO.dtype
+    out = {"dx": new(x, gt), "ddt": new(dt, gt), "dA": new(A, f32), "dB": new(B, gt),
+           "dC": new(C, gt), "dD": new(D, f32), "dgate": new(gate, gt),
+           "ddt_bias": new(dt_bias, f32), "dS0": new(S0, f32)}
+    ws = _workspace(workspace, lib().gdn2_selective_scan_bwd_workspace_bytes(ctypes.byref(d)), dev)
+    _call(dev, lib().gdn2_selective_scan_bwd, *_scan_ptrs(x, dt, A, B, C, D, gate, dt_bias), s0,
+          _ptr(cu_seqlens), pdo, pds, *(_ptr(t) for t in out.values()), ctypes.byref(d),
+          ws.data_ptr(), ws.numel())
+    return {n: t for n, t in out.items() if t is not None}
+
+
+def selective_scan_bwd_workspace_bytes(batch: int, seqlen: int, channels: int, d_state: int,
+                                       groups: int, dtype: torch.dtype, num_seqs: int = 0) -> int:
+    d = ScanDims(batch, seqlen, num_seqs, channels, d_state, groups, _dtype_code(dtype))
+    return int(lib().gdn2_selective_scan_bwd_workspace_bytes(ctypes.byref(d)))
 
 
 def selective_scan_step(x, dt, A, B, C, state, D: Optional[torch.Tensor] = None,

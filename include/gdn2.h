@@ -30,10 +30,10 @@
  *   - gdn2_short_conv_fwd, gdn2_short_conv_bwd, gdn2_short_conv_step
  *                               the short causal convolution before the recurrence, over
  *                               prompts, its gradients, and for single tokens;
- *   - gdn2_selective_scan_fwd, gdn2_selective_scan_step
+ *   - gdn2_selective_scan_fwd, gdn2_selective_scan_bwd, gdn2_selective_scan_step
  *                               the selective state space scan, the other linear recurrence
  *                               of hybrid layers (a decay per channel and state), over
- *                               prompts and for single tokens;
+ *                               prompts, its gradients, and for single tokens;
  *   - gdn2_block_norm_fwd, gdn2_block_norm_bwd
  *                               the norms after and before a block, fused with its gate, the
  *                               residual and its scale, and their gradients.
@@ -575,6 +575,30 @@ gdn2_status gdn2_selective_scan_fwd(const void *x, const void *dt, const float *
                                     const void *C, const float *D, const void *gate,
                                     const float *dt_bias, const float *S0, const int32_t *cu_seqlens,
                                     void *o, float *S_T, const gdn2_scan_dims *dims, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace gdn2_selective_scan_bwd needs, or 0 if the dims are invalid. */
+size_t gdn2_selective_scan_bwd_workspace_bytes(const gdn2_scan_dims *dims);
+
+/*
+ * Gradients of gdn2_selective_scan_fwd, which is formed again from its inputs.
+ *   x .. cu_seqlens   the forward's inputs
+ *   dO           device [B, T, channels] (grad_dtype): dL/do
+ *   dS_T         device fp32 [N][channels][d_state]: dL/dS_T, or NULL for zero
+ *   dx, ddt      device [B, T, channels] (grad_dtype); ddt is of dt as given, before dt_bias
+ *   dgate        device [B, T, channels] (grad_dtype), required with a gate
+ *   dB, dC       device [B, T, groups, d_state] (grad_dtype), contiguous
+ *   dA           device fp32 [channels][d_state]
+ *   dD, ddt_bias device fp32 [channels], each required with its input
+ *   dS0          device fp32 [N][channels][d_state], or NULL to skip it
+ *   workspace    at least gdn2_selective_scan_bwd_workspace_bytes() bytes, 256-byte aligned
+ */
+gdn2_status gdn2_selective_scan_bwd(const void *x, const void *dt, const float *A, const void *B,
+                                    const void *C, const float *D, const void *gate,
+                                    const float *dt_bias, const float *S0, const int32_t *cu_seqlens,
+                                    const void *dO, const float *dS_T, void *dx, void *ddt, float *dA,
+                                    void *dB, void *dC, float *dD, void *dgate, float *ddt_bias,
+                                    float *dS0, const gdn2_scan_dims *dims, void *workspace,
                                     size_t workspace_bytes, void *stream);
 
 /*

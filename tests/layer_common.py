@@ -216,3 +216,102 @@ def norm_ref(x, nw, gate, res, scale, nxt, eps, dh=None, dy=None):
         ge = rx * (we + np.abs(x) * me + 3 * U * (np.abs(w) + np.abs(x * m))) + np.abs(g) * R
     out["dx"], out["dx_b"] = g, ge
     return out
+
+
+def scan_bwd_ref(x, dt, A, B, C, D, gate, dt_bias, softplus, S0, lens, dO, dS_T, tile=32):
+    """Gradients of scan_ref's o and S_T and their bounds, token by token from the last to the
+    first. `gm` holds the magnitudes behind the state's gradient, `ge` its error."""
+    T, ch = x.shape
+    G, M = B.shape[1:]
+    rep = ch // G
+    cu = offsets(lens)
+    raw = dt + (0.0 if dt_bias is None else dt_bias)
+    step = np.logaddexp(0.0, raw) if softplus else raw
+    rel = U * ((3 * np.abs(raw) + 24) if softplus else np.ones_like(raw))
+    sp = sigmoid(raw) if softplus else np.ones_like(raw)
+    spe = (np.abs(raw) + 6) * 2 * U * sp if softplus else np.zeros_like(raw)
+    skip = np.zeros(ch) if D is None else D
+    z = lambda *s: np.zeros(s)  # noqa: E731
+    names = {"dx": (T, ch), "ddt": (T, ch), "dgate": (T, ch), "dB": (T, G, M), "dC": (T, G, M),
+             "dA": (ch, M), "dD": (ch,), "ddt_bias": (ch,), "dS0": (len(lens), ch, M)}
+    r = {n: z(*s) for n, s in names.items()}
+    r.update({n + "_b": z(*s) for n, s in names.items()})
+    # tiles' sums in order, a few lanes' sums before them
+    grow = (tile + T / tile + 8) * U
+    over = (16 + ch / 32) * U                 # channels: lanes, waves, workgroups
+    chan = lambda v: v.reshape(G, rep, M).sum(1)  # noqa: E731
+    for n in range(len(lens)):
+        lo, hi = cu[n], cu[n + 1]
+        L = hi - lo
+        H, HM, HE = z(L + 1, ch, M), z(L + 1, ch, M), z(L + 1, ch, M)
+        a, da = z(L, ch, M), z(L, ch, M)
+        H[0] = 0.0 if S0 is None else S0[n]
+        HM[0] = np.abs(H[0])
+        for k in range(L):
+            t = lo + k
+            er = rel[t][:, None]
+            zz = step[t][:, None] * A
+            a[k] = np.exp(zz)
+            da[k] = a[k] * (np.abs(zz) * (er + 3 * U) + 2 * U)
+            b = (step[t] * x[t])[:, None] * np.repeat(B[t], rep, 0)
+            HE[k + 1] = a[k] * HE[k] + da[k] * HM[k] + np.abs(b) * (er + 4 * U)
+            H[k + 1], HM[k + 1] = a[k] * H[k] + b, a[k] * HM[k] + np.abs(b)
+            HE[k + 1] += 2 * U * HM[k + 1]
+        HE = HE + 0.4 * tile * U * HM
+        g = z(ch, M) if dS_T is None else dS_T[n].copy()
+        gm, ge = np.abs(g), z(ch, M)
+        for k in range(L - 1, -1, -1):
+            t = lo + k
+            er = rel[t][:, None]
+            b, c = np.repeat(B[t], rep, 0), np.repeat(C[t], rep, 0)
+            u = (step[t] * x[t])[:, None]
+            dy, dye = dO[t], z(ch)
+            if gate is not None:
+                s = sigmoid(gate[t])
+                sl = gate[t] * s
+                y = (c * H[k + 1]).sum(-1) + skip * x[t]
+                ye = (np.abs(c) * (HE[k + 1] + (M + 4) * U * HM[k + 1])).sum(-1) + 2 * U * np.abs(skip * x[t])
+                slope = s * (1 + gate[t] * (1 - s))
+                r["dgate"][t] = dO[t] * y * slope
+                r["dgate_b"][t] = np.abs(dO[t]) * (ye * np.abs(slope) + np.abs(y) * slope_err(gate[t], 0.0)) \
+                    + 3 * U * np.abs(r["dgate"][t])
+                dy = dO[t] * sl
+                dye = np.abs(dy) * (np.abs(gate[t]) + 9) * 2 * U
+            cy = c * dy[:, None]
+            gh, ghm = cy + g, np.abs(cy) + gm
+            ghe = np.abs(c) * dye[:, None] + ge + 2 * U * ghm
+            gt = ghe + 0.4 * tile * U * ghm
+            v = dy[:, None] * H[k + 1]
+            r["dC"][t] = chan(v)
+            r["dC_b"][t] = chan(np.abs(dy)[:, None] * HE[k + 1] + dye[:, None] * np.abs(H[k + 1])
+                                + over * np.abs(dy)[:, None] * HM[k + 1])
+            r["dB"][t] = chan(gh * u)
+            r["dB_b"][t] = chan(np.abs(u) * (gt + ghm * (er + over + 2 * U)))
+            sB = (gh * b).sum(-1)
+            sBm = (ghm * np.abs(b)).sum(-1)
+            sBe = (gt * np.abs(b)).sum(-1) + (M + 3) * U * sBm
+            ah, ahm = a[k] * H[k], a[k] * HM[k]
+            ahe = a[k] * HE[k] + da[k] * HM[k] + U * ahm
+            q = gh * ah
+            qe = gt * ahm + ghm * ahe + 2 * U * ghm * ahm
+            sA = (q * A).sum(-1)
+            sAe = (qe * np.abs(A)).sum(-1) + (M + 5) * U * (ghm * ahm * np.abs(A)).sum(-1)
+            d = step[t]
+            r["dx"][t] = skip * dy + d * sB
+            r["dx_b"][t] = np.abs(skip) * (dye + 2 * U * np.abs(dy)) + np.abs(d) * (sBe + (rel[t] + 2 * U) * sBm)
+            full = x[t] * sB + sA
+            fe = np.abs(x[t]) * sBe + sAe + 2 * U * (np.abs(x[t]) * sBm + (ghm * ahm * np.abs(A)).sum(-1))
+            r["ddt"][t] = full * sp[t]
+            de = fe * sp[t] + np.abs(full) * spe[t] + U * np.abs(r["ddt"][t])
+            r["ddt_b"][t] = de
+            r["dA"] += q * d[:, None]
+            r["dA_b"] += np.abs(d)[:, None] * (qe + ghm * ahm * (er + grow))
+            r["dD"] += dy * x[t]
+            r["dD_b"] += np.abs(x[t]) * (dye + (grow + U) * np.abs(dy))
+            r["ddt_bias"] += r["ddt"][t]
+            r["ddt_bias_b"] += de + grow * np.abs(r["ddt"][t])
+            g, ge = a[k] * gh, a[k] * ghe + da[k] * ghm
+            gm = a[k] * ghm
+            ge = ge + U * gm
+        r["dS0"][n], r["dS0_b"][n] = g, ge + 0.4 * tile * U * gm
+    return r

@@ -184,3 +184,23 @@ def test_block_norm_backward_refusals(L):
     assert norm_bwd(L, dx=P(8), ws=None) == WORKSPACE
     assert norm_bwd(L, dx=P(8), nbytes=need - 1) == WORKSPACE
     assert norm_bwd(L, dx=P(8), ws=ctypes.c_void_p(0x10040)) == WORKSPACE
+
+
+def scan_bwd(L, dx=P(1), dA=P(11), D=None, dD=None, gate=None, ws=P(16), nbytes=1 << 34, dS0=None, **kw):
+    # dx defaults to x's pointer
+    return L.gdn2_selective_scan_bwd(P(1), P(2), P(3), P(4), P(5), D, gate, None, None, None, P(9), None,
+                                     dx, P(10), dA, P(12), P(13), dD, None, None, dS0,
+                                     dims(ScanDims, SCAN, **kw), ws, nbytes, None)
+
+
+def test_selective_scan_backward_refusals(L):
+    need = L.gdn2_selective_scan_bwd_workspace_bytes(dims(ScanDims, SCAN))
+    assert need > 0 and L.gdn2_selective_scan_bwd_workspace_bytes(dims(ScanDims, SCAN, d_state=200)) == 0
+    assert scan_bwd(L, dtype=0) == UNSUPPORTED
+    assert scan_bwd(L) == SHAPE
+    assert scan_bwd(L, dx=None) == NULL and scan_bwd(L, dx=P(6), dA=None) == NULL
+    assert scan_bwd(L, dx=P(6), D=P(7)) == NULL and scan_bwd(L, dx=P(6), gate=P(7)) == NULL
+    assert scan_bwd(L, dx=P(6), dS0=P(6)) == SHAPE
+    assert scan_bwd(L, dx=P(6), ws=None) == WORKSPACE
+    assert scan_bwd(L, dx=P(6), nbytes=need - 1) == WORKSPACE
+    assert scan_bwd(L, dx=P(6), ws=ctypes.c_void_p(0x10008)) == WORKSPACE
