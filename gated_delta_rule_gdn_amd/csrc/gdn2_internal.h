@@ -177,12 +177,13 @@ struct ScanArgs {
     float *tiles_db = nullptr;       // [tiles][channels]: sums for ddt_bias
     float *part_bc = nullptr;        // [workgroups across channels][tokens][2][d_state]
 };
-constexpr int kScanMaxBwdTile = 32;  // tokens of a tile of the backward, which LDS holds whole
+constexpr int kScanMaxBwdTile = 64;  // tokens of a tile of the backward, which LDS holds whole
 int scan_parts(int d_state);                              // lanes that share a channel's states
 int scan_blocks(int channels, int groups, int parts);     // workgroups across the channels
 int scan_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed);
 int scan_tiles(int total, int tile);
 bool scan_chained(int batch, int seqlen, bool packed, int tile);
+int scan_bwd_parts(int d_state);                          // the same in the backward
 int scan_bwd_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed);
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st);
 hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st);

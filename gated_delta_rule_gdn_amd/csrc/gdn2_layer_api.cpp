@@ -154,7 +154,7 @@ struct ScanPlan {
         states = padded(static_cast<size_t>(tiles) * d->d_state * d->channels * sizeof(float));
         sums = padded(static_cast<size_t>(tiles) * d->channels * sizeof(float));
         flags = padded(static_cast<size_t>(tiles) * sizeof(int32_t));
-        shares = padded(static_cast<size_t>(gdn2::scan_blocks(d->channels, d->groups, gdn2::scan_parts(d->d_state))) *
+        shares = padded(static_cast<size_t>(gdn2::scan_blocks(d->channels, d->groups, gdn2::scan_bwd_parts(d->d_state))) *
                         d->batch * d->seqlen * 2 * d->d_state * sizeof(float));
     }
     size_t fwd_bytes() const { return chained ? states + sums + flags : 0; }

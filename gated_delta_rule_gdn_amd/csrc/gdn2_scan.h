@@ -39,33 +39,31 @@ __device__ __forceinline__ float sum_parts(float x) {
     return x;
 }
 
-// log(1 + e), 0 <= e <= 1, as 2 atanh(e / (2 + e)): the series in s^2 <= 1/9, cut where the next
-// term is below 2^-26 of the value, so small e keep their relative precision (log(1 + e) of the
-// rounded sum would lose it: steps of 0.001 are usual).
-__device__ __forceinline__ float log1p_unit(float e) {
-    const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
-    float p = 1.f / 15.f;
-    p = fmaf(p, q, 1.f / 13.f);
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    return 2.f * fmaf(p * q, s, s);
-}
-
-// softplus(x) = max(x, 0) + log(1 + e^-|x|)
+// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in [0, 1]. log(1 + e) / e is a polynomial of
+// degree 8, fitted for the least relative error on [0, 1] (3e-8; with fp32 Horner steps 2.8 * 2^-24),
+// so that a small e, a usual step of 0.001, keeps its relative precision.
 __device__ __forceinline__ float softplus(float x) {
-    return fmaxf(x, 0.f) + log1p_unit(__builtin_amdgcn_exp2f(-kLog2e * fabsf(x)));
+    const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(x));
+    float p = 0.005232692696154118f;
+    p = fmaf(p, e, -0.029505232349038124f);
+    p = fmaf(p, e, 0.07822594046592712f);
+    p = fmaf(p, e, -0.13663244247436523f);
+    p = fmaf(p, e, 0.19106006622314453f);
+    p = fmaf(p, e, -0.2484298199415207f);
+    p = fmaf(p, e, 0.3331909775733948f);
+    p = fmaf(p, e, -0.4999949336051941f);
+    p = fmaf(p, e, 0.9999999403953552f);
+    return fmaf(p, e, fmaxf(x, 0.f));
 }
 
-// The decay rates of a lane's states times log2(e), so that a decay is exp2(dt * A2).
+// The decay rates of a lane's states times log2(e), so that a decay is exp2(dt * A2). A rate of
+// -inf becomes the lowest value, so that a step of zero keeps the state (0 * -inf would not).
 template <int NS, int S>
 __device__ __forceinline__ void load_rates(const ScanArgs &a, const ScanLane<NS, S> &l, float (&A2)[NS]) {
     const float *A = a.A + static_cast<int64_t>(l.c) * a.d_state;
 #pragma unroll
     for (int n = 0; n < NS; ++n)
-        A2[n] = l.on && l.n0 + n < a.d_state ? kLog2e * A[l.n0 + n] : 0.f;
+        A2[n] = l.on && l.n0 + n < a.d_state ? fmaxf(kLog2e * A[l.n0 + n], -3.4e38f) : 0.f;
 }
 
 // A lane's states from / to a row of [N][channels][d_state].
@@ -106,21 +104,21 @@ __device__ __forceinline__ void store_tile(const ScanArgs &a, const ScanLane<NS,
 
 constexpr int kB = 8;        // tokens whose inputs are in flight and whose B and C are staged together
 
-// B (and C) of tokens [t, hi) of a group, staged as fp32 [kB][NP] each, zero where there is none.
-// take() loads this thread's share of a batch into registers, put() writes it to LDS.
+// B (and C) of the m <= kB tokens from t on, staged as fp32 [kB][NP] each, zero where there is
+// none. take() loads this thread's share of a batch into registers, put() writes it to LDS.
 template <typename T, int NP, bool WITH_C>
 struct Stage {
     static constexpr int ROW = WITH_C ? 2 * NP : NP, PER = (kB * ROW + 255) / 256;
-    float r[PER];
-    __device__ __forceinline__ void take(const ScanArgs &a, int g, int t, int hi) {
+    T r[PER];
+    __device__ __forceinline__ void take(const ScanArgs &a, int g, int t, int m) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = threadIdx.x + 256 * i, k = e / ROW, j = e % ROW, n = j % NP;
-            r[i] = 0.f;
-            if (k < kB && t + k < hi && n < a.d_state) {
+            r[i] = T{};
+            if (k < m && n < a.d_state) {
                 const bool c = WITH_C && j >= NP;
                 const T *p = static_cast<const T *>(c ? a.C : a.B);
-                r[i] = io<T>::ld(p + (t + k) * (c ? a.c_stride : a.b_stride) + g * a.d_state + n);
+                r[i] = p[(t + k) * (c ? a.c_stride : a.b_stride) + g * a.d_state + n];
             }
         }
     }
@@ -128,10 +126,37 @@ struct Stage {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = threadIdx.x + 256 * i;
-            if (PER * 256 == kB * ROW || e < kB * ROW) s[e] = r[i];
+            if (PER * 256 == kB * ROW || e < kB * ROW) s[e] = io<T>::val(r[i]);
         }
     }
 };
+
+// Element c of a row: one pointer for the wave and 32 bits of offset per lane (c < 2^20), the
+// form that global memory instructions take without address arithmetic.
+template <typename T>
+__device__ __forceinline__ const T *elem(const T *row, uint32_t c) {
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) + c * static_cast<uint32_t>(sizeof(T)));
+}
+template <typename T>
+__device__ __forceinline__ T *elem(T *row, uint32_t c) {
+    return reinterpret_cast<T *>(reinterpret_cast<char *>(row) + c * static_cast<uint32_t>(sizeof(T)));
+}
+
+// Element c of the K rows from `row` on; rows from m on repeat row m - 1, so no access is
+// conditional.
+template <typename T, int K>
+__device__ __forceinline__ void fetch_rows(const T *row, int64_t stride, uint32_t c, int m, T (&v)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        v[k] = *elem(row, c);
+        row += k + 1 < m ? stride : 0;
+    }
+}
+template <typename T, int K>
+__device__ __forceinline__ void widen(const T (&r)[K], float (&v)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = io<T>::val(r[k]);
+}
 
 // NS floats from LDS, the same address in all lanes of a part.
 template <int NS>
@@ -141,6 +166,15 @@ __device__ __forceinline__ void lds_row(const float *s, float (&v)[NS]) {
         const f32x4 x = *reinterpret_cast<const f32x4 *>(s + n);
         v[n] = x.x; v[n + 1] = x.y; v[n + 2] = x.z; v[n + 3] = x.w;
     }
+}
+
+// Holds values where they are computed, at no cost: behind an unrolled batch of tokens it keeps the
+// compiler from moving most of the batch into the next block, with all its LDS reads live until
+// there.
+template <int N>
+__device__ __forceinline__ void pin(float (&v)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) asm volatile("" : "+v"(v[n]));
 }
 
 // Tiles are spread over the grid's second and third dimension.

@@ -15,6 +15,8 @@
 // tile): one pass forms each tile's state from zero and its sum of dt (the decay over a tile is
 // exp(A sum dt)), a second chains the tiles, a third runs them from their true states. That costs
 // the exp2 and three operations once more, so the rule takes it only when it is the faster.
+#include <type_traits>
+
 #include "gdn2_internal.h"
 #include "gdn2_layer.h"
 #include "gdn2_scan.h"
@@ -25,8 +27,11 @@ namespace {
 
 // FINAL: runs a tile from its true state and writes o (and S_T). Otherwise: runs it from zero
 // and writes its state, its sum of dt and whether one sequence passes through all of it.
+// A batch of kB tokens has no branch between its tokens, so their LDS reads and arithmetic
+// overlap; in a sequence's last batch the missing tokens take steps of zero, which leave h as
+// it is.
 template <typename T, int NS, int S, bool FINAL>
-__global__ __launch_bounds__(256) void scan_fwd_kernel(ScanArgs a) {
+__global__ __launch_bounds__(256, FINAL ? 3 : 4) void scan_fwd_kernel(ScanArgs a) {
     using Lane = ScanLane<NS, S>;
     constexpr int NP = Lane::NP, ROW = FINAL ? 2 * NP : NP;
     __shared__ __align__(16) float s_bc[2][kB * ROW];
@@ -35,92 +40,101 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanArgs a) {
     if (tile * a.tile >= a.map.total && tile > 0) return;      // the whole workgroup
     const int t0 = static_cast<int>(tile * a.tile);
     const int t1 = a.map.total - t0 < a.tile ? a.map.total : t0 + a.tile;
-    const T *x = static_cast<const T *>(a.x) + l.c, *dt = static_cast<const T *>(a.dt) + l.c;
-    const T *gate = a.gate ? static_cast<const T *>(a.gate) + l.c : nullptr;
-    T *o = static_cast<T *>(a.o) + l.c;
+    const uint32_t c = l.c;
+    const bool gated = FINAL && a.gate;
     float A2[NS], h[NS];
     load_rates(a, l, A2);
-    const float bias = a.dt_bias ? a.dt_bias[l.c] : 0.f, skip = a.D ? a.D[l.c] : 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.D ? a.D[c] : 0.f;
     float sum = 0.f;
     bool pass = false;
 #pragma unroll
     for (int n = 0; n < NS; ++n) h[n] = 0.f;
     for_spans(a.map, t0, t1, [&](const Span &s) {
-        if (s.starts) {
-            if (a.S0) load_state(a, l, a.S0, s.i, h);
-            else
-#pragma unroll
-                for (int n = 0; n < NS; ++n) h[n] = 0.f;
-        } else if (FINAL) {
+        if (!s.starts && FINAL) {
             load_tile(a, l, a.tiles_h, tile, h);
+        } else if (s.starts && a.S0) {
+            load_state(a, l, a.S0, s.i, h);
         } else {
 #pragma unroll
             for (int n = 0; n < NS; ++n) h[n] = 0.f;
         }
         pass = !s.starts && !s.ends;
+        Stage<T, NP, FINAL> st;
+        T xr[kB], dr[kB], gr[kB];
+        auto fetch = [&](int t) {
+            const int m = s.hi - t;
+            st.take(a, l.g, t, m);
+            fetch_rows(static_cast<const T *>(a.dt) + t * a.dt_stride, a.dt_stride, c, m, dr);
+            fetch_rows(static_cast<const T *>(a.x) + t * a.x_stride, a.x_stride, c, m, xr);
+            if (gated) fetch_rows(static_cast<const T *>(a.gate) + t * a.gate_stride, a.gate_stride, c, m, gr);
+        };
         if (s.lo < s.hi) {
-            Stage<T, NP, FINAL> st;
-            T xr[kB], dr[kB], gr[kB];
-            auto fetch = [&](int t) {
-                st.take(a, l.g, t, s.hi);
-#pragma unroll
-                for (int k = 0; k < kB; ++k)
-                    if (t + k < s.hi) {
-                        xr[k] = x[(t + k) * a.x_stride];
-                        dr[k] = dt[(t + k) * a.dt_stride];
-                        if (FINAL && gate) gr[k] = gate[(t + k) * a.gate_stride];
-                    }
-            };
             fetch(s.lo);
             st.put(s_bc[0]);
             __syncthreads();
-            int buf = 0;
-            for (int t = s.lo; t < s.hi; t += kB, buf ^= 1) {
-                float xv[kB], dv[kB], gv[kB];
+        }
+        int buf = 0;
+        for (int t = s.lo; t < s.hi; t += kB, buf ^= 1) {
+            float x[kB], d[kB], g[kB], y[kB] = {};
+            widen(dr, d);
+            widen(xr, x);
+            if (gated) widen(gr, g);
+            const int m = s.hi - t;
+            if (m > kB) fetch(t + kB);
 #pragma unroll
-                for (int k = 0; k < kB; ++k) {
-                    xv[k] = io<T>::val(xr[k]);
-                    dv[k] = io<T>::val(dr[k]);
-                    gv[k] = io<T>::val(gr[k]);
+            for (int k = 0; k < kB; ++k) d[k] += bias;
+            if (a.softplus)
+#pragma unroll
+                for (int k = 0; k < kB; ++k) d[k] = softplus(d[k]);
+            if (m < kB)
+#pragma unroll
+                for (int k = 1; k < kB; ++k)
+                    if (k >= m) d[k] = x[k] = 0.f;
+            const float *bc = s_bc[buf] + l.n0;
+#pragma unroll
+            for (int k = 0; k < kB; ++k) {
+                float b[NS];
+                lds_row<NS>(bc + k * ROW, b);
+                const float u = d[k] * x[k];
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    h[n] = fmaf(__builtin_amdgcn_exp2f(d[k] * A2[n]), h[n], u * b[n]);
+                if constexpr (FINAL) {
+                    float cv[NS];
+                    lds_row<NS>(bc + k * ROW + NP, cv);
+                    y[k] = 0.f;
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) y[k] = fmaf(cv[n], h[n], y[k]);
+                } else {
+                    sum += d[k];
                 }
-                const bool more = t + kB < s.hi;
-                if (more) fetch(t + kB);
-                const int m = s.hi - t;
+            }
+            pin(h);
+            if (FINAL) pin(y);
+            if constexpr (FINAL) {
 #pragma unroll
-                for (int k = 0; k < kB; ++k) {
-                    if (k >= m) break;
-                    float d = dv[k] + bias;
-                    if (a.softplus) d = softplus(d);
-                    const float u = d * xv[k];
-                    const float *row = s_bc[buf] + k * ROW + l.n0;
-                    float b[NS];
-                    lds_row<NS>(row, b);
+                for (int k = 0; k < kB; ++k) y[k] = fmaf(skip, x[k], sum_parts<S>(y[k]));
+                if (gated)
 #pragma unroll
-                    for (int n = 0; n < NS; ++n)
-                        h[n] = fmaf(__builtin_amdgcn_exp2f(d * A2[n]), h[n], u * b[n]);
-                    if constexpr (FINAL) {
-                        float c[NS];
-                        lds_row<NS>(row + NP, c);
-                        float y = 0.f;
+                    for (int k = 0; k < kB; ++k) y[k] *= silu(g[k]);
+                pin(y);
+                if (l.on && l.part == 0) {
+                    T *row = static_cast<T *>(a.o) + t * static_cast<int64_t>(a.channels);
 #pragma unroll
-                        for (int n = 0; n < NS; ++n) y = fmaf(c[n], h[n], y);
-                        y = fmaf(skip, xv[k], sum_parts<S>(y));
-                        if (gate) y *= silu(gv[k]);
-                        if (l.on && l.part == 0)
-                            io<T>::st(o + (t + k) * static_cast<int64_t>(a.channels), y);
-                    } else {
-                        sum += d;
+                    for (int k = 0; k < kB; ++k) {
+                        if (k < m) io<T>::st(elem(row, c), y[k]);
+                        row += a.channels;
                     }
                 }
-                if (more) st.put(s_bc[buf ^ 1]);
-                __syncthreads();
             }
+            if (m > kB) st.put(s_bc[buf ^ 1]);
+            __syncthreads();
         }
         if (FINAL && s.ends && a.S_T) store_state(a, l, a.S_T, s.i, h);
     });
     if constexpr (!FINAL) {
         store_tile(a, l, a.tiles_h, tile, h);
-        if (l.on && l.part == 0) a.tiles_dt[tile * a.channels + l.c] = sum;
+        if (l.on && l.part == 0) a.tiles_dt[tile * a.channels + c] = sum;
         if (blockIdx.x == 0 && threadIdx.x == 0) a.tiles_pass[tile] = pass ? 1 : 0;
     }
 }
@@ -205,9 +219,10 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepArgs a) {
 template <typename T, int NS, int S>
 hipError_t launch_fwd(const ScanArgs &a, hipStream_t st) {
     const int tiles = scan_tiles(a.map.total, a.tile);
-    const dim3 grid = scan_grid(scan_blocks(a.channels, a.groups, S), tiles);
-    if (a.chained) {
-        hipLaunchKernelGGL((scan_fwd_kernel<T, NS, S, false>), grid, dim3(256), 0, st, a);
+    const int blocks = scan_blocks(a.channels, a.groups, S);
+    const dim3 grid = scan_grid(blocks, tiles);
+    if (a.chained) {        // what the last tile reaches goes nowhere
+        hipLaunchKernelGGL((scan_fwd_kernel<T, NS, S, false>), scan_grid(blocks, tiles - 1), dim3(256), 0, st, a);
         const int64_t cols = static_cast<int64_t>(a.d_state) * a.channels;
         hipLaunchKernelGGL(scan_chain_kernel, dim3(static_cast<unsigned>((cols + 255) / 256)), dim3(256),
                            0, st, a, tiles);
@@ -257,12 +272,12 @@ int scan_blocks(int channels, int groups, int parts) {
 int scan_tiles(int total, int tile) { return total > tile ? (total + tile - 1) / tile : 1; }
 
 // Tokens per tile. A dense batch whose sequences alone give 1,024 waves (one per SIMD) is not
-// cut: its tile is a sequence. Otherwise about 2,048 waves, 16 tokens at least.
+// cut: its tile is a sequence. Otherwise about 3,072 waves (three per SIMD), 16 tokens at least.
 int scan_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed) {
     const int64_t total = static_cast<int64_t>(batch) * seqlen;
     const int64_t waves = static_cast<int64_t>(kScanWaves) * scan_blocks(channels, groups, scan_parts(d_state));
     if (!packed && (batch * waves >= 1024 || seqlen <= 16)) return seqlen > 0 ? seqlen : 1;
-    const int64_t t = (total * waves / 2048 + kB - 1) / kB * kB;
+    const int64_t t = (total * waves / 3072 + kB - 1) / kB * kB;
     return t < 16 ? 16 : static_cast<int>(t);
 }
 

@@ -16,8 +16,8 @@
 // Every sum has a fixed order: the same bits at every call.
 //
 // dB and dC sum over channels, which lie across the lanes. A wave reduces and spreads at once:
-// each step sends half of a lane's values to the partner lane and adds the other half, so 16
-// values over 64 lanes cost about 35 operations instead of 96 (reduce_spread).
+// each step sends half of a lane's values to the partner lane and adds the other half, so 8
+// values over 32 lanes cost about 19 operations instead of 40 (reduce_spread).
 #include "gdn2_internal.h"
 #include "gdn2_layer.h"
 #include "gdn2_scan.h"
@@ -95,9 +95,10 @@ __device__ __forceinline__ int spread_index(bool *writes) {
     return n;
 }
 
-// Launch 1. See the head of the file; `chain` is the running product of decays.
+// Launch 1. See the head of the file; `chain` is the running product of decays, which only the
+// sequence that enters the tile needs (it is zero behind that sequence's end).
 template <typename T, typename TG, int NS, int S>
-__global__ __launch_bounds__(256) void scan_bwd_tile_kernel(ScanArgs a) {
+__global__ __launch_bounds__(256, 2) void scan_bwd_tile_kernel(ScanArgs a) {
     using Lane = ScanLane<NS, S>;
     constexpr int NP = Lane::NP;
     __shared__ __align__(16) float s_bc[2][kB * 2 * NP];
@@ -106,12 +107,10 @@ __global__ __launch_bounds__(256) void scan_bwd_tile_kernel(ScanArgs a) {
     if (tile * a.tile >= a.map.total && tile > 0) return;      // the whole workgroup
     const int t0 = static_cast<int>(tile * a.tile);
     const int t1 = a.map.total - t0 < a.tile ? a.map.total : t0 + a.tile;
-    const T *x = static_cast<const T *>(a.x) + l.c, *dt = static_cast<const T *>(a.dt) + l.c;
-    const T *gate = a.gate ? static_cast<const T *>(a.gate) + l.c : nullptr;
-    const TG *dO = static_cast<const TG *>(a.dO) + l.c;
+    const uint32_t c = l.c;
     float A2[NS], h[NS], back[NS], chain[NS];
     load_rates(a, l, A2);
-    const float bias = a.dt_bias ? a.dt_bias[l.c] : 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
     float sum = 0.f;
     bool pass = false;
 #pragma unroll
@@ -122,79 +121,80 @@ __global__ __launch_bounds__(256) void scan_bwd_tile_kernel(ScanArgs a) {
             else
 #pragma unroll
                 for (int n = 0; n < NS; ++n) h[n] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NS; ++n) chain[n] = 0.f;
         }
         pass = !s.starts && !s.ends;
+        Stage<T, NP, true> st;
+        T xr[kB], dr[kB], gr[kB];
+        TG yr[kB];
+        auto fetch = [&](int t) {
+            const int m = s.hi - t;
+            st.take(a, l.g, t, m);
+            fetch_rows(static_cast<const T *>(a.dt) + t * a.dt_stride, a.dt_stride, c, m, dr);
+            fetch_rows(static_cast<const T *>(a.x) + t * a.x_stride, a.x_stride, c, m, xr);
+            fetch_rows(static_cast<const TG *>(a.dO) + t * static_cast<int64_t>(a.channels), a.channels, c, m, yr);
+            if (a.gate) fetch_rows(static_cast<const T *>(a.gate) + t * a.gate_stride, a.gate_stride, c, m, gr);
+        };
         if (s.lo < s.hi) {
-            Stage<T, NP, true> st;
-            T xr[kB], dr[kB], gr[kB];
-            TG yr[kB];
-            auto fetch = [&](int t) {
-                st.take(a, l.g, t, s.hi);
-#pragma unroll
-                for (int k = 0; k < kB; ++k)
-                    if (t + k < s.hi) {
-                        xr[k] = x[(t + k) * a.x_stride];
-                        dr[k] = dt[(t + k) * a.dt_stride];
-                        yr[k] = dO[(t + k) * static_cast<int64_t>(a.channels)];
-                        if (gate) gr[k] = gate[(t + k) * a.gate_stride];
-                    }
-            };
             fetch(s.lo);
             st.put(s_bc[0]);
             __syncthreads();
-            int buf = 0;
-            for (int t = s.lo; t < s.hi; t += kB, buf ^= 1) {
-                float xv[kB], dv[kB], yv[kB];
-#pragma unroll
-                for (int k = 0; k < kB; ++k) {
-                    xv[k] = io<T>::val(xr[k]);
-                    dv[k] = io<T>::val(dr[k]);
-                    yv[k] = io<TG>::val(yr[k]);
-                    if (gate) yv[k] *= silu(io<T>::val(gr[k]));
-                }
-                const bool more = t + kB < s.hi;
-                if (more) fetch(t + kB);
-                const int m = s.hi - t;
-#pragma unroll
-                for (int k = 0; k < kB; ++k) {
-                    if (k >= m) break;
-                    float d = dv[k] + bias;
-                    if (a.softplus) d = softplus(d);
-                    const float u = d * xv[k];
-                    const float *row = s_bc[buf] + k * 2 * NP + l.n0;
-                    float b[NS];
-                    lds_row<NS>(row, b);
-                    if (!s.starts) {
-                        float c[NS];
-                        lds_row<NS>(row + NP, c);
-#pragma unroll
-                        for (int n = 0; n < NS; ++n) {
-                            const float decay = __builtin_amdgcn_exp2f(d * A2[n]);
-                            h[n] = fmaf(decay, h[n], u * b[n]);
-                            chain[n] *= decay;
-                            back[n] = fmaf(chain[n], c[n] * yv[k], back[n]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < NS; ++n)
-                            h[n] = fmaf(__builtin_amdgcn_exp2f(d * A2[n]), h[n], u * b[n]);
-                    }
-                    sum += d;
-                }
-                if (more) st.put(s_bc[buf ^ 1]);
-                __syncthreads();
-            }
         }
-        if (!s.starts && s.ends && a.dS_T) {
-            float g[NS];
-            load_state(a, l, a.dS_T, s.i, g);
+        int buf = 0;
+        for (int t = s.lo; t < s.hi; t += kB, buf ^= 1) {
+            float x[kB], d[kB], dy[kB];
+            widen(dr, d);
+            widen(xr, x);
+            widen(yr, dy);
+            if (a.gate)
 #pragma unroll
-            for (int n = 0; n < NS; ++n) back[n] = fmaf(chain[n], g[n], back[n]);
+                for (int k = 0; k < kB; ++k) dy[k] *= silu(io<T>::val(gr[k]));
+            const int m = s.hi - t;
+            if (m > kB) fetch(t + kB);
+#pragma unroll
+            for (int k = 0; k < kB; ++k) d[k] += bias;
+            if (a.softplus)
+#pragma unroll
+                for (int k = 0; k < kB; ++k) d[k] = softplus(d[k]);
+            if (m < kB)         // steps of zero: h and chain stay, and nothing comes back
+#pragma unroll
+                for (int k = 1; k < kB; ++k)
+                    if (k >= m) d[k] = x[k] = dy[k] = 0.f;
+            const float *bc = s_bc[buf] + l.n0;
+#pragma unroll
+            for (int k = 0; k < kB; ++k) {
+                float b[NS], cv[NS];
+                lds_row<NS>(bc + k * 2 * NP, b);
+                lds_row<NS>(bc + k * 2 * NP + NP, cv);
+                const float u = d[k] * x[k];
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    const float decay = __builtin_amdgcn_exp2f(d[k] * A2[n]);
+                    h[n] = fmaf(decay, h[n], u * b[n]);
+                    chain[n] *= decay;
+                    back[n] = fmaf(chain[n], cv[n] * dy[k], back[n]);
+                }
+                sum += d[k];
+            }
+            pin(h);
+            pin(chain);
+            pin(back);
+            if (m > kB) st.put(s_bc[buf ^ 1]);
+            __syncthreads();
+        }
+        if (!s.starts && s.ends) {
+            if (a.dS_T) {
+                float g[NS];
+                load_state(a, l, a.dS_T, s.i, g);
+#pragma unroll
+                for (int n = 0; n < NS; ++n) back[n] = fmaf(chain[n], g[n], back[n]);
+            }
         }
     });
     store_tile(a, l, a.tiles_h, tile, h);
     store_tile(a, l, a.tiles_g, tile, back);
-    if (l.on && l.part == 0) a.tiles_dt[tile * a.channels + l.c] = sum;
+    if (l.on && l.part == 0) a.tiles_dt[tile * a.channels + c] = sum;
     if (blockIdx.x == 0 && threadIdx.x == 0) a.tiles_pass[tile] = pass ? 1 : 0;
 }
 
@@ -204,191 +204,251 @@ __global__ __launch_bounds__(256) void scan_bwd_chain_kernel(ScanArgs a, int til
     else chain_tiles<-1>(a, a.tiles_g, tiles);
 }
 
-// Launch 3.
+// Launch 3. As in the forward, a group of kG tokens has no branch between its tokens: the ones
+// missing from a sequence's last group take steps of zero, with no input and no gradient.
 template <typename T, typename TG, int NS, int S>
-__global__ __launch_bounds__(256) void scan_bwd_kernel(ScanArgs a) {
+__global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
     using Lane = ScanLane<NS, S>;
-    constexpr int NP = Lane::NP, CW = Lane::CW, TOP = CW == 64 ? 5 : CW == 32 ? 4 : CW == 16 ? 3 : 2;
+    constexpr int NP = Lane::NP, CW = Lane::CW, TOP = __builtin_ctz(CW) - 1;
+    constexpr int LEFT = spread_left(CW, NS);
     extern __shared__ __align__(16) float lds[];
-    // B and C of the tile [tile][2][NP]; states every kG tokens [waves][groups][NS][64];
+    // B and C of the tile [groups * kG][2][NP]; states every kG tokens [waves][groups][NS][64];
     // the waves' dB and dC [waves][kG][2][NP]
-    float *s_bc = lds, *s_h = s_bc + a.tile * 2 * NP;
-    const int tile_groups = (a.tile + kG - 1) / kG;
-    float *s_red = s_h + kScanWaves * tile_groups * NS * 64;
+    const int groups_max = (a.tile + kG - 1) / kG;
+    float *s_bc = lds, *s_h = s_bc + groups_max * kG * 2 * NP;
+    float *s_red = s_h + kScanWaves * groups_max * NS * 64;
     const Lane l(a, blockIdx.x);
     const int lane = threadIdx.x & 63;
     const int64_t tile = tile_index();
     if (tile * a.tile >= a.map.total && tile > 0) return;      // the whole workgroup
     const int t0 = static_cast<int>(tile * a.tile);
     const int t1 = a.map.total - t0 < a.tile ? a.map.total : t0 + a.tile;
-    const T *x = static_cast<const T *>(a.x) + l.c, *dt = static_cast<const T *>(a.dt) + l.c;
-    const T *gate = a.gate ? static_cast<const T *>(a.gate) + l.c : nullptr;
-    const TG *dO = static_cast<const TG *>(a.dO) + l.c;
-    TG *dx = static_cast<TG *>(a.dx) + l.c, *ddt = static_cast<TG *>(a.ddt) + l.c;
-    TG *dgate = a.gate ? static_cast<TG *>(a.dgate) + l.c : nullptr;
-    float *my_h = s_h + l.wave * tile_groups * NS * 64 + lane;
-    float *my_red = s_red + l.wave * kG * 2 * NP;
+    const uint32_t c = l.c;
+    float *my_h = s_h + l.wave * groups_max * NS * 64 + lane;
     float A2[NS], dA[NS];
     load_rates(a, l, A2);
 #pragma unroll
     for (int n = 0; n < NS; ++n) dA[n] = 0.f;
-    const float bias = a.dt_bias ? a.dt_bias[l.c] : 0.f, skip = a.D ? a.D[l.c] : 0.f;
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.D ? a.D[c] : 0.f;
     float dD = 0.f, dbias = 0.f;
     bool writes;
-    const int red_n = l.n0 + spread_index<CW, NS>(&writes);
-    // inputs of a token; zero in lanes without a channel, so that they add nothing to any sum
-    auto in = [&](const T *p, int64_t at) { return l.on ? io<T>::ld(p + at) : 0.f; };
-    auto step = [&](float raw) { return a.softplus ? softplus(raw) : raw; };
+    float *my_red = s_red + l.wave * kG * 2 * NP + l.n0 + spread_index<CW, NS>(&writes);
+    const bool gated = a.gate != nullptr;
+    // the step sizes of a group, zero from m on and in lanes without a channel (which then add
+    // nothing to the sums over channels)
+    auto steps = [&](float (&d)[kG], int m) {
+        if (a.softplus)
+#pragma unroll
+            for (int k = 0; k < kG; ++k) d[k] = softplus(d[k]);
+        if (m < kG)
+#pragma unroll
+            for (int k = 1; k < kG; ++k)
+                if (k >= m) d[k] = 0.f;
+        if (!l.on)
+#pragma unroll
+            for (int k = 0; k < kG; ++k) d[k] = 0.f;
+    };
     for_spans(a.map, t0, t1, [&](const Span &s) {
         float h[NS], g[NS];        // g: the gradient that comes to h_t from behind, a_{t+1} gh_{t+1}
-        if (s.ends) {
-            if (a.dS_T) load_state(a, l, a.dS_T, s.i, g);
-            else
-#pragma unroll
-                for (int n = 0; n < NS; ++n) g[n] = 0.f;
-        } else {
+        if (!s.ends) {
             load_tile(a, l, a.tiles_g, tile, g);
-        }
-        if (s.starts) {
-            if (a.S0) load_state(a, l, a.S0, s.i, h);
-            else
-#pragma unroll
-                for (int n = 0; n < NS; ++n) h[n] = 0.f;
+        } else if (a.dS_T) {
+            load_state(a, l, a.dS_T, s.i, g);
         } else {
-            load_tile(a, l, a.tiles_h, tile, h);
+#pragma unroll
+            for (int n = 0; n < NS; ++n) g[n] = 0.f;
         }
-        const int len = s.hi - s.lo;
+        if (!s.starts) {
+            load_tile(a, l, a.tiles_h, tile, h);
+        } else if (a.S0) {
+            load_state(a, l, a.S0, s.i, h);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NS; ++n) h[n] = 0.f;
+        }
+        const int len = s.hi - s.lo, groups = (len + kG - 1) / kG;
         if (len > 0) {
             __syncthreads();       // the span before is done with s_bc
-            for (int e = threadIdx.x; e < len * 2 * NP; e += 256) {
+            for (int e = threadIdx.x; e < groups * kG * 2 * NP; e += 256) {
                 const int k = e / (2 * NP), j = e % (2 * NP), n = j % NP;
                 float v = 0.f;
-                if (n < a.d_state) {
-                    const bool c = j >= NP;
-                    const T *p = static_cast<const T *>(c ? a.C : a.B);
-                    v = io<T>::ld(p + (s.lo + k) * (c ? a.c_stride : a.b_stride) + l.g * a.d_state + n);
+                if (n < a.d_state && k < len) {
+                    const bool is_c = j >= NP;
+                    const T *p = static_cast<const T *>(is_c ? a.C : a.B);
+                    v = io<T>::ld(p + (s.lo + k) * (is_c ? a.c_stride : a.b_stride) + l.g * a.d_state + n);
                 }
                 s_bc[e] = v;
             }
             __syncthreads();
-            const int groups = (len + kG - 1) / kG;
-            // forward: the state entering every group of kG tokens
-            for (int q = 0; q < groups; ++q) {
+        }
+        // forward: the state entering every group of kG tokens
+        for (int q = 0; q < groups; ++q) {
 #pragma unroll
-                for (int n = 0; n < NS; ++n) my_h[(q * NS + n) * 64] = h[n];
-                if (q == groups - 1) break;
-                float xv[kG], dv[kG];
+            for (int n = 0; n < NS; ++n) my_h[(q * NS + n) * 64] = h[n];
+            if (q == groups - 1) break;
+            const int64_t t = s.lo + q * kG;
+            T xr[kG], dr[kG];
+            fetch_rows(static_cast<const T *>(a.dt) + t * a.dt_stride, a.dt_stride, c, kG, dr);
+            fetch_rows(static_cast<const T *>(a.x) + t * a.x_stride, a.x_stride, c, kG, xr);
+            float x[kG], d[kG];
+            widen(dr, d);
+            widen(xr, x);
 #pragma unroll
-                for (int k = 0; k < kG; ++k) {
-                    const int64_t t = s.lo + q * kG + k;
-                    xv[k] = in(x, t * a.x_stride);
-                    dv[k] = in(dt, t * a.dt_stride);
+            for (int k = 0; k < kG; ++k) d[k] += bias;
+            steps(d, kG);
+            const float *bc = s_bc + q * kG * 2 * NP + l.n0;
+#pragma unroll
+            for (int k = 0; k < kG; ++k) {
+                const float u = d[k] * x[k];
+                float b[NS];
+                lds_row<NS>(bc + k * 2 * NP, b);
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    h[n] = fmaf(__builtin_amdgcn_exp2f(d[k] * A2[n]), h[n], u * b[n]);
+            }
+            pin(h);
+        }
+        // back, group by group
+        for (int q = groups - 1; q >= 0; --q) {
+            const int m = len - q * kG < kG ? len - q * kG : kG;
+            const int64_t t = s.lo + q * kG;
+            T xr[kG], dr[kG], gr[kG];
+            TG yr[kG];
+            fetch_rows(static_cast<const T *>(a.dt) + t * a.dt_stride, a.dt_stride, c, m, dr);
+            fetch_rows(static_cast<const T *>(a.x) + t * a.x_stride, a.x_stride, c, m, xr);
+            fetch_rows(static_cast<const TG *>(a.dO) + t * a.channels, a.channels, c, m, yr);
+            if (gated) fetch_rows(static_cast<const T *>(a.gate) + t * a.gate_stride, a.gate_stride, c, m, gr);
+            float x[kG], d[kG], raw[kG], gt[kG], go[kG], hist[kG][NS], rb[kG][LEFT], rc[kG][LEFT];
+            widen(dr, d);
+            widen(xr, x);
+            widen(yr, go);
+            if (gated) widen(gr, gt);
+#pragma unroll
+            for (int k = 0; k < kG; ++k) raw[k] = d[k] += bias;
+            steps(d, m);
+            if (m < kG || !l.on)
+#pragma unroll
+                for (int k = 0; k < kG; ++k)
+                    if (k >= m || !l.on) x[k] = go[k] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NS; ++n) h[n] = my_h[(q * NS + n) * 64];
+            const float *bc = s_bc + q * kG * 2 * NP + l.n0;
+#pragma unroll
+            for (int k = 0; k < kG; ++k) {
+                const float u = d[k] * x[k];
+                float b[NS];
+                lds_row<NS>(bc + k * 2 * NP, b);
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    // kept: a_t h_{t-1}, from which h_t follows by one operation
+                    hist[k][n] = __builtin_amdgcn_exp2f(d[k] * A2[n]) * h[n];
+                    h[n] = fmaf(u, b[n], hist[k][n]);
                 }
+                pin(hist[k]);
+            }
+            pin(d);        // the decays are formed again below: kept, they would take kG * NS registers
+#pragma unroll
+            for (int k = kG - 1; k >= 0; --k) {
+                // what is kept of the group's tokens takes most registers, so the two products
+                // that are summed over channels are formed one after the other
+                const float u = d[k] * x[k];
+                float sg = 1.f, dy = go[k];
+                if (gated) {
+                    sg = sigmoid_hw(gt[k]);
+                    dy *= gt[k] * sg;
+                }
+                float y = 0.f, sB = 0.f, sA = 0.f;
+                {
+                    float b[NS], cv[NS], p[NS];
+                    lds_row<NS>(bc + k * 2 * NP, b);
+                    lds_row<NS>(bc + k * 2 * NP + NP, cv);
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) {
+                        const float ht = fmaf(u, b[n], hist[k][n]);
+                        y = fmaf(cv[n], ht, y);
+                        p[n] = dy * ht;
+                        g[n] = fmaf(cv[n], dy, g[n]);        // gh_t
+                        sB = fmaf(g[n], b[n], sB);
+                    }
+                    reduce_spread<TOP, NS>(p);
+#pragma unroll
+                    for (int i = 0; i < LEFT; ++i) rc[k][i] = p[i];
+                }
+                {
+                    float p[NS];
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) {
+                        p[n] = g[n] * u;
+                        const float r = g[n] * hist[k][n];
+                        sA = fmaf(r, A2[n], sA);
+                        dA[n] = fmaf(r, d[k], dA[n]);
+                        g[n] *= __builtin_amdgcn_exp2f(d[k] * A2[n]);
+                    }
+                    reduce_spread<TOP, NS>(p);
+#pragma unroll
+                    for (int i = 0; i < LEFT; ++i) rb[k][i] = p[i];
+                }
+                sB = sum_parts<S>(sB);
+                float dd = fmaf(x[k], sB, sum_parts<S>(sA) * (1.f / kLog2e));
+                if (a.softplus) dd *= sigmoid_hw(raw[k]);
+                dD = fmaf(dy, x[k], dD);
+                dbias += k < m ? dd : 0.f;
+                if (gated) {        // dgate, dx and ddt take the places of gate, dO and raw
+                    y = fmaf(skip, x[k], sum_parts<S>(y));
+                    gt[k] = go[k] * y * (sg * fmaf(gt[k], 1.f - sg, 1.f));
+                }
+                go[k] = fmaf(skip, dy, d[k] * sB);
+                raw[k] = dd;
+                float out[5] = {go[k], raw[k], gated ? gt[k] : 0.f, dD, dbias};
+                pin(out);
+                go[k] = out[0];
+                raw[k] = out[1];
+                gt[k] = out[2];
+                dD = out[3];
+                dbias = out[4];
+                pin(g);
+                pin(dA);
+                pin(rb[k]);
+                pin(rc[k]);
+            }
+            if (l.on && l.part == 0) {
+                TG *px = static_cast<TG *>(a.dx) + t * a.channels, *pd = static_cast<TG *>(a.ddt) + t * a.channels;
 #pragma unroll
                 for (int k = 0; k < kG; ++k) {
-                    const float d = l.on ? step(dv[k] + bias) : 0.f, u = d * xv[k];
-                    float b[NS];
-                    lds_row<NS>(s_bc + (q * kG + k) * 2 * NP + l.n0, b);
+                    if (k < m) {
+                        io<TG>::st(elem(px, c), go[k]);
+                        io<TG>::st(elem(pd, c), raw[k]);
+                    }
+                    px += a.channels;
+                    pd += a.channels;
+                }
+                if (gated) {
+                    TG *pg = static_cast<TG *>(a.dgate) + t * a.channels;
 #pragma unroll
-                    for (int n = 0; n < NS; ++n)
-                        h[n] = fmaf(__builtin_amdgcn_exp2f(d * A2[n]), h[n], u * b[n]);
+                    for (int k = 0; k < kG; ++k) {
+                        if (k < m) io<TG>::st(elem(pg, c), gt[k]);
+                        pg += a.channels;
+                    }
                 }
             }
-            // back, group by group
-            for (int q = groups - 1; q >= 0; --q) {
-                const int m = len - q * kG < kG ? len - q * kG : kG;
-                float xv[kG], dv[kG], rv[kG], gv[kG], yv[kG], hist[kG][NS];
+            __syncthreads();       // the group behind is done with s_red
+            if (writes)
 #pragma unroll
-                for (int k = 0; k < kG; ++k) {
-                    xv[k] = dv[k] = gv[k] = yv[k] = 0.f;
-                    if (k < m) {
-                        const int64_t t = s.lo + q * kG + k;
-                        xv[k] = in(x, t * a.x_stride);
-                        dv[k] = in(dt, t * a.dt_stride);
-                        if (l.on) yv[k] = io<TG>::ld(dO + t * a.channels);
-                        if (gate) gv[k] = in(gate, t * a.gate_stride);
+                for (int k = 0; k < kG; ++k)
+#pragma unroll
+                    for (int i = 0; i < LEFT; ++i) {
+                        my_red[k * 2 * NP + i] = rb[k][i];
+                        my_red[k * 2 * NP + NP + i] = rc[k][i];
                     }
-                }
+            __syncthreads();
+            // the waves' shares of dB and dC, added in their order
+            for (int e = threadIdx.x; e < m * 2 * NP; e += 256) {
+                const int k = e / (2 * NP), j = e % (2 * NP), n = j % NP;
+                if (n >= a.d_state) continue;
+                float v = 0.f;
 #pragma unroll
-                for (int n = 0; n < NS; ++n) h[n] = my_h[(q * NS + n) * 64];
-#pragma unroll
-                for (int k = 0; k < kG; ++k) {
-                    rv[k] = dv[k] + bias;
-                    dv[k] = l.on ? step(rv[k]) : 0.f;
-                    if (k >= m) break;
-                    const float u = dv[k] * xv[k];
-                    const float *row = s_bc + (q * kG + k) * 2 * NP + l.n0;
-                    float b[NS];
-                    lds_row<NS>(row, b);
-#pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        // kept: a_t h_{t-1}, from which h_t follows by one operation
-                        hist[k][n] = __builtin_amdgcn_exp2f(dv[k] * A2[n]) * h[n];
-                        h[n] = fmaf(u, b[n], hist[k][n]);
-                    }
-                }
-                __syncthreads();       // the group behind is done with s_red
-#pragma unroll
-                for (int k = kG - 1; k >= 0; --k) {
-                    if (k >= m) continue;
-                    const int64_t t = s.lo + q * kG + k;
-                    const float d = dv[k], u = d * xv[k];
-                    const float *row = s_bc + (q * kG + k) * 2 * NP + l.n0;
-                    float b[NS], c[NS];
-                    lds_row<NS>(row, b);
-                    lds_row<NS>(row + NP, c);
-                    const float sg = gate ? sigmoid_hw(gv[k]) : 1.f;
-                    const float dy = gate ? yv[k] * (gv[k] * sg) : yv[k];
-                    float y = 0.f, sB = 0.f, sA = 0.f, pb[NS], pc[NS];
-#pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        const float ah = hist[k][n], ht = fmaf(u, b[n], ah);
-                        y = fmaf(c[n], ht, y);
-                        pc[n] = dy * ht;
-                        const float gh = fmaf(c[n], dy, g[n]);
-                        pb[n] = gh * u;
-                        sB = fmaf(gh, b[n], sB);
-                        const float r = gh * ah;
-                        sA = fmaf(r, A2[n], sA);
-                        dA[n] = fmaf(r, d, dA[n]);
-                        g[n] = __builtin_amdgcn_exp2f(d * A2[n]) * gh;
-                    }
-                    reduce_spread<TOP, NS>(pb);
-                    reduce_spread<TOP, NS>(pc);
-                    if (writes)
-#pragma unroll
-                        for (int i = 0; i < spread_left(CW, NS); ++i) {
-                            my_red[k * 2 * NP + red_n + i] = pb[i];
-                            my_red[k * 2 * NP + NP + red_n + i] = pc[i];
-                        }
-                    sB = sum_parts<S>(sB);
-                    sA = sum_parts<S>(sA);
-                    if (gate) {
-                        y = fmaf(skip, xv[k], sum_parts<S>(y));
-                        if (l.on && l.part == 0)
-                            io<TG>::st(dgate + t * a.channels,
-                                       yv[k] * y * (sg * fmaf(gv[k], 1.f - sg, 1.f)));
-                    }
-                    float dd = fmaf(xv[k], sB, sA * (1.f / kLog2e));
-                    if (a.softplus) dd *= sigmoid_hw(rv[k]);
-                    dD = fmaf(dy, xv[k], dD);
-                    dbias += dd;
-                    if (l.on && l.part == 0) {
-                        io<TG>::st(dx + t * a.channels, fmaf(skip, dy, d * sB));
-                        io<TG>::st(ddt + t * a.channels, dd);
-                    }
-                }
-                __syncthreads();
-                // the waves' shares of dB and dC, added in their order
-                for (int e = threadIdx.x; e < m * 2 * NP; e += 256) {
-                    const int k = e / (2 * NP), j = e % (2 * NP), n = j % NP;
-                    if (n >= a.d_state) continue;
-                    float v = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kScanWaves; ++w) v += s_red[w * kG * 2 * NP + e];
-                    const int64_t t = s.lo + q * kG + k;
-                    a.part_bc[((static_cast<int64_t>(blockIdx.x) * a.map.total + t) * 2 + (j >= NP)) * a.d_state + n] = v;
-                }
+                for (int w = 0; w < kScanWaves; ++w) v += s_red[w * kG * 2 * NP + e];
+                a.part_bc[((static_cast<int64_t>(blockIdx.x) * a.map.total + t + k) * 2 + (j >= NP)) * a.d_state + n] = v;
             }
         }
         if (s.starts && a.dS0) store_state(a, l, a.dS0, s.i, g);
@@ -396,8 +456,8 @@ __global__ __launch_bounds__(256) void scan_bwd_kernel(ScanArgs a) {
     // the tile's sums for dA, dD and ddt_bias, where its state and sum of dt were
     store_tile(a, l, a.tiles_h, tile, dA);
     if (l.on && l.part == 0) {
-        a.tiles_dt[tile * a.channels + l.c] = dD;
-        a.tiles_db[tile * a.channels + l.c] = dbias;
+        a.tiles_dt[tile * a.channels + c] = dD;
+        a.tiles_db[tile * a.channels + c] = dbias;
     }
 }
 
@@ -415,6 +475,7 @@ __global__ __launch_bounds__(256) void scan_bwd_params_kernel(ScanArgs a, int ti
     else if (col < cols + 2 * a.channels) p = a.ddt_bias ? a.tiles_db + (col - cols - a.channels) : nullptr;
     float sum = 0.f;
     if (p)
+#pragma unroll 8
         for (int i = wave; i < tiles; i += 4) sum += p[i * step];
     s[wave][lane] = sum;
     __syncthreads();
@@ -460,8 +521,8 @@ hipError_t launch_bwd(const ScanArgs &a, hipStream_t st) {
         hipLaunchKernelGGL(scan_bwd_chain_kernel, dim3(static_cast<unsigned>((cols + 255) / 256), 2),
                            dim3(256), 0, st, a, tiles);
     }
-    const size_t lds = sizeof(float) * (static_cast<size_t>(a.tile) * 2 * NS * S +
-                                        kScanWaves * ((a.tile + kG - 1) / kG) * NS * 64 +
+    const size_t groups = (a.tile + kG - 1) / kG;
+    const size_t lds = sizeof(float) * (groups * kG * 2 * NS * S + kScanWaves * groups * NS * 64 +
                                         kScanWaves * kG * 2 * NS * S);
     static_assert(kScanMaxBwdTile % kG == 0, "whole groups of tokens in a tile");
     static_assert(sizeof(float) * (kScanMaxBwdTile * 2 * NS * S + kScanWaves * (kScanMaxBwdTile / kG) * NS * 64 +
@@ -485,22 +546,31 @@ hipError_t launch_bwd(const ScanArgs &a, hipStream_t st) {
 
 template <typename T, typename TG>
 hipError_t launch_bwd_t(const ScanArgs &a, hipStream_t st) {
-    switch (scan_parts(a.d_state)) {
-    case 1: return a.d_state <= 8 ? launch_bwd<T, TG, 8, 1>(a, st) : launch_bwd<T, TG, 16, 1>(a, st);
-    case 2: return launch_bwd<T, TG, 16, 2>(a, st);
-    case 4: return launch_bwd<T, TG, 16, 4>(a, st);
-    default: return launch_bwd<T, TG, 16, 8>(a, st);
+    switch (scan_bwd_parts(a.d_state)) {
+    case 1: return launch_bwd<T, TG, 8, 1>(a, st);
+    case 2: return launch_bwd<T, TG, 8, 2>(a, st);
+    case 4: return launch_bwd<T, TG, 8, 4>(a, st);
+    case 8: return launch_bwd<T, TG, 8, 8>(a, st);
+    default: return launch_bwd<T, TG, 8, 16>(a, st);
     }
 }
 
 }  // namespace
+
+// Eight states per lane: a group's kept states are 64 registers, so that two waves fit a SIMD
+// without spilling. Sixteen, as in the forward, need 350: on 4,096 tokens x 2,048 channels x 16
+// states 209.6 us at one wave per SIMD against 197.6 us, although a channel's step, gate and
+// loads are then done by twice the lanes.
+int scan_bwd_parts(int d_state) {
+    return d_state <= 8 ? 1 : d_state <= 16 ? 2 : d_state <= 32 ? 4 : d_state <= 64 ? 8 : 16;
+}
 
 // Tokens per tile: whole sequences where they are short enough, else about 2,048 waves, between
 // 8 tokens and what LDS holds.
 int scan_bwd_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed) {
     if (!packed && seqlen <= kScanMaxBwdTile) return seqlen > 0 ? seqlen : 1;
     const int64_t total = static_cast<int64_t>(batch) * seqlen;
-    const int64_t waves = static_cast<int64_t>(kScanWaves) * scan_blocks(channels, groups, scan_parts(d_state));
+    const int64_t waves = static_cast<int64_t>(kScanWaves) * scan_blocks(channels, groups, scan_bwd_parts(d_state));
     const int64_t t = (total * waves / 2048 + kG - 1) / kG * kG;
     return t < kG ? kG : t > kScanMaxBwdTile ? kScanMaxBwdTile : static_cast<int>(t);
 }
