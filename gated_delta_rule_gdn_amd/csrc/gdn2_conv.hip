@@ -8,7 +8,9 @@
 // The same sum at the W - 1 positions before the sequence is the gradient of the conv state.
 //
 // All three are bound by memory: 2 W operations per element against 2 or 3 element accesses. A
-// lane owns V neighbouring channels (16 bytes of x) and walks a tile of tokens with the last
+// lane owns V neighbouring channels (4 forward, where 8 left too few waves: 28 against 22 us on
+// 4,096 tokens x 6,144 bf16 channels; 2 backward, where 4 take 200 registers and two waves per
+// SIMD hide neither memory nor arithmetic: 52 against 39 us) and walks a tile of tokens with the last
 // W - 1 inputs (and, backward, the last W values of e) in registers, so every element is read
 // from memory once; only the W - 1 rows next to a tile are read again by its neighbour. Tiles cut
 // the token axis without regard to sequences: a wave walks the sequences inside its tile, so the
@@ -27,7 +29,7 @@ constexpr int kBatch = 4;    // rows whose loads are in flight together
 // The W - 1 inputs before token t of a span, oldest first.
 template <typename T, int W, int V>
 __device__ __forceinline__ void load_history(const ConvArgs &a, const T *x, const Span &s, int t,
-                                             int c, float (&h)[W - 1][V]) {
+                                             uint32_t c, float (&h)[W - 1][V]) {
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {
         const int at = t - (W - 1) + r;
@@ -64,7 +66,7 @@ __device__ __forceinline__ void load_taps(const float *weight, const float *bias
     if (bias) ldv<float, V>(bias + c, b);
 }
 
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t0l = (static_cast<int64_t>(blockIdx.y) * 4 + wave) * a.tile;
@@ -73,14 +75,12 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
     const int t1 = a.map.total - t0 < a.tile ? a.map.total : t0 + a.tile;
     const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63)) * V;
     const bool on = c0 < a.channels;
-    const int c = on ? static_cast<int>(c0) : 0;
+    const uint32_t c = on ? static_cast<uint32_t>(c0) : 0;
     const T *x = static_cast<const T *>(a.x);
-    T *y = static_cast<T *>(a.y);
     float w[W][V], bias[V];
     load_taps<W, V>(a.weight, a.bias, c, w, bias);
     for_spans(a.map, t0, t1, [&](const Span &s) {
-        if (!on) return;
-        float h[W - 1 + kBatch][V];
+        float h[W - 1 + kBatch][V];      // the last W - 1 inputs, then a batch of new ones
         {
             float old[W - 1][V];
             load_history<T, W, V>(a, x, s, s.lo, c, old);
@@ -89,36 +89,43 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) h[r][v] = old[r][v];
         }
-        const T *px = x + s.lo * a.x_stride + c;
-        T *py = y + static_cast<int64_t>(s.lo) * a.channels + c;
-        // n tokens: their rows follow the W - 1 inputs in h, which then moves on by n rows
-        auto step = [&](auto n) {
-            constexpr int K = decltype(n)::value;
+        Raw<T, V> raw[kBatch];
+        if (s.lo < s.hi) load_rows(x + s.lo * a.x_stride, a.x_stride, c, s.hi - s.lo, raw);
+        for (int t = s.lo; t < s.hi; t += kBatch) {
+            const int m = s.hi - t;
 #pragma unroll
-            for (int k = 0; k < K; ++k) ldv<T, V>(px + k * a.x_stride, h[W - 1 + k]);
+            for (int k = 0; k < kBatch; ++k) raw[k].get(h[W - 1 + k]);
+            if (m > kBatch) load_rows(x + (t + kBatch) * a.x_stride, a.x_stride, c, m - kBatch, raw);
+            T *row = static_cast<T *>(a.y) + static_cast<int64_t>(t) * a.channels;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
+            for (int k = 0; k < kBatch; ++k) {
                 float o[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     float acc = bias[v];
 #pragma unroll
                     for (int j = 0; j < W; ++j) acc = fmaf(w[j][v], h[k + j][v], acc);
-                    o[v] = a.silu ? silu(acc) : acc;
+                    o[v] = SILU ? silu(acc) : acc;
                 }
-                stv<T, V>(py + k * static_cast<int64_t>(a.channels), o);
+                if (k < m && on) stv<T, V>(elem(row, c), o);
+                row += a.channels;
+            }
+            // the last W - 1 inputs move to the front
+            if (m < kBatch) {
+#pragma unroll
+                for (int r = 0; r < W - 1; ++r)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+#pragma unroll
+                        for (int q = 1; q < kBatch; ++q) h[r][v] = m == q ? h[r + q][v] : h[r][v];
+                break;
             }
 #pragma unroll
             for (int r = 0; r < W - 1; ++r)
 #pragma unroll
-                for (int v = 0; v < V; ++v) h[r][v] = h[r + K][v];
-            px += K * a.x_stride;
-            py += K * static_cast<int64_t>(a.channels);
-        };
-        int t = s.lo;
-        for (; t + kBatch <= s.hi; t += kBatch) step(std::integral_constant<int, kBatch>{});
-        for (; t < s.hi; ++t) step(std::integral_constant<int, 1>{});
-        if (s.ends && a.state_T) {
+                for (int v = 0; v < V; ++v) h[r][v] = h[r + kBatch][v];
+        }
+        if (s.ends && a.state_T && on) {
             float *st = a.state_T + static_cast<int64_t>(s.i) * (W - 1) * a.channels + c;
 #pragma unroll
             for (int r = 0; r < W - 1; ++r)
@@ -129,7 +136,9 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a) {
 
 // One tile's dx (and dstate0), and its partial sums of dweight and dbias. The wave walks the
 // tile's tokens and W - 1 more, forming e_t once per token, and writes dx W - 1 tokens behind.
-template <typename T, typename TG, int W, int V>
+// Batches inside a sequence, nearly all of a long one, take a path without the conditions of its
+// ends.
+template <typename T, typename TG, int W, int V, bool SILU>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t tile = static_cast<int64_t>(blockIdx.y) * 4 + wave;
@@ -139,10 +148,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a) {
     const int t1 = a.map.total - t0 < a.tile ? a.map.total : t0 + a.tile;
     const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x & 63)) * V;
     const bool on = c0 < a.channels;
-    const int c = on ? static_cast<int>(c0) : 0;
+    const uint32_t c = on ? static_cast<uint32_t>(c0) : 0;
     const T *x = static_cast<const T *>(a.x);
     const TG *dy = static_cast<const TG *>(a.dy);
-    TG *dx = static_cast<TG *>(a.dx);
     float w[W][V], bias[V], dw[W][V], db[V];
     load_taps<W, V>(a.weight, a.bias, c, w, bias);
 #pragma unroll
@@ -152,85 +160,93 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a) {
         for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
     }
     for_spans(a.map, t0, t1, [&](const Span &s) {
-        if (!on) return;
-        float h[W][V], e[W][V];      // the last W inputs (newest last) and the last W of e
+        // the last W - 1 inputs and values of e, then a batch of new ones
+        float h[W - 1 + kBatch][V], e[W - 1 + kBatch][V];
         {
             float old[W - 1][V];
             load_history<T, W, V>(a, x, s, s.lo, c, old);
 #pragma unroll
             for (int r = 0; r < W - 1; ++r)
 #pragma unroll
-                for (int v = 0; v < V; ++v) h[r + 1][v] = old[r][v];
+                for (int v = 0; v < V; ++v) { h[r][v] = old[r][v]; e[r][v] = 0.f; }
         }
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) e[j][v] = 0.f;
         const int last = s.hi + W - 1;       // one past the last step; e = 0 from s.end on
-        for (int t = s.lo; t < last; t += kBatch) {
-            float xn[kBatch][V], gn[kBatch][V];
+        Raw<T, V> rx[kBatch];
+        Raw<TG, V> rg[kBatch];
+        auto fetch = [&](int t) {
+            if (t >= s.end || t >= last) return;
+            load_rows(x + t * a.x_stride, a.x_stride, c, s.end - t, rx);
+            load_rows(dy + static_cast<int64_t>(t) * a.channels, a.channels, c, s.end - t, rg);
+        };
+        auto batch = [&](auto inner, int t) {
+            constexpr bool INNER = decltype(inner)::value;
+            float g[kBatch][V];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (t + k < last && t + k < s.end) {
-                    ldv<T, V>(x + (t + k) * a.x_stride + c, xn[k]);
-                    ldv<TG, V>(dy + static_cast<int64_t>(t + k) * a.channels + c, gn[k]);
-                }
+            for (int k = 0; k < kBatch; ++k) {
+                rx[k].get(h[W - 1 + k]);
+                rg[k].get(g[k]);
+            }
+            if (t + kBatch < last) fetch(t + kBatch);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int tk = t + k;
-                if (tk >= last) break;
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
+                for (int v = 0; v < V; ++v) {
+                    float ek = g[k][v];
+                    if (SILU) {
+                        float acc = bias[v];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) { h[j][v] = h[j + 1][v]; e[j][v] = e[j + 1][v]; }
-                if (tk < s.end) {
+                        for (int j = 0; j < W; ++j) acc = fmaf(w[j][v], h[k + j][v], acc);
+                        ek *= silu_slope(acc);
+                    }
+                    e[W - 1 + k][v] = INNER || tk < s.end ? ek : 0.f;
+                }
+                if (tk < s.hi)               // each token counts in one tile
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        h[W - 1][v] = xn[k][v];
-                        float g = gn[k][v];
-                        if (a.silu) {
-                            float acc = bias[v];
+                        db[v] += e[W - 1 + k][v];
 #pragma unroll
-                            for (int j = 0; j < W; ++j) acc = fmaf(w[j][v], h[j][v], acc);
-                            g *= silu_slope(acc);
-                        }
-                        e[W - 1][v] = g;
+                        for (int j = 0; j < W; ++j) dw[j][v] = fmaf(e[W - 1 + k][v], h[k + j][v], dw[j][v]);
                     }
-                    if (tk < s.hi) {         // each token counts in one tile
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            db[v] += e[W - 1][v];
-#pragma unroll
-                            for (int j = 0; j < W; ++j) dw[j][v] = fmaf(e[W - 1][v], h[j][v], dw[j][v]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) e[W - 1][v] = 0.f;
-                }
-                const int at = tk - (W - 1);             // the token whose gradient is whole now
-                const bool before = at < s.first;        // a row of the conv state
-                if (before ? !(s.starts && a.dstate0) : at < s.lo) continue;
                 float o[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     o[v] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < W; ++j) o[v] = fmaf(w[j][v], e[W - 1 - j][v], o[v]);
+                    for (int j = 0; j < W; ++j) o[v] = fmaf(w[j][v], e[W - 1 + k - j][v], o[v]);
                 }
-                const int r = at - (s.end - (W - 1));    // the row of state_T that is this input
-                if (a.dstate_T && r >= 0) {
-                    float g[V];
-                    ldv<float, V>(a.dstate_T + (static_cast<int64_t>(s.i) * (W - 1) + r) * a.channels + c, g);
+                const int at = tk - (W - 1);             // the token whose gradient is whole now
+                if constexpr (INNER) {
+                    if (at < s.lo || at >= s.hi) continue;
+                } else {
+                    if (tk >= last) continue;
+                    const bool before = at < s.first;    // a row of the conv state
+                    if (before ? !(s.starts && a.dstate0) : at < s.lo) continue;
+                    const int r = at - (s.end - (W - 1));     // the row of state_T that is this input
+                    if (a.dstate_T && r >= 0) {
+                        float d[V];
+                        ldv<float, V>(a.dstate_T + (static_cast<int64_t>(s.i) * (W - 1) + r) * a.channels + c, d);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) o[v] += g[v];
+                        for (int v = 0; v < V; ++v) o[v] += d[v];
+                    }
+                    if (before) {
+                        const int64_t row = static_cast<int64_t>(s.i) * (W - 1) + (at - s.first + W - 1);
+                        if (on) stv<float, V>(a.dstate0 + row * a.channels + c, o);
+                        continue;
+                    }
                 }
-                if (before)
-                    stv<float, V>(a.dstate0 + (static_cast<int64_t>(s.i) * (W - 1) + (at - s.first + W - 1)) *
-                                                  a.channels + c, o);
-                else
-                    stv<TG, V>(dx + static_cast<int64_t>(at) * a.channels + c, o);
+                if (on) stv<TG, V>(elem(static_cast<TG *>(a.dx) + static_cast<int64_t>(at) * a.channels, c), o);
             }
+#pragma unroll
+            for (int r = 0; r < W - 1; ++r)
+#pragma unroll
+                for (int v = 0; v < V; ++v) { h[r][v] = h[r + kBatch][v]; e[r][v] = e[r + kBatch][v]; }
+        };
+        fetch(s.lo);
+        for (int t = s.lo; t < last; t += kBatch) {
+            const bool rows = s.starts && a.dstate0 && t - (W - 1) < s.first;    // of the conv state
+            if (t + kBatch <= s.end && !rows) batch(std::true_type{}, t);
+            else batch(std::false_type{}, t);
         }
     });
     if (!on) return;
@@ -251,6 +267,7 @@ __global__ __launch_bounds__(1024) void conv_reduce_kernel(const float *part, in
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
     float sum = 0.f;
     if (col < cols)
+#pragma unroll 4
         for (int i = wave; i < tiles; i += 16) sum += part[i * cols + col];
     s[wave][lane] = sum;
     __syncthreads();
@@ -265,7 +282,7 @@ __global__ __launch_bounds__(1024) void conv_reduce_kernel(const float *part, in
 
 // T tokens of every sequence against its slot of the pool: one lane per sequence and V channels,
 // the state row read once and written once. A slot index outside the pool marks padding.
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
     const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
     if (c0 >= a.channels) return;
@@ -292,7 +309,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
                 float acc = bias[v];
 #pragma unroll
                 for (int j = 0; j < W; ++j) acc = fmaf(w[j][v], h[j][v], acc);
-                o[v] = a.silu ? silu(acc) : acc;
+                o[v] = SILU ? silu(acc) : acc;
             }
             stv<T, V>(y + static_cast<int64_t>(t) * a.channels, o);
 #pragma unroll
@@ -321,26 +338,36 @@ dim3 tile_grid(const ConvArgs &a, int V) {
                 static_cast<unsigned>((tiles + 3) / 4));
 }
 
-template <typename T, int V>
-hipError_t launch_fwd(const ConvArgs &a, hipStream_t st) {
+template <typename T, int V, bool SILU>
+hipError_t launch_fwd_s(const ConvArgs &a, hipStream_t st) {
     const dim3 grid = tile_grid(a, V);
     switch (a.width) {
-    case 2: hipLaunchKernelGGL((conv_fwd_kernel<T, 2, V>), grid, dim3(256), 0, st, a); break;
-    case 3: hipLaunchKernelGGL((conv_fwd_kernel<T, 3, V>), grid, dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((conv_fwd_kernel<T, 4, V>), grid, dim3(256), 0, st, a); break;
+    case 2: hipLaunchKernelGGL((conv_fwd_kernel<T, 2, V, SILU>), grid, dim3(256), 0, st, a); break;
+    case 3: hipLaunchKernelGGL((conv_fwd_kernel<T, 3, V, SILU>), grid, dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((conv_fwd_kernel<T, 4, V, SILU>), grid, dim3(256), 0, st, a); break;
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t launch_fwd(const ConvArgs &a, hipStream_t st) {
+    return a.silu ? launch_fwd_s<T, V, true>(a, st) : launch_fwd_s<T, V, false>(a, st);
+}
+
+template <typename T, typename TG, int V, bool SILU>
+hipError_t launch_bwd_s(const ConvArgs &a, hipStream_t st) {
+    const dim3 grid = tile_grid(a, V);
+    switch (a.width) {
+    case 2: hipLaunchKernelGGL((conv_bwd_kernel<T, TG, 2, V, SILU>), grid, dim3(256), 0, st, a); break;
+    case 3: hipLaunchKernelGGL((conv_bwd_kernel<T, TG, 3, V, SILU>), grid, dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((conv_bwd_kernel<T, TG, 4, V, SILU>), grid, dim3(256), 0, st, a); break;
     }
     return hipGetLastError();
 }
 
 template <typename T, typename TG, int V>
 hipError_t launch_bwd(const ConvArgs &a, hipStream_t st) {
-    const dim3 grid = tile_grid(a, V);
-    switch (a.width) {
-    case 2: hipLaunchKernelGGL((conv_bwd_kernel<T, TG, 2, V>), grid, dim3(256), 0, st, a); break;
-    case 3: hipLaunchKernelGGL((conv_bwd_kernel<T, TG, 3, V>), grid, dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((conv_bwd_kernel<T, TG, 4, V>), grid, dim3(256), 0, st, a); break;
-    }
-    hipError_t e = hipGetLastError();
+    const hipError_t e = a.silu ? launch_bwd_s<T, TG, V, true>(a, st) : launch_bwd_s<T, TG, V, false>(a, st);
     if (e != hipSuccess) return e;
     const int64_t cols = static_cast<int64_t>(a.channels) * (a.width + 1);
     hipLaunchKernelGGL(conv_reduce_kernel, dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(1024),
@@ -349,25 +376,33 @@ hipError_t launch_bwd(const ConvArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <typename T, int V>
-hipError_t launch_step(const ConvStepArgs &a, hipStream_t st) {
+template <typename T, int V, bool SILU>
+hipError_t launch_step_s(const ConvStepArgs &a, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>((a.channels + 256 * V - 1) / (256 * V)),
                     static_cast<unsigned>(a.num_seqs < 65535 ? a.num_seqs : 65535));
     switch (a.width) {
-    case 2: hipLaunchKernelGGL((conv_step_kernel<T, 2, V>), grid, dim3(256), 0, st, a); break;
-    case 3: hipLaunchKernelGGL((conv_step_kernel<T, 3, V>), grid, dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((conv_step_kernel<T, 4, V>), grid, dim3(256), 0, st, a); break;
+    case 2: hipLaunchKernelGGL((conv_step_kernel<T, 2, V, SILU>), grid, dim3(256), 0, st, a); break;
+    case 3: hipLaunchKernelGGL((conv_step_kernel<T, 3, V, SILU>), grid, dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL((conv_step_kernel<T, 4, V, SILU>), grid, dim3(256), 0, st, a); break;
     }
     return hipGetLastError();
 }
 
+template <typename T, int V>
+hipError_t launch_step(const ConvStepArgs &a, hipStream_t st) {
+    return a.silu ? launch_step_s<T, V, true>(a, st) : launch_step_s<T, V, false>(a, st);
+}
+
 }  // namespace
 
-// Tokens per tile: about 2,048 waves of 512 channels (two per SIMD), between 8 tokens, where the
-// neighbouring rows are nearly half of what a wave reads, and 64.
-int conv_tile(int64_t tokens, int channels) {
-    const int64_t waves = (static_cast<int64_t>(channels) + 511) / 512;
-    int64_t t = (tokens * waves / 2048 + 3) / 4 * 4;
+// Tokens per tile: about 6,144 waves of the forward's 256 channels or 3,072 of the backward's 128
+// (six and three per SIMD), and at least 8 tokens, where the rows next to a tile are nearly half
+// of what a wave reads. On 4,096 tokens x 6,144 channels: 16 tokens forward (21.1 us; 24 tokens
+// 22.0, 48 tokens 25.4), 64 backward (39.0 us; 24 tokens 45.0).
+int conv_tile(int64_t tokens, int channels, bool backward) {
+    const int per = backward ? 128 : 256;
+    const int64_t waves = (static_cast<int64_t>(channels) + per - 1) / per;
+    int64_t t = (tokens * waves / (backward ? 3072 : 6144) + kBatch - 1) / kBatch * kBatch;
     if (t < 8) t = 8;
     if (t > 64) t = 64;
     // the grid's second dimension holds at most 65,535 workgroups of four tiles
@@ -381,16 +416,16 @@ int64_t conv_tiles(int64_t tokens, int tile) {
 }
 
 hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t st) {
-    if (a.bf16) return vector_ok(a, 8) ? launch_fwd<bf16_t, 8>(a, st) : launch_fwd<bf16_t, 1>(a, st);
+    if (a.bf16) return vector_ok(a, 4) ? launch_fwd<bf16_t, 4>(a, st) : launch_fwd<bf16_t, 1>(a, st);
     return vector_ok(a, 4) ? launch_fwd<float, 4>(a, st) : launch_fwd<float, 1>(a, st);
 }
 
 hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t st) {
     if (!a.bf16)
-        return vector_ok(a, 4) ? launch_bwd<float, float, 4>(a, st) : launch_bwd<float, float, 1>(a, st);
-    const bool v = vector_ok(a, 8);
-    if (a.grad_bf16) return v ? launch_bwd<bf16_t, bf16_t, 8>(a, st) : launch_bwd<bf16_t, bf16_t, 1>(a, st);
-    return v ? launch_bwd<bf16_t, float, 8>(a, st) : launch_bwd<bf16_t, float, 1>(a, st);
+        return vector_ok(a, 2) ? launch_bwd<float, float, 2>(a, st) : launch_bwd<float, float, 1>(a, st);
+    const bool v = vector_ok(a, 2);
+    if (a.grad_bf16) return v ? launch_bwd<bf16_t, bf16_t, 2>(a, st) : launch_bwd<bf16_t, bf16_t, 1>(a, st);
+    return v ? launch_bwd<bf16_t, float, 2>(a, st) : launch_bwd<bf16_t, float, 1>(a, st);
 }
 
 hipError_t launch_conv_step(const ConvStepArgs &a, hipStream_t st) {

@@ -135,7 +135,7 @@ struct ConvArgs {
     int channels, width, tile;
     bool silu, bf16, grad_bf16 = false;
 };
-int conv_tile(int64_t tokens, int channels);             // tokens a wave takes
+int conv_tile(int64_t tokens, int channels, bool backward);    // tokens a wave takes
 int64_t conv_tiles(int64_t tokens, int tile);            // at least one
 hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t st);
 hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t st);

@@ -13,6 +13,16 @@ template <typename T, int V>
 __device__ __forceinline__ void ldv(const T *p, float (&x)[V]) {
     if constexpr (V == 1) {
         x[0] = io<T>::ld(p);
+    } else if constexpr (V % 4 == 2 && sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(p + i);
+            x[i] = v.x; x[i + 1] = v.y;
+        }
+    } else if constexpr (V == 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+        x[0] = __uint_as_float(w << 16);
+        x[1] = __uint_as_float(w & 0xffff0000u);
     } else if constexpr (sizeof(T) == 4) {
         static_assert(V % 4 == 0, "whole 16-byte pieces");
 #pragma unroll
@@ -24,7 +34,7 @@ __device__ __forceinline__ void ldv(const T *p, float (&x)[V]) {
         const f32x4 v = io<T>::ld4(p);
         x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
     } else {
-        static_assert(V == 8, "bf16 vectors have 1, 4 or 8 elements");
+        static_assert(V == 8, "bf16 vectors have 1, 2, 4 or 8 elements");
         const uint4 v = *reinterpret_cast<const uint4 *>(p);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -39,6 +49,11 @@ template <typename T, int V>
 __device__ __forceinline__ void stv(T *p, const float (&x)[V]) {
     if constexpr (V == 1) {
         io<T>::st(p, x[0]);
+    } else if constexpr (V == 2 && sizeof(T) == 4) {
+        *reinterpret_cast<float2 *>(p) = float2{x[0], x[1]};
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<uint32_t *>(p) = static_cast<uint32_t>(f32_to_bf16_bits(x[0])) |
+                                           (static_cast<uint32_t>(f32_to_bf16_bits(x[1])) << 16);
     } else if constexpr (sizeof(T) == 4 || V == 4) {
 #pragma unroll
         for (int i = 0; i < V; i += 4) io<T>::st4(p + i, f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]});
@@ -49,6 +64,55 @@ __device__ __forceinline__ void stv(T *p, const float (&x)[V]) {
             w[i] = static_cast<uint32_t>(f32_to_bf16_bits(x[2 * i])) |
                    (static_cast<uint32_t>(f32_to_bf16_bits(x[2 * i + 1])) << 16);
         *reinterpret_cast<uint4 *>(p) = uint4{w[0], w[1], w[2], w[3]};
+    }
+}
+
+// Element c of a row: one pointer for the wave and 32 bits of offset per lane (c < 2^20), the
+// form that global memory instructions take without address arithmetic.
+template <typename T>
+__device__ __forceinline__ const T *elem(const T *row, uint32_t c) {
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) + c * static_cast<uint32_t>(sizeof(T)));
+}
+template <typename T>
+__device__ __forceinline__ T *elem(T *row, uint32_t c) {
+    return reinterpret_cast<T *>(reinterpret_cast<char *>(row) + c * static_cast<uint32_t>(sizeof(T)));
+}
+
+// V elements as they are in memory: loaded now, widened when they are used, so that the load does
+// not have to be waited for before.
+template <typename T, int V>
+struct Raw {
+    static constexpr int N = V * sizeof(T) / 4;
+    typedef uint32_t words __attribute__((ext_vector_type(N), aligned(N * 4 < 16 ? N * 4 : 16)));
+    words w;
+    __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const words *>(p); }
+    __device__ __forceinline__ void get(float (&x)[V]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                x[i] = __uint_as_float(w[i]);
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+template <typename T>
+struct Raw<T, 1> {
+    T w;
+    __device__ __forceinline__ void load(const T *p) { w = *p; }
+    __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = io<T>::val(w); }
+};
+
+// Element c of the K rows from `row` on, V of them; rows from m on repeat row m - 1, so no access
+// is conditional (m >= 1).
+template <typename T, int V, int K>
+__device__ __forceinline__ void load_rows(const T *row, int64_t stride, uint32_t c, int m, Raw<T, V> (&v)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        v[k].load(elem(row, c));
+        row += k + 1 < m ? stride : 0;
     }
 }
 

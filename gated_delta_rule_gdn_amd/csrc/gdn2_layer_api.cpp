@@ -81,13 +81,13 @@ gdn2_status check_conv(const gdn2_conv_dims *d, bool packed, bool backward) {
 }
 
 gdn2::ConvArgs conv_args(const gdn2_conv_dims *d, const void *x, const float *weight,
-                         const float *bias, const float *state0, const int32_t *cu) {
+                         const float *bias, const float *state0, const int32_t *cu, bool backward) {
     gdn2::ConvArgs a;
     a.x = x; a.weight = weight; a.bias = bias; a.state0 = state0;
     a.map = seq_map(cu, d->batch, d->seqlen, d->num_seqs);
     a.x_stride = d->x_stride ? d->x_stride : d->channels;
     a.channels = d->channels; a.width = d->width;
-    a.tile = gdn2::conv_tile(a.map.total, a.channels);
+    a.tile = gdn2::conv_tile(a.map.total, a.channels, backward);
     a.silu = d->silu != 0;
     a.bf16 = d->dtype == GDN2_BF16;
     return a;
@@ -218,7 +218,7 @@ gdn2_status gdn2_short_conv_fwd(const void *x, const float *weight, const float 
     const void *outs[] = {y, state_T}, *ins[] = {x, weight, bias, state0, cu_seqlens};
     if (aliases(outs, ins)) return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input or the other output");
     if (!tokens && !state_T) return ok();
-    gdn2::ConvArgs a = conv_args(dims, x, weight, bias, state0, cu_seqlens);
+    gdn2::ConvArgs a = conv_args(dims, x, weight, bias, state0, cu_seqlens, false);
     a.y = y; a.state_T = state_T;
     return done(gdn2::launch_conv_fwd(a, static_cast<hipStream_t>(stream)), "gdn2_short_conv_fwd launch");
 }
@@ -226,7 +226,7 @@ gdn2_status gdn2_short_conv_fwd(const void *x, const float *weight, const float 
 size_t gdn2_short_conv_bwd_workspace_bytes(const gdn2_conv_dims *dims) {
     if (!dims || check_conv(dims, dims->num_seqs > 0 && dims->batch == 1, true) != GDN2_OK) return 0;
     const int64_t tokens = static_cast<int64_t>(dims->batch) * dims->seqlen;
-    const int64_t tiles = gdn2::conv_tiles(tokens, gdn2::conv_tile(tokens, dims->channels));
+    const int64_t tiles = gdn2::conv_tiles(tokens, gdn2::conv_tile(tokens, dims->channels, true));
     return static_cast<size_t>(tiles) * (dims->width + 1) * dims->channels * sizeof(float);
 }
 
@@ -244,7 +244,7 @@ gdn2_status gdn2_short_conv_bwd(const void *x, const float *weight, const float 
     const void *outs[] = {dx, dweight, dbias, dstate0};
     const void *ins[] = {x, weight, bias, state0, cu_seqlens, dy, dstate_T, workspace};
     if (aliases(outs, ins)) return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input, the workspace or another output");
-    gdn2::ConvArgs a = conv_args(dims, x, weight, bias, state0, cu_seqlens);
+    gdn2::ConvArgs a = conv_args(dims, x, weight, bias, state0, cu_seqlens, true);
     const size_t need = static_cast<size_t>(gdn2::conv_tiles(a.map.total, a.tile)) * (a.width + 1) *
                         a.channels * sizeof(float);
     st = check_workspace(workspace, workspace_bytes, need);

@@ -64,6 +64,25 @@ __device__ __forceinline__ void load_row(const T *p, const Cols<V, P> &k, float 
     }
 }
 
+// The same in two steps: loaded as it is in memory, widened when it is used.
+template <typename T, int V, int P>
+struct RawRow {
+    Raw<T, V> r[P];
+    __device__ __forceinline__ void load(const T *p, const Cols<V, P> &k) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (k.in(i)) r[i].load(p + k.at(i));
+    }
+    __device__ __forceinline__ void get(const Cols<V, P> &k, float (&x)[P][V]) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            r[i].get(x[i]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[i][v] = k.in(i) ? x[i][v] : 0.f;
+        }
+    }
+};
+
 template <typename T, int V, int P>
 __device__ __forceinline__ void store_row(T *p, const Cols<V, P> &k, const float (&x)[P][V]) {
 #pragma unroll
@@ -145,17 +164,45 @@ __global__ __launch_bounds__(norm_threads(L)) void norm_bwd_kernel(NormArgs a) {
         for (int v = 0; v < V; ++v) dnw[i][v] = dsc[i][v] = dxw[i][v] = 0.f;
     int slot = 0;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / L;
-    for (int64_t row = first; row < a.rows; row += static_cast<int64_t>(gridDim.x) * ROWS) {
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * ROWS;
+    // the next row's inputs are loaded while a row is worked on, where registers allow
+    constexpr bool AHEAD = L < 1024;
+    RawRow<T, V, P> nx, ngate;
+    RawRow<TR, V, P> nres;
+    RawRow<TGR, V, P> ndh;
+    RawRow<TG, V, P> ndy;
+    auto fetch = [&](int64_t row) {
+        nx.load(static_cast<const T *>(a.x) + row * a.x_stride, k);
+        if (a.gate) ngate.load(static_cast<const T *>(a.gate) + row * a.gate_stride, k);
+        if (a.dh) ndh.load(static_cast<const TGR *>(a.dh) + row * a.d, k);
+        if (a.next_weight) {
+            ndy.load(static_cast<const TG *>(a.dy) + row * a.d, k);
+            if (a.residual) nres.load(static_cast<const TR *>(a.residual) + row * a.d, k);
+        }
+    };
+    if (AHEAD && first < a.rows) fetch(first);
+    for (int64_t row = first; row < a.rows; row += stride) {
         // p: x through the first norm; u: through the gate; h: the new residual
-        float x[P][V], p[P][V], t[P][V], g[P][V], sl[P][V];
-        load_row<T>(static_cast<const T *>(a.x) + row * a.x_stride, k, x, 0.f);
-        if (a.gate) load_row<T>(static_cast<const T *>(a.gate) + row * a.gate_stride, k, sl, 0.f);
-        if (a.dh) load_row<TGR>(static_cast<const TGR *>(a.dh) + row * a.d, k, g, 0.f);
+        float x[P][V], p[P][V], t[P][V], g[P][V], sl[P][V], h[P][V], w[P][V];
+        if (!AHEAD) fetch(row);
+        nx.get(k, x);
+        if (a.gate) ngate.get(k, sl);
+        if (a.dh) ndh.get(k, g);
         else
 #pragma unroll
             for (int i = 0; i < P; ++i)
 #pragma unroll
                 for (int v = 0; v < V; ++v) g[i][v] = 0.f;
+        if (a.next_weight) {
+            ndy.get(k, w);
+            if (a.residual) nres.get(k, h);
+            else
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) h[i][v] = 0.f;
+        }
+        if (AHEAD && row + stride < a.rows) fetch(row + stride);
         float rx = 1.f;
         if (a.norm_weight) {
             float q = 0.f;
@@ -177,14 +224,6 @@ __global__ __launch_bounds__(norm_threads(L)) void norm_bwd_kernel(NormArgs a) {
                 for (int v = 0; v < V; ++v) p[i][v] = x[i][v];
         }
         if (a.next_weight) {
-            float h[P][V], w[P][V];
-            if (a.residual) load_row<TR>(static_cast<const TR *>(a.residual) + row * a.d, k, h, 0.f);
-            else
-#pragma unroll
-                for (int i = 0; i < P; ++i)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) h[i][v] = 0.f;
-            load_row<TG>(static_cast<const TG *>(a.dy) + row * a.d, k, w, 0.f);
             if (a.scale) load_row<float>(a.scale, k, t, 0.f);
             float q = 0.f;
 #pragma unroll
@@ -266,28 +305,30 @@ __global__ __launch_bounds__(norm_threads(L)) void norm_bwd_kernel(NormArgs a) {
     if (a.next_weight) store_row<float>(part + 2 * static_cast<int64_t>(a.d), k, dnw);
 }
 
-// The parameter gradients: the rows of a.partial added in a fixed order. 64 columns per
-// workgroup, sixteen waves taking every sixteenth row.
+// The parameter gradients: the rows of a.partial added in a fixed order. 32 columns per
+// workgroup, whose 32 halves of waves each take every 32nd row.
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormArgs a, int parts) {
-    __shared__ float s[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, half = threadIdx.x >> 5;
     const int which = blockIdx.y;
     float *out = which == 0 ? a.dnorm_weight : which == 1 ? a.dscale : a.dnext_weight;
     if (!(which == 0 ? a.norm_weight : which == 1 ? a.scale : a.next_weight)) return;
-    const int col = blockIdx.x * 64 + lane;
+    const int col = blockIdx.x * 32 + lane;
     float sum = 0.f;
-    if (col < a.d)
-        for (int i = wave; i < parts; i += 16)
-            sum += a.partial[(static_cast<int64_t>(i) * 3 + which) * a.d + col];
-    s[wave][lane] = sum;
+    if (col < a.d) {
+        const float *p = a.partial + static_cast<int64_t>(which) * a.d + col;
+#pragma unroll 8
+        for (int i = half; i < parts; i += 32) sum += p[static_cast<int64_t>(i) * 3 * a.d];
+    }
+    s[half][lane] = sum;
     __syncthreads();
-    if (wave != 0 || col >= a.d) return;
+    if (half != 0 || col >= a.d) return;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) sum += s[i][lane];
+    for (int i = 1; i < 32; ++i) sum += s[i][lane];
     out[col] = sum;
 }
 
-constexpr int kNormGroups = 512;      // workgroups of a backward pass: two per CU
+constexpr int kNormGroups = 768;      // workgroups of a backward pass: three per CU
 
 template <typename T, typename TR, typename TG, typename TGR, int L, int V, int P>
 hipError_t launch(const NormArgs &a, bool backward, hipStream_t st) {
@@ -302,7 +343,7 @@ hipError_t launch(const NormArgs &a, bool backward, hipStream_t st) {
     hipLaunchKernelGGL((norm_bwd_kernel<T, TR, TG, TGR, L, V, P>), dim3(groups), dim3(THREADS), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !(a.norm_weight || a.scale || a.next_weight)) return e;
-    hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((a.d + 63) / 64), 3), dim3(1024), 0,
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32), 3), dim3(1024), 0,
                        st, a, static_cast<int>(groups) * ROWS);
     return hipGetLastError();
 }

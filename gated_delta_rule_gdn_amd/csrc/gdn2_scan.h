@@ -131,17 +131,6 @@ struct Stage {
     }
 };
 
-// Element c of a row: one pointer for the wave and 32 bits of offset per lane (c < 2^20), the
-// form that global memory instructions take without address arithmetic.
-template <typename T>
-__device__ __forceinline__ const T *elem(const T *row, uint32_t c) {
-    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) + c * static_cast<uint32_t>(sizeof(T)));
-}
-template <typename T>
-__device__ __forceinline__ T *elem(T *row, uint32_t c) {
-    return reinterpret_cast<T *>(reinterpret_cast<char *>(row) + c * static_cast<uint32_t>(sizeof(T)));
-}
-
 // Element c of the K rows from `row` on; rows from m on repeat row m - 1, so no access is
 // conditional.
 template <typename T, int K>

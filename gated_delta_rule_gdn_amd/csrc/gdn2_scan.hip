@@ -144,56 +144,100 @@ __global__ __launch_bounds__(256) void scan_chain_kernel(ScanArgs a, int tiles) 
     chain_tiles<1>(a, a.tiles_h, tiles);
 }
 
+// Four of a channel's states, or of a row of B or C, from state n0 on: loaded without a condition
+// (places behind the last state repeat one) and widened, with zeros there, when they are used. So
+// a token's loads are all in flight before the first is waited for.
+template <typename E, bool VEC>
+struct Four {
+    Raw<E, 4> v;
+    __device__ __forceinline__ void load(const E *row, int n0, int states) {
+        v.load(row + (n0 < states ? n0 : 0));
+    }
+    __device__ __forceinline__ void get(float (&x)[4], int n0, int states) const {
+        v.get(x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = n0 < states ? x[j] : 0.f;
+    }
+};
+template <typename E>
+struct Four<E, false> {
+    E v[4];
+    __device__ __forceinline__ void load(const E *row, int n0, int states) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = row[n0 + j < states ? n0 + j : states - 1];
+    }
+    __device__ __forceinline__ void get(float (&x)[4], int n0, int states) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = n0 + j < states ? io<E>::val(v[j]) : 0.f;
+    }
+};
+
 // T tokens of every sequence against its slot of a pool [num_slots][channels][d_state]. LP lanes
 // per channel, four consecutive states per lane: a wave reads and writes 1 KiB of states in a
-// row. Bound by that traffic; each state is read once and written once per call.
+// row. Bound by that traffic; each state is read once and written once per call. A workgroup
+// keeps its channels' rates for several sequences, and loads the next one's state and token
+// while it works on one. VEC: states, B and C are read in pieces of four.
 template <typename T, typename TS, int LP, bool VEC>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepArgs a) {
     constexpr int PER = 256 / LP;
-    const int part = threadIdx.x & (LP - 1);
+    const int part = threadIdx.x & (LP - 1), n0 = 4 * part, states = a.d_state;
     const int c = blockIdx.x * PER + threadIdx.x / LP;
     const bool on = c < a.channels;
-    const int cc = on ? c : a.channels - 1;
-    const int n0 = 4 * part, g = cc / (a.channels / a.groups);
-    float A2[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        A2[j] = n0 + j < a.d_state ? kLog2e * a.A[static_cast<int64_t>(cc) * a.d_state + n0 + j] : 0.f;
+    const uint32_t cc = on ? c : a.channels - 1;
+    const uint32_t bc = cc / (a.channels / a.groups) * states;       // in a row of B or C
+    struct Token { T x, dt, gate; Four<T, VEC> b, c; };
+    auto token = [&](int64_t row, Token &k) {
+        k.x = *elem(static_cast<const T *>(a.x) + row * a.x_stride, cc);
+        k.dt = *elem(static_cast<const T *>(a.dt) + row * a.dt_stride, cc);
+        k.gate = T{};
+        if (a.gate) k.gate = *elem(static_cast<const T *>(a.gate) + row * a.gate_stride, cc);
+        k.b.load(static_cast<const T *>(a.B) + row * a.b_stride + bc, n0, states);
+        k.c.load(static_cast<const T *>(a.C) + row * a.c_stride + bc, n0, states);
+    };
+    auto slot_of = [&](int64_t i) { return a.idx ? a.idx[i] : static_cast<int>(i); };
+    auto in_pool = [&](int slot) { return slot >= 0 && slot < a.num_slots; };
+    auto state_of = [&](int slot) {
+        return static_cast<TS *>(a.state) + (static_cast<int64_t>(slot) * a.channels + cc) * states;
+    };
+    int64_t i = blockIdx.y;
+    int slot = slot_of(i);
+    Four<float, false> rates;
+    Four<TS, VEC> next;
+    Token first;
+    rates.load(a.A + static_cast<int64_t>(cc) * states, n0, states);
+    token(i * a.ntok, first);
+    if (in_pool(slot)) next.load(state_of(slot), n0, states);
     const float bias = a.dt_bias ? a.dt_bias[cc] : 0.f, skip = a.D ? a.D[cc] : 0.f;
-    for (int64_t i = blockIdx.y; i < a.num_seqs; i += gridDim.y) {
-        const int slot = a.idx ? a.idx[i] : static_cast<int>(i);
-        T *o = static_cast<T *>(a.o) + i * a.ntok * static_cast<int64_t>(a.channels) + cc;
-        if (slot < 0 || slot >= a.num_slots) {
+    float A2[4];
+    rates.get(A2, n0, states);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) A2[j] *= kLog2e;
+    for (; i < a.num_seqs; i += gridDim.y) {
+        const int mine = slot;
+        const Four<TS, VEC> old = next;
+        Token k = first;
+        if (i + gridDim.y < a.num_seqs) {
+            slot = slot_of(i + gridDim.y);
+            token((i + gridDim.y) * a.ntok, first);
+            if (in_pool(slot)) next.load(state_of(slot), n0, states);
+        }
+        T *o = static_cast<T *>(a.o) + i * a.ntok * a.channels;
+        if (!in_pool(mine)) {
             if (on && part == 0)
-                for (int t = 0; t < a.ntok; ++t) io<T>::st(o + t * static_cast<int64_t>(a.channels), 0.f);
+                for (int t = 0; t < a.ntok; ++t) io<T>::st(elem(o + t * static_cast<int64_t>(a.channels), cc), 0.f);
             continue;
         }
-        TS *st = static_cast<TS *>(a.state) + (static_cast<int64_t>(slot) * a.channels + cc) * a.d_state + n0;
-        float h[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (VEC) {
-            if (n0 < a.d_state) ldv<TS, 4>(st, h);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n0 + j < a.d_state) h[j] = io<TS>::ld(st + j);
-        }
+        float h[4];
+        old.get(h, n0, states);
         for (int t = 0; t < a.ntok; ++t) {
-            const int64_t row = i * a.ntok + t;
-            const float xv = io<T>::ld(static_cast<const T *>(a.x) + row * a.x_stride + cc);
-            float d = io<T>::ld(static_cast<const T *>(a.dt) + row * a.dt_stride + cc) + bias;
-            const float gv = a.gate ? io<T>::ld(static_cast<const T *>(a.gate) + row * a.gate_stride + cc) : 0.f;
-            const T *pb = static_cast<const T *>(a.B) + row * a.b_stride + g * a.d_state + n0;
-            const T *pc = static_cast<const T *>(a.C) + row * a.c_stride + g * a.d_state + n0;
             float b[4], cv[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = n0 + j < a.d_state;
-                b[j] = in ? io<T>::ld(pb + j) : 0.f;
-                cv[j] = in ? io<T>::ld(pc + j) : 0.f;
-            }
+            k.b.get(b, n0, states);
+            k.c.get(cv, n0, states);
+            const float x = io<T>::val(k.x), g = io<T>::val(k.gate);
+            float d = io<T>::val(k.dt) + bias, y = 0.f;
+            if (t + 1 < a.ntok) token(i * a.ntok + t + 1, k);
             if (a.softplus) d = softplus(d);
-            const float u = d * xv;
-            float y = 0.f;
+            const float u = d * x;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 h[j] = fmaf(__builtin_amdgcn_exp2f(d * A2[j]), h[j], u * b[j]);
@@ -201,17 +245,17 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepArgs a) {
             }
 #pragma unroll
             for (int m = 1; m < LP; m <<= 1) y += __shfl_xor(y, m);
-            y = fmaf(skip, xv, y);
-            if (a.gate) y *= silu(gv);
-            if (on && part == 0) io<T>::st(o + t * static_cast<int64_t>(a.channels), y);
+            y = fmaf(skip, x, y);
+            if (a.gate) y *= silu(g);
+            if (on && part == 0) io<T>::st(elem(o + t * static_cast<int64_t>(a.channels), cc), y);
         }
-        if (!on) continue;
+        TS *st = state_of(mine) + n0;
         if constexpr (VEC) {
-            if (n0 < a.d_state) stv<TS, 4>(st, h);
+            if (on && n0 < states) stv<TS, 4>(st, h);
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (n0 + j < a.d_state) io<TS>::st(st + j, h[j]);
+                if (on && n0 + j < states) io<TS>::st(st + j, h[j]);
         }
     }
 }
@@ -243,9 +287,15 @@ hipError_t launch_fwd_t(const ScanArgs &a, hipStream_t st) {
 
 template <typename T, typename TS, int LP>
 hipError_t launch_step(const ScanStepArgs &a, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>((a.channels + 256 / LP - 1) / (256 / LP)),
-                    static_cast<unsigned>(a.num_seqs < 65535 ? a.num_seqs : 65535));
-    const bool vec = a.d_state % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
+    // about 1,024 workgroups, four waves per SIMD, each with as many sequences as that leaves
+    // (64 sequences x 4,096 channels x 16 states: 12.3 us; 512 14.7 us, one each 14.8 us)
+    const int wide = (a.channels + 256 / LP - 1) / (256 / LP);
+    int rows = (1024 + wide - 1) / wide;
+    if (rows > a.num_seqs) rows = a.num_seqs;
+    const dim3 grid(wide, rows);
+    auto whole = [](const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+    const bool vec = a.d_state % 4 == 0 && a.b_stride % 4 == 0 && a.c_stride % 4 == 0 &&
+                     whole(a.state, 4 * sizeof(TS)) && whole(a.B, 4 * sizeof(T)) && whole(a.C, 4 * sizeof(T));
     if (vec) hipLaunchKernelGGL((scan_step_kernel<T, TS, LP, true>), grid, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((scan_step_kernel<T, TS, LP, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
@@ -253,6 +303,7 @@ hipError_t launch_step(const ScanStepArgs &a, hipStream_t st) {
 
 template <typename T, typename TS>
 hipError_t launch_step_t(const ScanStepArgs &a, hipStream_t st) {
+    if (a.d_state <= 4) return launch_step<T, TS, 1>(a, st);
     if (a.d_state <= 8) return launch_step<T, TS, 2>(a, st);
     if (a.d_state <= 16) return launch_step<T, TS, 4>(a, st);
     if (a.d_state <= 32) return launch_step<T, TS, 8>(a, st);
