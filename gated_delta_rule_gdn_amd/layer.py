@@ -71,33 +71,40 @@ def declare(L: ctypes.CDLL) -> None:
 
 def _call(dev: torch.device, f, *args) -> None:
     """f(*args, stream) on the device's current stream, with that device current."""
-    if torch.cuda.current_device() == dev.index:
-        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     if st:
         _raise_on(st)
 
 
-def _on_gpu(name: str, t: torch.Tensor, dev) -> None:
+def _gpu_of(name: str, t: torch.Tensor) -> torch.device:
+    """The GPU a call runs on: that of its first input."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
+    return t.device
+
+
+def _check(name: str, t: torch.Tensor, dev, dtype, shape) -> None:
+    """Says what is wrong with a tensor's device, type or shape."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (the library has no CPU path)")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-
-
-def _tokens(name: str, t: torch.Tensor, dev, dtype, lead, inner) -> int:
-    """Checks a token input [*lead, *inner] that may be a column slice. Returns the elements
-    from one token to the next."""
-    _on_gpu(name, t, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != lead + inner:
-        raise ValueError(f"{name} must be {list(lead + inner)}, not {list(t.shape)}")
-    row = 1
-    for n in inner:
-        row *= n
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+
+
+def _tokens(name: str, t: torch.Tensor, dev, dtype, shape, row: int) -> int:
+    """Checks a token input [B, T, ...] of `row` values per token that may be a column slice.
+    Returns the elements from one token to the next."""
+    if t.dtype != dtype or t.device != dev or t.shape != shape:
+        _check(name, t, dev, dtype, shape)
     if t.is_contiguous():
         return row
     want = 1
@@ -105,7 +112,7 @@ def _tokens(name: str, t: torch.Tensor, dev, dtype, lead, inner) -> int:
         if t.shape[d] != 1 and t.stride(d) != want:
             raise ValueError(f"{name}: every token's values must be contiguous")
         want *= t.shape[d]
-    B, T = lead
+    B, T = shape[0], shape[1]
     if T > 1:
         step = t.stride(1)
         if B > 1 and t.stride(0) != T * step:
@@ -121,11 +128,10 @@ def _whole(name: str, t: Optional[torch.Tensor], dev, dtype, shape) -> Optional[
     """Checks a contiguous tensor of one type and shape (None is let through); its pointer."""
     if t is None:
         return None
-    _need_gpu(name, t, dev)
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.dtype != dtype or t.device != dev or t.shape != shape:
+        _check(name, t, dev, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
@@ -161,18 +167,19 @@ def _workspace(workspace, need: int, dev) -> torch.Tensor:
 
 def _conv_dims(x, weight, bias, cu_seqlens, silu, grad_code) -> Tuple[ConvDims, int]:
     """The checked dims of a prompt call, and the number of sequences."""
-    dev = x.device
+    dev = _gpu_of("x", x)
     if x.dim() != 3:
         raise ValueError("x must be [B,T,C]")
     B, T, C = x.shape
     code = _dtype_code(x.dtype)
-    step = _tokens("x", x, dev, x.dtype, (B, T), (C,))
+    step = _tokens("x", x, dev, x.dtype, x.shape, C)
     if weight.dim() != 2 or weight.shape[0] != C:
         raise ValueError(f"weight must be fp32 [{C},W]")
-    _whole("weight", weight, dev, torch.float32, (C, weight.shape[1]))
+    W = weight.shape[1]
+    _whole("weight", weight, dev, torch.float32, (C, W))
     _whole("bias", bias, dev, torch.float32, (C,))
     N, num_seqs = _sequences(cu_seqlens, B, dev)
-    return ConvDims(B, T, num_seqs, C, weight.shape[1], code, grad_code, 1 if silu else 0, step), N
+    return ConvDims(B, T, num_seqs, C, W, code, grad_code, 1 if silu else 0, step), N
 
 
 def short_conv_fwd(x, weight, bias: Optional[torch.Tensor] = None,
@@ -188,7 +195,7 @@ def short_conv_fwd(x, weight, bias: Optional[torch.Tensor] = None,
     recurrent_fwd and short_conv_step keep in their conv_state. It must not be state0's own
     buffer."""
     d, N = _conv_dims(x, weight, bias, cu_seqlens, silu, 0)
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     f32 = torch.float32
     st_shape = (N, d.width - 1, d.channels)
     s0 = _whole("state0", state0, dev, f32, st_shape)
@@ -212,7 +219,7 @@ def short_conv_bwd(x, weight, dy, bias: Optional[torch.Tensor] = None,
     dL/dstate_T (None: zero). Returns dx (dy's dtype), dweight fp32 [C,W], and dbias, dstate0
     where the call has a bias, a state0."""
     d, N = _conv_dims(x, weight, bias, cu_seqlens, silu, _grad_code("dy", dy, x.dtype))
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     f32 = torch.float32
     st_shape = (N, d.width - 1, d.channels)
     s0 = _whole("state0", state0, dev, f32, st_shape)
@@ -255,7 +262,7 @@ def short_conv_step(x, weight, conv_state, bias: Optional[torch.Tensor] = None,
     slot n); an entry outside the pool marks padding (zero y rows, no state touched). Returns
     y [N,T,C]."""
     d, N = _conv_dims(x, weight, bias, None, silu, 0)
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     if conv_state.dim() != 3:
         raise ValueError(f"conv_state must be fp32 [num_slots,{d.width - 1},{d.channels}]")
     slots = conv_state.shape[0]
@@ -272,22 +279,22 @@ def short_conv_step(x, weight, conv_state, bias: Optional[torch.Tensor] = None,
 
 def _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, num_seqs, grad_code) -> ScanDims:
     """The checked dims of a scan call."""
-    dev, dtype = x.device, x.dtype
+    dev, dtype, shape = _gpu_of("x", x), x.dtype, x.shape
     if x.dim() != 3:
         raise ValueError("x must be [B,T,channels]")
     if B.dim() != 4:
         raise ValueError("B and C must be [B,T,groups,d_state]")
-    lead, ch = tuple(x.shape[:2]), x.shape[2]
+    n, T, ch = shape
     G, M = B.shape[2], B.shape[3]
-    code = _dtype_code(dtype)
-    strides = [_tokens("x", x, dev, dtype, lead, (ch,)), _tokens("dt", dt, dev, dtype, lead, (ch,)),
-               _tokens("B", B, dev, dtype, lead, (G, M)), _tokens("C", C, dev, dtype, lead, (G, M)),
-               0 if gate is None else _tokens("gate", gate, dev, dtype, lead, (ch,))]
+    code, bc = _dtype_code(dtype), (n, T, G, M)
+    strides = [_tokens("x", x, dev, dtype, shape, ch), _tokens("dt", dt, dev, dtype, shape, ch),
+               _tokens("B", B, dev, dtype, bc, G * M), _tokens("C", C, dev, dtype, bc, G * M),
+               0 if gate is None else _tokens("gate", gate, dev, dtype, shape, ch)]
     f32 = torch.float32
     _whole("A", A, dev, f32, (ch, M))
     _whole("D", D, dev, f32, (ch,))
     _whole("dt_bias", dt_bias, dev, f32, (ch,))
-    return ScanDims(lead[0], lead[1], num_seqs, ch, M, G, code, grad_code, 1 if dt_softplus else 0,
+    return ScanDims(n, T, num_seqs, ch, M, G, code, grad_code, 1 if dt_softplus else 0,
                     *strides)
 
 
@@ -311,9 +318,9 @@ def selective_scan_fwd(x, dt, A, B, C, D: Optional[torch.Tensor] = None,
     a column slice); A fp32 [channels,d_state]; D, dt_bias fp32 [channels]; dt_softplus: the
     step is softplus(dt + dt_bias); S0 fp32 [N,channels,d_state]; cu_seqlens int32 [N+1] for a
     packed batch. Returns (o [B,T,channels], S_T fp32 [N,channels,d_state] or None)."""
-    N, num_seqs = _sequences(cu_seqlens, x.shape[0], x.device)
+    N, num_seqs = _sequences(cu_seqlens, x.shape[0], _gpu_of("x", x))
     d = _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, num_seqs, 0)
-    dev, shape, f32 = x.device, tuple(x.shape), torch.float32
+    dev, shape, f32 = x.device, x.shape, torch.float32
     st_shape = (N, d.channels, d.d_state)
     s0 = _whole("S0", S0, dev, f32, st_shape)
     o = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
@@ -349,10 +356,10 @@ def selective_scan_bwd(x, dt, A, B, C, dO, D: Optional[torch.Tensor] = None,
     """Gradients of selective_scan_fwd given dO = dL/do [B,T,channels] (x's dtype or fp32) and
     dS_T = dL/dS_T (None: zero). Returns dx, ddt, dB, dC (and dgate) in dO's dtype, dA (and dD,
     ddt_bias, dS0) in fp32, each optional one for the argument given."""
-    N, num_seqs = _sequences(cu_seqlens, x.shape[0], x.device)
+    N, num_seqs = _sequences(cu_seqlens, x.shape[0], _gpu_of("x", x))
     d = _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, num_seqs,
                    _grad_code("dO", dO, x.dtype))
-    dev, shape, f32 = x.device, tuple(x.shape), torch.float32
+    dev, shape, f32 = x.device, x.shape, torch.float32
     st_shape = (N, d.channels, d.d_state)
     s0 = _whole("S0", S0, dev, f32, st_shape)
     pdo = _whole("dO", dO, dev, dO.dtype, shape)
@@ -386,7 +393,7 @@ def selective_scan_step(x, dt, A, B, C, state, D: Optional[torch.Tensor] = None,
     updated in place. state_idx int32 [N]: the slot of each sequence (None: slot n); an entry
     outside the pool marks padding (zero o rows, no state touched). Returns o [N,T,channels]."""
     d = _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, 0, 0)
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     if state.dim() != 3:
         raise ValueError(f"state must be [num_slots,{d.channels},{d.d_state}]")
     if state.dtype not in (torch.float32, torch.bfloat16):
@@ -406,11 +413,8 @@ def selective_scan_step(x, dt, A, B, C, state, D: Optional[torch.Tensor] = None,
 
 def _rows(name: str, t: torch.Tensor, dev, dtype, shape) -> int:
     """Checks an input of rows that may be a column slice. Returns the elements between rows."""
-    _on_gpu(name, t, dev)
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.dtype != dtype or t.device != dev or t.shape != shape:
+        _check(name, t, dev, dtype, shape)
     d = shape[-1]
     if t.is_contiguous():
         return d
@@ -433,7 +437,7 @@ def _rows(name: str, t: torch.Tensor, dev, dtype, shape) -> int:
 
 def _norm_dims(x, gate, residual, norm_weight, scale, next_weight, eps, grad_code) -> NormDims:
     """The checked dims of a block norm call."""
-    dev, dtype, shape = x.device, x.dtype, x.shape
+    dev, dtype, shape = _gpu_of("x", x), x.dtype, x.shape
     if x.dim() < 1:
         raise ValueError("x must be [*rows,d]")
     d = shape[-1]
@@ -445,7 +449,7 @@ def _norm_dims(x, gate, residual, norm_weight, scale, next_weight, eps, grad_cod
         rcode = _dtype_code(residual.dtype)
         if residual.dtype not in (dtype, torch.float32):
             raise TypeError(f"residual has dtype {residual.dtype}, expected {dtype} or torch.float32")
-        _whole("residual", residual, dev, residual.dtype, tuple(shape))
+        _whole("residual", residual, dev, residual.dtype, shape)
     for name, t in (("norm_weight", norm_weight), ("scale", scale), ("next_weight", next_weight)):
         _whole(name, t, dev, torch.float32, (d,))
     rows = x.numel() // d if d else 0
@@ -464,7 +468,7 @@ def block_norm_fwd(x, norm_weight: Optional[torch.Tensor] = None,
     be a column slice); residual [*rows,d] in x's dtype or fp32; norm_weight, scale, next_weight
     fp32 [d]. Returns (h in residual's dtype, y in x's dtype or None). out may be residual."""
     d = _norm_dims(x, gate, residual, norm_weight, scale, next_weight, eps, 0)
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     ht = x.dtype if residual is None else residual.dtype
     h = torch.empty(shape, dtype=ht, device=dev) if out is None else out
     ph = _whole("out", h, dev, ht, shape)
@@ -493,7 +497,7 @@ def block_norm_bwd(x, dh: Optional[torch.Tensor] = None, dy: Optional[torch.Tens
         raise ValueError("dy and next_weight go together")
     if dh is None and dy is None:
         raise ValueError("without next_weight, dh is required")
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     wide = residual is not None and residual.dtype == torch.float32 and x.dtype != torch.float32
     gt = grad_dtype
     if gt is None:      # with an fp32 residual dh says nothing about the other gradients' type
