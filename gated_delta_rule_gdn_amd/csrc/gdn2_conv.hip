@@ -322,14 +322,14 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
     }
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Whether V channels per lane can be read and written in whole pieces.
+// Whether V channels per lane can be read and written in whole pieces: V elements of the token
+// tensors, up to 16 bytes of the fp32 ones.
+bool whole(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (bytes < 16 ? bytes : 16) == 0; }
 bool vector_ok(const ConvArgs &a, int V) {
-    return a.channels % V == 0 && a.x_stride % V == 0 && aligned16(a.x) && aligned16(a.y) &&
-           aligned16(a.dy) && aligned16(a.dx) && aligned16(a.state0) && aligned16(a.state_T) &&
-           aligned16(a.dstate0) && aligned16(a.dstate_T) &&
-           aligned16(a.weight) && aligned16(a.bias);
+    const int t = V * (a.bf16 ? 2 : 4), g = V * (a.grad_bf16 ? 2 : 4), f = V * 4;
+    return a.channels % V == 0 && a.x_stride % V == 0 && whole(a.x, t) && whole(a.y, t) &&
+           whole(a.dy, g) && whole(a.dx, g) && whole(a.state0, f) && whole(a.state_T, f) &&
+           whole(a.dstate0, f) && whole(a.dstate_T, f) && whole(a.weight, 16) && whole(a.bias, f);
 }
 
 dim3 tile_grid(const ConvArgs &a, int V) {
@@ -429,8 +429,9 @@ hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_conv_step(const ConvStepArgs &a, hipStream_t st) {
-    const bool v = a.channels % 4 == 0 && a.x_stride % 4 == 0 && aligned16(a.x) && aligned16(a.y) &&
-                   aligned16(a.state) && aligned16(a.weight) && aligned16(a.bias);
+    const int t = a.bf16 ? 8 : 16;
+    const bool v = a.channels % 4 == 0 && a.x_stride % 4 == 0 && whole(a.x, t) && whole(a.y, t) &&
+                   whole(a.state, 16) && whole(a.weight, 16) && whole(a.bias, 16);
     if (a.bf16) return v ? launch_step<bf16_t, 4>(a, st) : launch_step<bf16_t, 1>(a, st);
     return v ? launch_step<float, 4>(a, st) : launch_step<float, 1>(a, st);
 }

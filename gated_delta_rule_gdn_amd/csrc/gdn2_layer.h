@@ -182,7 +182,9 @@ __device__ __forceinline__ void for_spans(const SeqMap &m, int t0, int t1, F &&f
         if (!inside && first >= t1 && t1 < m.total) return;
         int end = seq_begin(m, i + 1);
         if (end < first) end = first;
-        f(Span{i, first, end, inside ? t0 : first, end < t1 ? end : t1, !inside, end <= t1});
+        // (first >= t0 where offsets do not decrease; a span never leaves its tile in any case)
+        const int lo = inside || first < t0 ? t0 : first, hi = end < t1 ? end : t1;
+        f(Span{i, first, end, lo, hi < lo ? lo : hi, !inside, end <= t1});
         if (end > t1) return;
         inside = false;
     }

@@ -229,6 +229,24 @@ def test_step(N, T, ch, M, G, sdtype):
     assert torch.equal(P[rest].cpu(), pool[rest])
 
 
+def test_slots_behind_two_gib():
+    """A bf16 pool of more than 2^31 elements: the last slots hold what a small pool would."""
+    ch, M, N = 512, 64, 2
+    slots = (1 << 31) // (ch * M) + 3
+    h = make((N, 1), ch, M, 1, N, torch.bfloat16, seed=31, state=False)
+    d = gpu(h)
+    small = Draw(6).normal(N, ch, M, dtype=torch.bfloat16).cuda()
+    pool = torch.empty(slots, ch, M, dtype=torch.bfloat16, device="cuda")
+    pool[-N:] = small
+    args = dict(D=d["D"], gate=d["gate"], dt_bias=d["dt_bias"], dt_softplus=True)
+    x = (d["x"], d["dt"], d["A"], d["B"], d["C"])
+    idx = torch.tensor([slots - 2, slots - 1], dtype=torch.int32, device="cuda")
+    o = g.selective_scan_step(*x, pool, state_idx=idx, **args)
+    o2 = g.selective_scan_step(*x, small, **args)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(pool[-N:], small)
+
+
 def test_prompt_then_tokens():
     """A prompt's states go on token by token to the same o and states as one longer prompt."""
     T, cut, ch = 50, 37, 66
