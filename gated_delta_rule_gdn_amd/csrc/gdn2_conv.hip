@@ -395,14 +395,14 @@ hipError_t launch_step(const ConvStepArgs &a, hipStream_t st) {
 
 }  // namespace
 
-// Tokens per tile: about 6,144 waves of the forward's 256 channels or 3,072 of the backward's 128
-// (six and three per SIMD), and at least 8 tokens, where the rows next to a tile are nearly half
-// of what a wave reads. On 4,096 tokens x 6,144 channels: 16 tokens forward (21.1 us; 24 tokens
+// Tokens per tile: about six waves of the forward's 256 channels or three of the backward's 128 on
+// each SIMD, and at least 8 tokens, where the rows next to a tile are nearly half of what a wave
+// reads. On 4,096 tokens x 6,144 channels: 16 tokens forward (21.1 us; 24 tokens
 // 22.0, 48 tokens 25.4), 64 backward (39.0 us; 24 tokens 45.0).
 int conv_tile(int64_t tokens, int channels, bool backward) {
     const int per = backward ? 128 : 256;
     const int64_t waves = (static_cast<int64_t>(channels) + per - 1) / per;
-    int64_t t = (tokens * waves / (backward ? 3072 : 6144) + kBatch - 1) / kBatch * kBatch;
+    int64_t t = (tokens * waves / ((backward ? 3 : 6) * kSimds) + kBatch - 1) / kBatch * kBatch;
     if (t < 8) t = 8;
     if (t > 64) t = 64;
     // the grid's second dimension holds at most 65,535 workgroups of four tiles

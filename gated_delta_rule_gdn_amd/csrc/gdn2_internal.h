@@ -175,6 +175,8 @@ struct ScanArgs {
     bool grad_bf16 = false;
     float *tiles_g = nullptr;        // as tiles_h, of the states' gradients from the back
     float *tiles_db = nullptr;       // [tiles][channels]: sums for ddt_bias
+    float *kept_h = nullptr;         // [tokens / 8 + 1][d_state][channels]: states on the way
+    float *kept_dt = nullptr;        // [tokens / 8 + 1][channels]: sums of dt up to them
     float *part_bc = nullptr;        // [workgroups across channels][tokens][2][d_state]
 };
 constexpr int kScanMaxBwdTile = 64;  // tokens of a tile of the backward, which LDS holds whole

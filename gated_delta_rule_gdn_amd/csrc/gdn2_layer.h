@@ -7,6 +7,8 @@
 
 namespace gdn2 {
 
+constexpr int kSimds = 1024;     // 256 CUs of four
+
 // V consecutive elements of T as floats, in accesses of up to 16 bytes. The caller sees to the
 // alignment (V * sizeof(T), at most 16 bytes); V = 1 needs none beyond the element's own.
 template <typename T, int V>

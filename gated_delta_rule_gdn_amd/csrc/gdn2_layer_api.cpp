@@ -145,7 +145,7 @@ size_t padded(size_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 struct ScanPlan {
     int tile, tiles;
     bool chained;
-    size_t states, sums, flags, shares;
+    size_t states, sums, flags, shares, kept_h, kept_dt;
     ScanPlan(const gdn2_scan_dims *d, bool packed, bool backward = false) {
         tile = backward ? gdn2::scan_bwd_tile(d->channels, d->groups, d->d_state, d->batch, d->seqlen, packed)
                         : gdn2::scan_tile(d->channels, d->groups, d->d_state, d->batch, d->seqlen, packed);
@@ -156,9 +156,12 @@ struct ScanPlan {
         flags = padded(static_cast<size_t>(tiles) * sizeof(int32_t));
         shares = padded(static_cast<size_t>(gdn2::scan_blocks(d->channels, d->groups, gdn2::scan_bwd_parts(d->d_state))) *
                         d->batch * d->seqlen * 2 * d->d_state * sizeof(float));
+        const size_t kept = static_cast<size_t>(d->batch) * d->seqlen / 8 + 1;
+        kept_h = padded(kept * d->d_state * d->channels * sizeof(float));
+        kept_dt = padded(kept * d->channels * sizeof(float));
     }
     size_t fwd_bytes() const { return chained ? states + sums + flags : 0; }
-    size_t bwd_bytes() const { return 2 * states + 2 * sums + flags + shares; }
+    size_t bwd_bytes() const { return 2 * states + 2 * sums + flags + shares + kept_h + kept_dt; }
 };
 
 gdn2_status check_workspace(const void *ws, size_t bytes, size_t need) {
@@ -366,12 +369,19 @@ gdn2_status gdn2_selective_scan_bwd(const void *x, const void *dt, const float *
     a.tile = p.tile; a.chained = p.chained;
     a.grad_bf16 = dims->grad_dtype == GDN2_BF16;
     char *w = static_cast<char *>(workspace);
-    a.tiles_h = reinterpret_cast<float *>(w);
-    a.tiles_g = reinterpret_cast<float *>(w + p.states);
-    a.tiles_dt = reinterpret_cast<float *>(w + 2 * p.states);
-    a.tiles_db = reinterpret_cast<float *>(w + 2 * p.states + p.sums);
-    a.tiles_pass = reinterpret_cast<int32_t *>(w + 2 * p.states + 2 * p.sums);
-    a.part_bc = reinterpret_cast<float *>(w + 2 * p.states + 2 * p.sums + p.flags);
+    auto take = [&w](size_t bytes) {
+        char *at = w;
+        w += bytes;
+        return reinterpret_cast<float *>(at);
+    };
+    a.tiles_h = take(p.states);
+    a.tiles_g = take(p.states);
+    a.tiles_dt = take(p.sums);
+    a.tiles_db = take(p.sums);
+    a.tiles_pass = reinterpret_cast<int32_t *>(take(p.flags));
+    a.part_bc = take(p.shares);
+    a.kept_h = take(p.kept_h);
+    a.kept_dt = take(p.kept_dt);
     return done(gdn2::launch_scan_bwd(a, static_cast<hipStream_t>(stream)), "gdn2_selective_scan_bwd launch");
 }
 

@@ -56,6 +56,25 @@ __device__ __forceinline__ float softplus(float x) {
     return fmaf(p, e, fmaxf(x, 0.f));
 }
 
+// softplus of K values that are the same in the S lanes of a channel: with S > 1 the lanes of either
+// half of the wave form half of them, and the halves are exchanged.
+template <int S, int K>
+__device__ __forceinline__ void softplus_shared(float (&d)[K]) {
+    if constexpr (S == 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) d[k] = softplus(d[k]);
+    } else {
+        const bool up = threadIdx.x & 32;
+#pragma unroll
+        for (int k = 0; k < K / 2; ++k) {
+            const uint32_t v = __float_as_uint(softplus(up ? d[k + K / 2] : d[k]));
+            const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+            d[k] = __uint_as_float(r[0]);
+            d[k + K / 2] = __uint_as_float(r[1]);
+        }
+    }
+}
+
 // The decay rates of a lane's states times log2(e), so that a decay is exp2(dt * A2). A rate of
 // -inf becomes the lowest value, so that a step of zero keeps the state (0 * -inf would not).
 template <int NS, int S>

@@ -7,11 +7,12 @@
 //     ddt_t  = x_t sum_n gh_t B_t + sum_n gh_t a_t h_{t-1} A,   through softplus' for the input
 //     dA     = sum_t gh_t a_t h_{t-1} dt_t,         dS0 = a_0 gh_0,   dgate = dO y silu'(gate)
 // Nothing but the inputs is kept from the forward. Four launches:
-//   1. per tile of tokens: the state it reaches from zero, its sum of dt, and what its outputs
-//      alone give back to the state that enters it (sum_t prod_{s<=t} a_s C_t dy_t);
+//   1. per tile of tokens: the state it reaches from zero, every eighth on the way, its sum of dt,
+//      and what its outputs alone give back to the state that enters it
+//      (sum_t prod_{s<=t} a_s C_t dy_t);
 //   2. both chained over the tiles, one from the front, one from the back;
-//   3. per tile: the states forward once, every eighth into LDS; then back over groups of eight
-//      tokens: their states again into registers, and the gradients from the last to the first;
+//   3. per tile, back over groups of eight tokens: their states again into registers, and the
+//      gradients from the last to the first;
 //   4. the sums over tiles (dA, dD, ddt_bias) and over workgroups of channels (dB, dC).
 // Every sum has a fixed order: the same bits at every call.
 //
@@ -96,7 +97,9 @@ __device__ __forceinline__ int spread_index(bool *writes) {
 }
 
 // Launch 1. See the head of the file; `chain` is the running product of decays, which only the
-// sequence that enters the tile needs (it is zero behind that sequence's end).
+// sequence that enters the tile needs (it is zero behind that sequence's end). Also keeps the state
+// before every eighth token of a sequence's share of the tile, and the sum of dt up to there. Such
+// places are at least eight tokens apart, so token t's are kept at t / 8.
 template <typename T, typename TG, int NS, int S>
 __global__ __launch_bounds__(256, 2) void scan_bwd_tile_kernel(ScanArgs a) {
     using Lane = ScanLane<NS, S>;
@@ -152,11 +155,13 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_tile_kernel(ScanArgs a) {
                 for (int k = 0; k < kB; ++k) dy[k] *= silu(io<T>::val(gr[k]));
             const int m = s.hi - t;
             if (m > kB) fetch(t + kB);
+            if (t > s.lo) {
+                store_tile(a, l, a.kept_h, t / kG, h);
+                if (l.on && l.part == 0) a.kept_dt[(t / kG) * static_cast<int64_t>(a.channels) + c] = sum;
+            }
 #pragma unroll
             for (int k = 0; k < kB; ++k) d[k] += bias;
-            if (a.softplus)
-#pragma unroll
-                for (int k = 0; k < kB; ++k) d[k] = softplus(d[k]);
+            if (a.softplus) softplus_shared<S>(d);
             if (m < kB)         // steps of zero: h and chain stay, and nothing comes back
 #pragma unroll
                 for (int k = 1; k < kB; ++k)
@@ -212,19 +217,16 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
     constexpr int NP = Lane::NP, CW = Lane::CW, TOP = __builtin_ctz(CW) - 1;
     constexpr int LEFT = spread_left(CW, NS);
     extern __shared__ __align__(16) float lds[];
-    // B and C of the tile [groups * kG][2][NP]; states every kG tokens [waves][groups][NS][64];
-    // the waves' dB and dC [waves][kG][2][NP]
-    const int groups_max = (a.tile + kG - 1) / kG;
-    float *s_bc = lds, *s_h = s_bc + groups_max * kG * 2 * NP;
-    float *s_red = s_h + kScanWaves * groups_max * NS * 64;
+    // B and C of the tile [groups * kG][2][NP]; the waves' dB and dC, for two groups in turn
+    // [2][waves][kG][2][NP], and a place for what lanes without a result of their own write
+    constexpr int RED = kG * 2 * NP;
+    float *s_bc = lds, *s_red = s_bc + (a.tile + kG - 1) / kG * RED, *s_none = s_red + 2 * kScanWaves * RED;
     const Lane l(a, blockIdx.x);
-    const int lane = threadIdx.x & 63;
     const int64_t tile = tile_index();
     if (tile * a.tile >= a.map.total && tile > 0) return;      // the whole workgroup
     const int t0 = static_cast<int>(tile * a.tile);
     const int t1 = a.map.total - t0 < a.tile ? a.map.total : t0 + a.tile;
     const uint32_t c = l.c;
-    float *my_h = s_h + l.wave * groups_max * NS * 64 + lane;
     float A2[NS], dA[NS];
     load_rates(a, l, A2);
 #pragma unroll
@@ -232,14 +234,15 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.D ? a.D[c] : 0.f;
     float dD = 0.f, dbias = 0.f;
     bool writes;
-    float *my_red = s_red + l.wave * kG * 2 * NP + l.n0 + spread_index<CW, NS>(&writes);
+    float *my_red = s_red + l.wave * RED + l.n0 + spread_index<CW, NS>(&writes);
+    const int other = writes ? kScanWaves * RED : 0;
+    if (!writes) my_red = s_none + (threadIdx.x & 63);
+    int turn = 0;
     const bool gated = a.gate != nullptr;
     // the step sizes of a group, zero from m on and in lanes without a channel (which then add
     // nothing to the sums over channels)
     auto steps = [&](float (&d)[kG], int m) {
-        if (a.softplus)
-#pragma unroll
-            for (int k = 0; k < kG; ++k) d[k] = softplus(d[k]);
+        if (a.softplus) softplus_shared<S>(d);
         if (m < kG)
 #pragma unroll
             for (int k = 1; k < kG; ++k)
@@ -249,7 +252,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
             for (int k = 0; k < kG; ++k) d[k] = 0.f;
     };
     for_spans(a.map, t0, t1, [&](const Span &s) {
-        float h[NS], g[NS];        // g: the gradient that comes to h_t from behind, a_{t+1} gh_{t+1}
+        float g[NS];        // the gradient that comes to h_t from behind, a_{t+1} gh_{t+1}
         if (!s.ends) {
             load_tile(a, l, a.tiles_g, tile, g);
         } else if (a.dS_T) {
@@ -257,14 +260,6 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
         } else {
 #pragma unroll
             for (int n = 0; n < NS; ++n) g[n] = 0.f;
-        }
-        if (!s.starts) {
-            load_tile(a, l, a.tiles_h, tile, h);
-        } else if (a.S0) {
-            load_state(a, l, a.S0, s.i, h);
-        } else {
-#pragma unroll
-            for (int n = 0; n < NS; ++n) h[n] = 0.f;
         }
         const int len = s.hi - s.lo, groups = (len + kG - 1) / kG;
         if (len > 0) {
@@ -281,44 +276,17 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
             }
             __syncthreads();
         }
-        // forward: the state entering every group of kG tokens
-        for (int q = 0; q < groups; ++q) {
-#pragma unroll
-            for (int n = 0; n < NS; ++n) my_h[(q * NS + n) * 64] = h[n];
-            if (q == groups - 1) break;
-            const int64_t t = s.lo + q * kG;
-            T xr[kG], dr[kG];
-            fetch_rows(static_cast<const T *>(a.dt) + t * a.dt_stride, a.dt_stride, c, kG, dr);
-            fetch_rows(static_cast<const T *>(a.x) + t * a.x_stride, a.x_stride, c, kG, xr);
-            float x[kG], d[kG];
-            widen(dr, d);
-            widen(xr, x);
-#pragma unroll
-            for (int k = 0; k < kG; ++k) d[k] += bias;
-            steps(d, kG);
-            const float *bc = s_bc + q * kG * 2 * NP + l.n0;
-#pragma unroll
-            for (int k = 0; k < kG; ++k) {
-                const float u = d[k] * x[k];
-                float b[NS];
-                lds_row<NS>(bc + k * 2 * NP, b);
-#pragma unroll
-                for (int n = 0; n < NS; ++n)
-                    h[n] = fmaf(__builtin_amdgcn_exp2f(d[k] * A2[n]), h[n], u * b[n]);
-            }
-            pin(h);
-        }
         // back, group by group
         for (int q = groups - 1; q >= 0; --q) {
             const int m = len - q * kG < kG ? len - q * kG : kG;
             const int64_t t = s.lo + q * kG;
+            float x[kG], d[kG], raw[kG], gt[kG], go[kG], hist[kG][NS];
             T xr[kG], dr[kG], gr[kG];
             TG yr[kG];
             fetch_rows(static_cast<const T *>(a.dt) + t * a.dt_stride, a.dt_stride, c, m, dr);
             fetch_rows(static_cast<const T *>(a.x) + t * a.x_stride, a.x_stride, c, m, xr);
             fetch_rows(static_cast<const TG *>(a.dO) + t * a.channels, a.channels, c, m, yr);
             if (gated) fetch_rows(static_cast<const T *>(a.gate) + t * a.gate_stride, a.gate_stride, c, m, gr);
-            float x[kG], d[kG], raw[kG], gt[kG], go[kG], hist[kG][NS], rb[kG][LEFT], rc[kG][LEFT];
             widen(dr, d);
             widen(xr, x);
             widen(yr, go);
@@ -330,8 +298,24 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
 #pragma unroll
                 for (int k = 0; k < kG; ++k)
                     if (k >= m || !l.on) x[k] = go[k] = 0.f;
+            // the state entering the group: the one that enters the span, or what launch 1 kept
+            // and, where that was reached from zero, what is left of the one that enters the tile
+            float h[NS];
+            if (!s.starts) {
+                load_tile(a, l, a.tiles_h, tile, h);
+            } else if (a.S0 && q == 0) {
+                load_state(a, l, a.S0, s.i, h);
+            } else {
 #pragma unroll
-            for (int n = 0; n < NS; ++n) h[n] = my_h[(q * NS + n) * 64];
+                for (int n = 0; n < NS; ++n) h[n] = 0.f;
+            }
+            if (q > 0) {
+                float kept[NS];
+                load_tile(a, l, a.kept_h, t / kG, kept);
+                const float cum = s.starts ? 0.f : a.kept_dt[(t / kG) * a.channels + c];
+#pragma unroll
+                for (int n = 0; n < NS; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(A2[n] * cum), h[n], kept[n]);
+            }
             const float *bc = s_bc + q * kG * 2 * NP + l.n0;
 #pragma unroll
             for (int k = 0; k < kG; ++k) {
@@ -346,6 +330,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
                 }
                 pin(hist[k]);
             }
+            float *red = my_red + turn * other;
             pin(d);        // the decays are formed again below: kept, they would take kG * NS registers
 #pragma unroll
             for (int k = kG - 1; k >= 0; --k) {
@@ -372,7 +357,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
                     }
                     reduce_spread<TOP, NS>(p);
 #pragma unroll
-                    for (int i = 0; i < LEFT; ++i) rc[k][i] = p[i];
+                    for (int i = 0; i < LEFT; ++i) red[k * 2 * NP + NP + i] = p[i];
                 }
                 {
                     float p[NS];
@@ -386,7 +371,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
                     }
                     reduce_spread<TOP, NS>(p);
 #pragma unroll
-                    for (int i = 0; i < LEFT; ++i) rb[k][i] = p[i];
+                    for (int i = 0; i < LEFT; ++i) red[k * 2 * NP + i] = p[i];
                 }
                 sB = sum_parts<S>(sB);
                 float dd = fmaf(x[k], sB, sum_parts<S>(sA) * (1.f / kLog2e));
@@ -408,8 +393,6 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
                 dbias = out[4];
                 pin(g);
                 pin(dA);
-                pin(rb[k]);
-                pin(rc[k]);
             }
             if (l.on && l.part == 0) {
                 TG *px = static_cast<TG *>(a.dx) + t * a.channels, *pd = static_cast<TG *>(a.ddt) + t * a.channels;
@@ -431,15 +414,6 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
                     }
                 }
             }
-            __syncthreads();       // the group behind is done with s_red
-            if (writes)
-#pragma unroll
-                for (int k = 0; k < kG; ++k)
-#pragma unroll
-                    for (int i = 0; i < LEFT; ++i) {
-                        my_red[k * 2 * NP + i] = rb[k][i];
-                        my_red[k * 2 * NP + NP + i] = rc[k][i];
-                    }
             __syncthreads();
             // the waves' shares of dB and dC, added in their order
             for (int e = threadIdx.x; e < m * 2 * NP; e += 256) {
@@ -447,9 +421,10 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
                 if (n >= a.d_state) continue;
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < kScanWaves; ++w) v += s_red[w * kG * 2 * NP + e];
+                for (int w = 0; w < kScanWaves; ++w) v += s_red[(turn * kScanWaves + w) * RED + e];
                 a.part_bc[((static_cast<int64_t>(blockIdx.x) * a.map.total + t + k) * 2 + (j >= NP)) * a.d_state + n] = v;
             }
+            turn ^= 1;
         }
         if (s.starts && a.dS0) store_state(a, l, a.dS0, s.i, g);
     });
@@ -516,17 +491,25 @@ hipError_t launch_bwd(const ScanArgs &a, hipStream_t st) {
     const int tiles = scan_tiles(a.map.total, a.tile), blocks = scan_blocks(a.channels, a.groups, S);
     const dim3 grid = scan_grid(blocks, tiles);
     const int64_t cols = static_cast<int64_t>(a.d_state) * a.channels;
+    if (a.chained || a.tile > kG) {
+        // sixteen states per lane where two waves per SIMD are left (a channel's step and gate are
+        // then formed by half the lanes: 62.4 against 70.7 us on 4,096 tokens x 2,048 channels x 16
+        // states; with one wave 34.5 against 28.8 us, 1,011 x 1,002 x 24)
+        constexpr int N1 = S > 1 ? 2 * NS : NS, S1 = S > 1 ? S / 2 : 1;
+        const int wide = scan_blocks(a.channels, a.groups, S1);
+        if (static_cast<int64_t>(wide) * tiles * kScanWaves >= 2 * kSimds)
+            hipLaunchKernelGGL((scan_bwd_tile_kernel<T, TG, N1, S1>), scan_grid(wide, tiles), dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL((scan_bwd_tile_kernel<T, TG, NS, S>), grid, dim3(256), 0, st, a);
+    }
     if (a.chained) {
-        hipLaunchKernelGGL((scan_bwd_tile_kernel<T, TG, NS, S>), grid, dim3(256), 0, st, a);
         hipLaunchKernelGGL(scan_bwd_chain_kernel, dim3(static_cast<unsigned>((cols + 255) / 256), 2),
                            dim3(256), 0, st, a, tiles);
     }
-    const size_t groups = (a.tile + kG - 1) / kG;
-    const size_t lds = sizeof(float) * (groups * kG * 2 * NS * S + kScanWaves * groups * NS * 64 +
-                                        kScanWaves * kG * 2 * NS * S);
-    static_assert(kScanMaxBwdTile % kG == 0, "whole groups of tokens in a tile");
-    static_assert(sizeof(float) * (kScanMaxBwdTile * 2 * NS * S + kScanWaves * (kScanMaxBwdTile / kG) * NS * 64 +
-                                   kScanWaves * kG * 2 * NS * S) <= 160 * 1024, "a tile fits the LDS");
+    constexpr int RED = kG * 2 * NS * S, FIXED = (2 * kScanWaves + 1) * RED + 64;
+    const size_t lds = sizeof(float) * (static_cast<size_t>((a.tile + kG - 1) / kG) * RED + FIXED);
+    static_assert(kB == kG, "what launch 1 keeps at its batches is what launch 3 reads at its groups");
+    static_assert(sizeof(float) * (kScanMaxBwdTile / kG * RED + FIXED) <= 160 * 1024, "a tile fits the LDS");
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(scan_bwd_kernel<T, TG, NS, S>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(lds));
@@ -571,7 +554,7 @@ int scan_bwd_tile(int channels, int groups, int d_state, int batch, int seqlen, 
     if (!packed && seqlen <= kScanMaxBwdTile) return seqlen > 0 ? seqlen : 1;
     const int64_t total = static_cast<int64_t>(batch) * seqlen;
     const int64_t waves = static_cast<int64_t>(kScanWaves) * scan_blocks(channels, groups, scan_bwd_parts(d_state));
-    const int64_t t = (total * waves / 2048 + kG - 1) / kG * kG;
+    const int64_t t = (total * waves / (2 * kSimds) + kG - 1) / kG * kG;
     return t < kG ? kG : t > kScanMaxBwdTile ? kScanMaxBwdTile : static_cast<int>(t);
 }
 
