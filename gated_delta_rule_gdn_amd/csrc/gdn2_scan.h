@@ -75,14 +75,20 @@ __device__ __forceinline__ void softplus_shared(float (&d)[K]) {
     }
 }
 
-// The decay rates of a lane's states times log2(e), so that a decay is exp2(dt * A2). A rate of
-// -inf becomes the lowest value, so that a step of zero keeps the state (0 * -inf would not).
+// A decay rate times log2(e), so that a decay is exp2(dt * rate2(A)). A rate of -inf becomes the
+// lowest value, so that a step of zero keeps the state (0 * -inf would not).
+__device__ __forceinline__ float rate2(float A) {
+    const float r = kLog2e * A;
+    return r == -__builtin_inff() ? -3.4e38f : r;
+}
+
+// The decay rates of a lane's states.
 template <int NS, int S>
 __device__ __forceinline__ void load_rates(const ScanArgs &a, const ScanLane<NS, S> &l, float (&A2)[NS]) {
     const float *A = a.A + static_cast<int64_t>(l.c) * a.d_state;
 #pragma unroll
     for (int n = 0; n < NS; ++n)
-        A2[n] = l.on && l.n0 + n < a.d_state ? fmaxf(kLog2e * A[l.n0 + n], -3.4e38f) : 0.f;
+        A2[n] = l.on && l.n0 + n < a.d_state ? rate2(A[l.n0 + n]) : 0.f;
 }
 
 // A lane's states from / to a row of [N][channels][d_state].
@@ -204,7 +210,7 @@ __device__ __forceinline__ void chain_tiles(const ScanArgs &a, float *states, in
     if (col >= cols) return;
     const int n = static_cast<int>(col / a.channels);
     const int c = static_cast<int>(col - static_cast<int64_t>(n) * a.channels);
-    const float A2 = kLog2e * a.A[static_cast<int64_t>(c) * a.d_state + n];
+    const float A2 = rate2(a.A[static_cast<int64_t>(c) * a.d_state + n]);
     float run = 0.f;
     constexpr int U = 16;
     for (int i0 = 0; i0 < tiles; i0 += U) {

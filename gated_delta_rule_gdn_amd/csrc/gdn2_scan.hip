@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepArgs a) {
     float A2[4];
     rates.get(A2, n0, states);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) A2[j] *= kLog2e;
+    for (int j = 0; j < 4; ++j) A2[j] = rate2(A2[j]);
     for (; i < a.num_seqs; i += gridDim.y) {
         const int mine = slot;
         const Four<TS, VEC> old = next;

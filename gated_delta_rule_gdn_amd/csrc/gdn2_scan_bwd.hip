@@ -96,8 +96,9 @@ __device__ __forceinline__ int spread_index(bool *writes) {
     return n;
 }
 
-// Launch 1. See the head of the file; `chain` is the running product of decays, which only the
-// sequence that enters the tile needs (it is zero behind that sequence's end). Also keeps the state
+// Launch 1. See the head of the file; `chain` is the running product of decays. Only the sequence
+// that enters the tile gives anything back, which is stored where that sequence's share ends, so
+// that nothing of the next one can reach it. Also keeps the state
 // before every eighth token of a sequence's share of the tile, and the sum of dt up to there. Such
 // places are at least eight tokens apart, so token t's are kept at t / 8.
 template <typename T, typename TG, int NS, int S>
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_tile_kernel(ScanArgs a) {
     load_rates(a, l, A2);
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
     float sum = 0.f;
-    bool pass = false;
+    bool pass = false, entered = false;
 #pragma unroll
     for (int n = 0; n < NS; ++n) { h[n] = 0.f; back[n] = 0.f; chain[n] = 1.f; }
     for_spans(a.map, t0, t1, [&](const Span &s) {
@@ -124,8 +125,6 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_tile_kernel(ScanArgs a) {
             else
 #pragma unroll
                 for (int n = 0; n < NS; ++n) h[n] = 0.f;
-#pragma unroll
-            for (int n = 0; n < NS; ++n) chain[n] = 0.f;
         }
         pass = !s.starts && !s.ends;
         Stage<T, NP, true> st;
@@ -188,17 +187,23 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_tile_kernel(ScanArgs a) {
             if (m > kB) st.put(s_bc[buf ^ 1]);
             __syncthreads();
         }
-        if (!s.starts && s.ends) {
-            if (a.dS_T) {
+        if (!s.starts) {
+            if (s.ends && a.dS_T) {
                 float g[NS];
                 load_state(a, l, a.dS_T, s.i, g);
 #pragma unroll
                 for (int n = 0; n < NS; ++n) back[n] = fmaf(chain[n], g[n], back[n]);
             }
+            store_tile(a, l, a.tiles_g, tile, back);
+            entered = true;
         }
     });
     store_tile(a, l, a.tiles_h, tile, h);
-    store_tile(a, l, a.tiles_g, tile, back);
+    if (!entered) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) back[n] = 0.f;
+        store_tile(a, l, a.tiles_g, tile, back);
+    }
     if (l.on && l.part == 0) a.tiles_dt[tile * a.channels + c] = sum;
     if (blockIdx.x == 0 && threadIdx.x == 0) a.tiles_pass[tile] = pass ? 1 : 0;
 }

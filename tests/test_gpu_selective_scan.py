@@ -283,3 +283,31 @@ def test_refusals():
         call(d, final_state=d["S0"])                           # in place
     with pytest.raises(TypeError):
         g.selective_scan_step(d["x"], d["dt"], d["A"], d["B"], d["C"], d["S0"].half())
+
+
+@pytest.mark.parametrize("T", [12, 200])
+def test_rates_of_minus_infinity_and_nan(T):
+    """A rate of -inf forgets at every step but keeps the state over steps of zero, over a tile's
+    bounds and in single tokens alike. A NaN rate spoils its channel and no other."""
+    h = make((1, T), 10, 16, 1, 1, torch.float32, seed=15)
+    h["A"][3, 2] = float("-inf")
+    h["dt"][:, T // 4:] = float("-inf")
+    d = gpu(h)
+    o, S = call(d)
+    r = ref({**h, "dt": h["dt"].clamp(min=-300.0), "A": h["A"].clamp(min=-1e30)}, [T])
+    check("o", o[0], r["o"], r["o_b"])
+    check("S_T", S, r["S_T"], r["S_T_b"])
+    pool = d["S0"].clone()
+    steps = []
+    for t in range(T):
+        x, dt, B, C, gate = (d[n][:, t:t + 1] for n in ("x", "dt", "B", "C", "gate"))
+        steps.append(g.selective_scan_step(x, dt, d["A"], B, C, pool, D=d["D"], gate=gate,
+                                           dt_bias=d["dt_bias"], dt_softplus=True)[0])
+    check("o by steps", torch.cat(steps), r["o"], r["o_b"])
+    check("S by steps", pool, r["S_T"], r["S_T_b"])
+    d["A"][5, 1] = float("nan")
+    bad, Sb = call(d)
+    torch.cuda.synchronize()
+    keep = [c for c in range(10) if c != 5]
+    assert torch.isnan(bad[0, :, 5]).all() and torch.isnan(Sb[0, 5]).any()
+    assert torch.equal(bad[:, :, keep], o[:, :, keep]) and torch.equal(Sb[0, keep], S[0, keep])

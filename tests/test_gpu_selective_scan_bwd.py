@@ -189,3 +189,50 @@ def test_refusals():
         call(d, dO, torch.zeros(2, 8, 4, device="cuda"))
     with pytest.raises(g.GDN2Error):
         call(d, dO, None, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("name", ["x", "dt", "B", "C", "gate", "dO", "S0", "dS_T"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_stay_in_their_sequence(name, bad):
+    """The middle one of three sequences, which meet inside tiles, holds NaN or infinities from
+    its start to its end: the bits of the others' gradients do not change."""
+    lens = [300, 90, 200]
+    h = make((1, 590), 24, 16, 1, 3, torch.float32, seed=14)
+    d = gpu(h)
+    q = Draw(5)
+    d["dO"], d["dS_T"] = q.normal(1, 590, 24).cuda(), q.normal(3, 24, 16).cuda()
+    clean = call(d, d["dO"], d["dS_T"], cu_seqlens=cu_of(lens))
+    if name in ("S0", "dS_T"):
+        d[name][1] = bad
+    else:
+        d[name][:, 300:390] = bad
+    o = call(d, d["dO"], d["dS_T"], cu_seqlens=cu_of(lens))
+    torch.cuda.synchronize()
+    for n in ("dx", "ddt", "dB", "dC", "dgate"):
+        for s in (slice(0, 300), slice(390, 590)):
+            assert torch.equal(o[n][:, s], clean[n][:, s]), n
+    assert torch.equal(o["dS0"][[0, 2]], clean["dS0"][[0, 2]])
+    assert not all(torch.equal(o[n], clean[n]) for n in o)
+
+
+def test_rates_of_minus_infinity_and_nan():
+    """A rate of -inf forgets at every step but keeps the state over steps of zero; the gradients
+    of inputs, B, C and gate stay finite. A NaN rate spoils its channel and no other."""
+    h = make((1, 200), 10, 16, 1, 2, torch.float32, seed=15)
+    h["A"][3, 2] = float("-inf")
+    h["dt"][:, 40:180] = float("-inf")
+    d = gpu(h)
+    q = Draw(6)
+    dO, dS = q.normal(1, 200, 10).cuda(), q.normal(2, 10, 16).cuda()
+    cu = cu_of([190, 10])
+    o = call(d, dO, dS, cu_seqlens=cu)
+    v = flat({**h, "dt": h["dt"].clamp(min=-300.0), "A": h["A"].clamp(min=-1e30)}, 200)
+    r = scan_bwd_ref(*ref_args(v, True, [190, 10]), f64(dO)[0], f64(dS))
+    for n in ("dx", "dB", "dC", "dgate"):
+        check(n, o[n][0], r[n], r[n + "_b"])
+    d["A"][5, 1] = float("nan")
+    bad = call(d, dO, dS, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    keep = [c for c in range(10) if c != 5]
+    assert torch.isnan(bad["dx"][0, :100, 5]).all()
+    assert torch.equal(bad["dx"][:, :, keep], o["dx"][:, :, keep])
