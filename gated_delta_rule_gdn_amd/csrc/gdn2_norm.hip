@@ -94,7 +94,8 @@ template <typename T, typename TR, int L, int V, int P>
 __global__ __launch_bounds__(norm_threads(L)) void norm_fwd_kernel(NormArgs a) {
     constexpr int ROWS = norm_threads(L) / L;          // rows of a workgroup
     __shared__ float s_sum[2][16];
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / L;
+    const int64_t set = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t row = set * ROWS + threadIdx.x / L;
     if (row >= a.rows) return;                          // L > 64: ROWS is 1, whole workgroups
     const Cols<V, P> k{static_cast<int>(threadIdx.x % L) * V, L * V, a.d};
     const float inv = 1.f / a.d;
@@ -328,6 +329,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormArgs a, int parts
     out[col] = sum;
 }
 
+constexpr int kNormGridX = 1 << 20;
 constexpr int kNormGroups = 768;      // workgroups of a backward pass: three per CU
 
 template <typename T, typename TR, typename TG, typename TGR, int L, int V, int P>
@@ -335,8 +337,10 @@ hipError_t launch(const NormArgs &a, bool backward, hipStream_t st) {
     constexpr int THREADS = norm_threads(L), ROWS = THREADS / L;
     const int64_t sets = norm_sets(a.rows, a.d);
     if (!backward) {
-        hipLaunchKernelGGL((norm_fwd_kernel<T, TR, L, V, P>), dim3(static_cast<unsigned>(sets)),
-                           dim3(THREADS), 0, st, a);
+        // one dimension of a grid holds less than 2^32 threads
+        const unsigned gx = static_cast<unsigned>(sets < kNormGridX ? sets : kNormGridX);
+        const unsigned gy = static_cast<unsigned>((sets + gx - 1) / gx);
+        hipLaunchKernelGGL((norm_fwd_kernel<T, TR, L, V, P>), dim3(gx, gy), dim3(THREADS), 0, st, a);
         return hipGetLastError();
     }
     const unsigned groups = static_cast<unsigned>(sets < kNormGroups ? sets : kNormGroups);

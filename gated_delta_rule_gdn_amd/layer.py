@@ -14,7 +14,8 @@ norms around a block.
 As in the rest of the package, these functions check shapes, allocate outputs and workspaces
 and call the C ABI (``include/gdn2.h``) on the current HIP stream of the tensors' device. Token
 inputs may be column slices of a wider tensor (one stride from token to token); everything else
-is contiguous. Gradients are returned in a dict, ``d`` before each input's name: those of token
+is contiguous. Rows behind the last sequence of a packed batch are not written, in outputs and
+gradients alike. Gradients are returned in a dict, ``d`` before each input's name: those of token
 tensors in the type of the incoming gradient, those of parameters and states in fp32.
 """
 from __future__ import annotations
@@ -149,10 +150,17 @@ def _sequences(cu_seqlens, B: int, dev) -> Tuple[int, int]:
     _need_gpu("cu_seqlens", cu_seqlens, dev)
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1:
         raise TypeError("cu_seqlens must be a 1-D int32 tensor")
-    N = cu_seqlens.numel() - 1
+    N = _fits("the number of sequences", cu_seqlens.numel() - 1)
     if N < 1 or B != 1:
         raise ValueError("a packed batch is [1,T,..] with cu_seqlens of N+1 >= 2 offsets")
     return N, N
+
+
+def _fits(name: str, value: int, limit: int = (1 << 31) - 1) -> int:
+    """A size that the C structs hold in 32 bits; the C ABI checks everything smaller."""
+    if value > limit:
+        raise ValueError(f"{name} is {value}, at most {limit}")
+    return value
 
 
 def _workspace(workspace, need: int, dev) -> torch.Tensor:
@@ -171,6 +179,8 @@ def _conv_dims(x, weight, bias, cu_seqlens, silu, grad_code) -> Tuple[ConvDims, 
     if x.dim() != 3:
         raise ValueError("x must be [B,T,C]")
     B, T, C = x.shape
+    _fits("the number of tokens", B * T)
+    _fits("channels", C)
     code = _dtype_code(x.dtype)
     step = _tokens("x", x, dev, x.dtype, x.shape, C)
     if weight.dim() != 2 or weight.shape[0] != C:
@@ -265,7 +275,7 @@ def short_conv_step(x, weight, conv_state, bias: Optional[torch.Tensor] = None,
     dev, shape = x.device, x.shape
     if conv_state.dim() != 3:
         raise ValueError(f"conv_state must be fp32 [num_slots,{d.width - 1},{d.channels}]")
-    slots = conv_state.shape[0]
+    slots = _fits("the number of slots", conv_state.shape[0])
     ps = _whole("conv_state", conv_state, dev, torch.float32, (slots, d.width - 1, d.channels))
     y = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
     py = _whole("out", y, dev, x.dtype, shape)
@@ -277,15 +287,22 @@ def short_conv_step(x, weight, conv_state, bias: Optional[torch.Tensor] = None,
 # ---- selective scan ----------------------------------------------------------------------
 
 
+def _batch(x) -> int:
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,channels]")
+    return x.shape[0]
+
+
 def _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, num_seqs, grad_code) -> ScanDims:
     """The checked dims of a scan call."""
     dev, dtype, shape = _gpu_of("x", x), x.dtype, x.shape
-    if x.dim() != 3:
-        raise ValueError("x must be [B,T,channels]")
+    _batch(x)
     if B.dim() != 4:
         raise ValueError("B and C must be [B,T,groups,d_state]")
     n, T, ch = shape
     G, M = B.shape[2], B.shape[3]
+    _fits("the number of tokens", n * T)
+    _fits("channels", max(ch, G * M))
     code, bc = _dtype_code(dtype), (n, T, G, M)
     strides = [_tokens("x", x, dev, dtype, shape, ch), _tokens("dt", dt, dev, dtype, shape, ch),
                _tokens("B", B, dev, dtype, bc, G * M), _tokens("C", C, dev, dtype, bc, G * M),
@@ -318,7 +335,7 @@ def selective_scan_fwd(x, dt, A, B, C, D: Optional[torch.Tensor] = None,
     a column slice); A fp32 [channels,d_state]; D, dt_bias fp32 [channels]; dt_softplus: the
     step is softplus(dt + dt_bias); S0 fp32 [N,channels,d_state]; cu_seqlens int32 [N+1] for a
     packed batch. Returns (o [B,T,channels], S_T fp32 [N,channels,d_state] or None)."""
-    N, num_seqs = _sequences(cu_seqlens, x.shape[0], _gpu_of("x", x))
+    N, num_seqs = _sequences(cu_seqlens, _batch(x), _gpu_of("x", x))
     d = _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, num_seqs, 0)
     dev, shape, f32 = x.device, x.shape, torch.float32
     st_shape = (N, d.channels, d.d_state)
@@ -356,7 +373,7 @@ def selective_scan_bwd(x, dt, A, B, C, dO, D: Optional[torch.Tensor] = None,
     """Gradients of selective_scan_fwd given dO = dL/do [B,T,channels] (x's dtype or fp32) and
     dS_T = dL/dS_T (None: zero). Returns dx, ddt, dB, dC (and dgate) in dO's dtype, dA (and dD,
     ddt_bias, dS0) in fp32, each optional one for the argument given."""
-    N, num_seqs = _sequences(cu_seqlens, x.shape[0], _gpu_of("x", x))
+    N, num_seqs = _sequences(cu_seqlens, _batch(x), _gpu_of("x", x))
     d = _scan_dims(x, dt, A, B, C, D, gate, dt_bias, dt_softplus, num_seqs,
                    _grad_code("dO", dO, x.dtype))
     dev, shape, f32 = x.device, x.shape, torch.float32
@@ -398,7 +415,7 @@ def selective_scan_step(x, dt, A, B, C, state, D: Optional[torch.Tensor] = None,
         raise ValueError(f"state must be [num_slots,{d.channels},{d.d_state}]")
     if state.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("state must be float32 or bfloat16")
-    slots = state.shape[0]
+    slots = _fits("the number of slots", state.shape[0])
     ps = _whole("state", state, dev, state.dtype, (slots, d.channels, d.d_state))
     o = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
     po = _whole("out", o, dev, x.dtype, shape)
@@ -440,7 +457,7 @@ def _norm_dims(x, gate, residual, norm_weight, scale, next_weight, eps, grad_cod
     dev, dtype, shape = _gpu_of("x", x), x.dtype, x.shape
     if x.dim() < 1:
         raise ValueError("x must be [*rows,d]")
-    d = shape[-1]
+    d = _fits("d", shape[-1])
     code = _dtype_code(dtype)
     xs = _rows("x", x, dev, dtype, shape)
     gs = 0 if gate is None else _rows("gate", gate, dev, dtype, shape)

@@ -634,7 +634,7 @@ typedef struct gdn2_norm_dims {
     int32_t residual_dtype;            /* of residual and h: GDN2_F32 or dtype */
     int32_t grad_dtype;                /* of dy, dx, dgate (backward only). dh and dresidual have
                                           it too, and GDN2_F32 with a GDN2_F32 residual */
-    float eps;                         /* >= 0 */
+    float eps;                         /* >= 0; with 0 a row of zeros gives NaN */
     int64_t x_stride, gate_stride;     /* elements between rows, >= d, or 0 */
 } gdn2_norm_dims;
 

@@ -164,3 +164,17 @@ def test_refusals():
         g.block_norm_bwd(c["x"])
     with pytest.raises(TypeError):
         g.block_norm_bwd(c["x"], dh=c["x"].half())
+
+
+def test_more_rows_than_one_grid_dimension_holds():
+    """2^28 + 5 rows of two columns: 16 lanes a row would be more than 2^32 threads in a row."""
+    rows = (1 << 28) + 5
+    x = torch.zeros(rows, 2, dtype=torch.bfloat16, device="cuda")
+    picked = [0, 1, 12345678, (1 << 28) - 1, 1 << 28, rows - 1]
+    x[picked] = torch.tensor([3.0, 4.0], dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(2, device="cuda")
+    h, _ = g.block_norm_fwd(x, norm_weight=w, eps=1e-5)
+    torch.cuda.synchronize()
+    want = torch.tensor([3.0, 4.0]) / 12.5 ** 0.5       # 1e-5 of 12.5 is below half a bf16 step
+    assert torch.equal(h[picked].cpu(), want.to(torch.bfloat16).expand(len(picked), 2))
+    assert int(torch.count_nonzero(h)) == 2 * len(picked)

@@ -255,3 +255,33 @@ def test_refusals():
         g.short_conv_step(x.expand(2, 4, 8).contiguous(), w, st)   # two sequences, one slot
     with pytest.raises(ValueError):
         g.short_conv_fwd(x, w, out=torch.zeros(1, 4, 9, device="cuda"))
+
+
+@pytest.mark.parametrize("name", ["x", "dy", "state0", "dstate_T"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_stay_in_their_sequence(name, bad):
+    """The middle one of three sequences, which meet inside tiles, holds NaN or infinities: the
+    bits of the others' outputs and gradients do not change."""
+    gen = torch.Generator().manual_seed(31)
+    n = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    w, b = n(20, 4), n(20)
+    d = {"x": n(1, 90, 20), "dy": n(1, 90, 20), "state0": n(3, 3, 20), "dstate_T": n(3, 3, 20)}
+    cu = torch.tensor([0, 41, 50, 90], dtype=torch.int32, device="cuda")
+
+    def run():
+        y, s = g.short_conv_fwd(d["x"], w, b, d["state0"], cu, silu=True)
+        o = g.short_conv_bwd(d["x"], w, d["dy"], b, d["state0"], cu, silu=True, dstate_T=d["dstate_T"])
+        return y, o["dx"], s, o["dstate0"]
+
+    clean = run()
+    if name in ("x", "dy"):
+        d[name][:, 41:50] = bad
+    else:
+        d[name][1] = bad
+    got = run()
+    torch.cuda.synchronize()
+    for a, c in zip(got[:2], clean[:2]):
+        assert torch.equal(a[:, :41], c[:, :41]) and torch.equal(a[:, 50:], c[:, 50:])
+    for a, c in zip(got[2:], clean[2:]):
+        assert torch.equal(a[[0, 2]], c[[0, 2]])
+    assert not all(torch.equal(a, c) for a, c in zip(got, clean))

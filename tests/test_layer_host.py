@@ -204,3 +204,11 @@ def test_selective_scan_backward_refusals(L):
     assert scan_bwd(L, dx=P(6), ws=None) == WORKSPACE
     assert scan_bwd(L, dx=P(6), nbytes=need - 1) == WORKSPACE
     assert scan_bwd(L, dx=P(6), ws=ctypes.c_void_p(0x10008)) == WORKSPACE
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """Python's sizes are checked before they go into the 32-bit fields of the dims."""
+    from gated_delta_rule_gdn_amd import layer
+    assert layer._fits("n", (1 << 31) - 1) == (1 << 31) - 1
+    with pytest.raises(ValueError, match="the number of tokens"):
+        layer._fits("the number of tokens", 1 << 31)
