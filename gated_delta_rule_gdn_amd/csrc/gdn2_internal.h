@@ -163,6 +163,7 @@ struct ScanArgs {
     int64_t x_stride, dt_stride, b_stride, c_stride, gate_stride;
     int channels, d_state, groups, tile;
     bool softplus, bf16;
+    bool vec;                        // rows of d_state floats can be taken in whole pieces of four
     bool chained;                    // sequences reach over tiles: the arrays below are used
     float *tiles_h = nullptr;        // [tiles][d_state][channels]: states reached, then entering
     float *tiles_dt = nullptr;       // [tiles][channels]: sums of dt

@@ -3,6 +3,8 @@
 // enqueued, so a rejected call has no effect on the device.
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "gdn2.h"
 #include "gdn2_internal.h"
 
@@ -135,6 +137,14 @@ void scan_inputs(Args *a, const gdn2_scan_dims *d, const void *x, const void *dt
     a->channels = d->channels; a->d_state = d->d_state; a->groups = d->groups;
     a->softplus = d->dt_softplus != 0;
     a->bf16 = d->dtype == GDN2_BF16;
+}
+
+// Whether rows of d_state floats can be taken in pieces of 16 bytes.
+bool d_state_pieces(const gdn2_scan_dims *d, std::initializer_list<const float *> rows) {
+    if (d->d_state % 4 != 0) return false;
+    for (const float *p : rows)
+        if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+    return true;
 }
 
 constexpr size_t kAlign = 256;
@@ -321,6 +331,7 @@ gdn2_status gdn2_selective_scan_fwd(const void *x, const void *dt, const float *
     a.S0 = S0; a.o = o; a.S_T = S_T;
     a.map = seq_map(cu_seqlens, dims->batch, dims->seqlen, dims->num_seqs);
     a.tile = p.tile; a.chained = p.chained;
+    a.vec = d_state_pieces(dims, {A, S0, S_T});
     if (p.chained) {
         char *w = static_cast<char *>(workspace);
         a.tiles_h = reinterpret_cast<float *>(w);
@@ -367,6 +378,7 @@ gdn2_status gdn2_selective_scan_bwd(const void *x, const void *dt, const float *
     a.dD = D ? dD : nullptr; a.dgate = gate ? dgate : nullptr; a.ddt_bias = dt_bias ? ddt_bias : nullptr;
     a.map = seq_map(cu_seqlens, dims->batch, dims->seqlen, dims->num_seqs);
     a.tile = p.tile; a.chained = p.chained;
+    a.vec = d_state_pieces(dims, {A, S0, dS_T, dS0});
     a.grad_bf16 = dims->grad_dtype == GDN2_BF16;
     char *w = static_cast<char *>(workspace);
     auto take = [&w](size_t bytes) {

@@ -82,30 +82,53 @@ __device__ __forceinline__ float rate2(float A) {
     return r == -__builtin_inff() ? -3.4e38f : r;
 }
 
+// A lane's states of one channel's row of d_state floats: zero where there is none, in whole pieces
+// of four where ScanArgs::vec allows.
+template <int NS, int S>
+__device__ __forceinline__ void load_row(const ScanArgs &a, const ScanLane<NS, S> &l, const float *row,
+                                         float (&h)[NS]) {
+    if (a.vec) {
+#pragma unroll
+        for (int n = 0; n < NS; n += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(row + (l.n0 + n < a.d_state ? l.n0 + n : 0));
+            h[n] = v.x; h[n + 1] = v.y; h[n + 2] = v.z; h[n + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) h[n] = row[l.n0 + n < a.d_state ? l.n0 + n : 0];
+    }
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = l.on && l.n0 + n < a.d_state ? h[n] : 0.f;
+}
+
 // The decay rates of a lane's states.
 template <int NS, int S>
 __device__ __forceinline__ void load_rates(const ScanArgs &a, const ScanLane<NS, S> &l, float (&A2)[NS]) {
-    const float *A = a.A + static_cast<int64_t>(l.c) * a.d_state;
+    load_row(a, l, a.A + static_cast<int64_t>(l.c) * a.d_state, A2);
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-        A2[n] = l.on && l.n0 + n < a.d_state ? rate2(A[l.n0 + n]) : 0.f;
+    for (int n = 0; n < NS; ++n) A2[n] = rate2(A2[n]);
 }
 
-// A lane's states from / to a row of [N][channels][d_state].
+// A lane's states of sequence i from / to [num_seqs][channels][d_state].
 template <int NS, int S>
 __device__ __forceinline__ void load_state(const ScanArgs &a, const ScanLane<NS, S> &l, const float *s,
                                            int i, float (&h)[NS]) {
-    const float *p = s + (static_cast<int64_t>(i) * a.channels + l.c) * a.d_state;
-#pragma unroll
-    for (int n = 0; n < NS; ++n) h[n] = l.on && l.n0 + n < a.d_state ? p[l.n0 + n] : 0.f;
+    load_row(a, l, s + (static_cast<int64_t>(i) * a.channels + l.c) * a.d_state, h);
 }
 template <int NS, int S>
 __device__ __forceinline__ void store_state(const ScanArgs &a, const ScanLane<NS, S> &l, float *s, int i,
                                             const float (&h)[NS]) {
     float *p = s + (static_cast<int64_t>(i) * a.channels + l.c) * a.d_state;
+    if (a.vec) {
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-        if (l.on && l.n0 + n < a.d_state) p[l.n0 + n] = h[n];
+        for (int n = 0; n < NS; n += 4)
+            if (l.on && l.n0 + n < a.d_state)
+                *reinterpret_cast<f32x4 *>(p + l.n0 + n) = f32x4{h[n], h[n + 1], h[n + 2], h[n + 3]};
+    } else {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            if (l.on && l.n0 + n < a.d_state) p[l.n0 + n] = h[n];
+    }
 }
 
 // The same from / to a tile's row of a workspace [tiles][d_state][channels] (neighbouring lanes
@@ -125,6 +148,35 @@ __device__ __forceinline__ void store_tile(const ScanArgs &a, const ScanLane<NS,
 #pragma unroll
     for (int n = 0; n < NS; ++n)
         if (l.on && l.n0 + n < a.d_state) p[static_cast<int64_t>(l.n0 + n) * a.channels] = h[n];
+}
+
+// The state that enters a tile, chained here from the tiles that sequence `s` reaches through
+// before it: what chain_tiles leaves in the workspace.
+template <int NS, int S>
+__device__ __forceinline__ void walk_tiles(const ScanArgs &a, const ScanLane<NS, S> &l, const Span &s,
+                                           int64_t tile, const float (&A2)[NS], float (&h)[NS]) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = 0.f;
+    constexpr int U = 8;       // tiles whose loads are in flight together
+    for (int64_t i0 = s.first / a.tile; i0 < tile; i0 += U) {
+        float hl[U][NS], dl[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int64_t i = i0 + k < tile ? i0 + k : tile - 1;
+            const float *p = a.tiles_h + i * a.d_state * a.channels + l.c;
+            dl[k] = a.tiles_dt[i * a.channels + l.c];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                hl[k][n] = p[static_cast<int64_t>(l.n0 + n < a.d_state ? l.n0 + n : 0) * a.channels];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (i0 + k < tile)
+#pragma unroll
+                for (int n = 0; n < NS; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(A2[n] * dl[k]), h[n], hl[k][n]);
+    }
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = l.on && l.n0 + n < a.d_state ? h[n] : 0.f;
 }
 
 constexpr int kB = 8;        // tokens whose inputs are in flight and whose B and C are staged together

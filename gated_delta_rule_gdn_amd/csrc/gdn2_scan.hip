@@ -25,6 +25,8 @@ namespace gdn2 {
 
 namespace {
 
+constexpr int kFew = 4;      // states per lane where there are few tokens: see few()
+
 // FINAL: runs a tile from its true state and writes o (and S_T). Otherwise: runs it from zero
 // and writes its state, its sum of dt and whether one sequence passes through all of it.
 // A batch of kB tokens has no branch between its tokens, so their LDS reads and arithmetic
@@ -51,7 +53,8 @@ __global__ __launch_bounds__(256, FINAL ? 3 : 4) void scan_fwd_kernel(ScanArgs a
     for (int n = 0; n < NS; ++n) h[n] = 0.f;
     for_spans(a.map, t0, t1, [&](const Span &s) {
         if (!s.starts && FINAL) {
-            load_tile(a, l, a.tiles_h, tile, h);
+            if constexpr (NS == kFew) walk_tiles(a, l, s, tile, A2, h);
+            else load_tile(a, l, a.tiles_h, tile, h);
         } else if (s.starts && a.S0) {
             load_state(a, l, a.S0, s.i, h);
         } else {
@@ -268,15 +271,43 @@ hipError_t launch_fwd(const ScanArgs &a, hipStream_t st) {
     if (a.chained) {        // what the last tile reaches goes nowhere
         hipLaunchKernelGGL((scan_fwd_kernel<T, NS, S, false>), scan_grid(blocks, tiles - 1), dim3(256), 0, st, a);
         const int64_t cols = static_cast<int64_t>(a.d_state) * a.channels;
-        hipLaunchKernelGGL(scan_chain_kernel, dim3(static_cast<unsigned>((cols + 255) / 256)), dim3(256),
-                           0, st, a, tiles);
+        if constexpr (NS != kFew)
+            hipLaunchKernelGGL(scan_chain_kernel, dim3(static_cast<unsigned>((cols + 255) / 256)), dim3(256),
+                               0, st, a, tiles);
     }
     hipLaunchKernelGGL((scan_fwd_kernel<T, NS, S, true>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
+// Few tokens leave most of the chip idle with 16 states per lane, and a call's time is that of its
+// waves' start, one tile and the launches. With four states per lane a tile takes a third of the
+// time, and the last pass chains the tiles itself (walk_tiles) instead of a launch in between:
+// 197 tokens x 768 channels x 16 states 15.1 us against 21.9 us; 4 tokens 5.9 against 10.4 us. Taken
+// up to three waves per SIMD and 32 tiles (320 x 1,536 x 16, 1,920 waves: 19.5 against 24.5 us; 197
+// x 4,096, 3,328 waves: 21.9 against 22.7; 256 x 4,096, 4,096 waves: 25.8 against 23.9; 700 x 768, 44
+// tiles: 26.9 both). At 32 lanes per channel a wave reads only eight neighbouring bytes of a tile's
+// states, so that six tiles are the limit (96 tokens x 256 channels x 128 states 20.2 against 27.7 us;
+// 197 tokens, 13 tiles, 30.7 against 28.4).
+int few_parts(int d_state) {
+    return d_state <= 8 ? 2 : d_state <= 16 ? 4 : d_state <= 32 ? 8 : d_state <= 64 ? 16 : 32;
+}
+bool few(const ScanArgs &a) {
+    const int parts = few_parts(a.d_state), tiles = scan_tiles(a.map.total, a.tile);
+    if (a.chained ? tiles > (parts < 32 ? 32 : 6) : a.tile > 16) return false;
+    return static_cast<int64_t>(scan_blocks(a.channels, a.groups, parts)) * tiles * kScanWaves <= 3 * kSimds;
+}
+
 template <typename T>
 hipError_t launch_fwd_t(const ScanArgs &a, hipStream_t st) {
+    if (few(a)) {
+        switch (few_parts(a.d_state)) {
+        case 2: return launch_fwd<T, kFew, 2>(a, st);
+        case 4: return launch_fwd<T, kFew, 4>(a, st);
+        case 8: return launch_fwd<T, kFew, 8>(a, st);
+        case 16: return launch_fwd<T, kFew, 16>(a, st);
+        default: return launch_fwd<T, kFew, 32>(a, st);
+        }
+    }
     switch (scan_parts(a.d_state)) {
     case 1: return a.d_state <= 8 ? launch_fwd<T, 8, 1>(a, st) : launch_fwd<T, 16, 1>(a, st);
     case 2: return launch_fwd<T, 16, 2>(a, st);

@@ -553,14 +553,18 @@ int scan_bwd_parts(int d_state) {
     return d_state <= 8 ? 1 : d_state <= 16 ? 2 : d_state <= 32 ? 4 : d_state <= 64 ? 8 : 16;
 }
 
-// Tokens per tile: whole sequences where they are short enough, else about 2,048 waves, between
-// 8 tokens and what LDS holds.
+// Tokens per tile: about two waves per SIMD, between 8 tokens (16 where that would be more than 64
+// tiles to chain) and what LDS holds; whole sequences where they are no longer than that. Few waves
+// take 10 us per eight tokens, so short sequences are cut too: 64 tokens x 768 channels x 16 states
+// 31 us in 8 tiles against 87 us whole, 16 x 64 tokens 66 against 92 us; 64 x 16 tokens x 256
+// channels 35 us whole against 46 us in halves.
 int scan_bwd_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed) {
-    if (!packed && seqlen <= kScanMaxBwdTile) return seqlen > 0 ? seqlen : 1;
     const int64_t total = static_cast<int64_t>(batch) * seqlen;
     const int64_t waves = static_cast<int64_t>(kScanWaves) * scan_blocks(channels, groups, scan_bwd_parts(d_state));
     const int64_t t = (total * waves / (2 * kSimds) + kG - 1) / kG * kG;
-    return t < kG ? kG : t > kScanMaxBwdTile ? kScanMaxBwdTile : static_cast<int>(t);
+    const int least = total <= 64 * kG ? kG : 2 * kG;
+    const int tile = t < least ? least : t > kScanMaxBwdTile ? kScanMaxBwdTile : static_cast<int>(t);
+    return !packed && seqlen <= tile ? (seqlen > 0 ? seqlen : 1) : tile;
 }
 
 hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
