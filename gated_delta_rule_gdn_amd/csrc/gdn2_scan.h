@@ -83,10 +83,16 @@ __device__ __forceinline__ float rate2(float A) {
 }
 
 // A lane's states of one channel's row of d_state floats: zero where there is none, in whole pieces
-// of four where ScanArgs::vec allows.
-template <int NS, int S>
+// of four where ScanArgs::vec allows. PIECES false: value by value, where the
+// pieces' registers would spill.
+template <bool PIECES, int NS, int S>
 __device__ __forceinline__ void load_row(const ScanArgs &a, const ScanLane<NS, S> &l, const float *row,
                                          float (&h)[NS]) {
+    if constexpr (!PIECES) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) h[n] = l.on && l.n0 + n < a.d_state ? row[l.n0 + n] : 0.f;
+        return;
+    }
     if (a.vec) {
 #pragma unroll
         for (int n = 0; n < NS; n += 4) {
@@ -104,16 +110,16 @@ __device__ __forceinline__ void load_row(const ScanArgs &a, const ScanLane<NS, S
 // The decay rates of a lane's states.
 template <int NS, int S>
 __device__ __forceinline__ void load_rates(const ScanArgs &a, const ScanLane<NS, S> &l, float (&A2)[NS]) {
-    load_row(a, l, a.A + static_cast<int64_t>(l.c) * a.d_state, A2);
+    load_row<true>(a, l, a.A + static_cast<int64_t>(l.c) * a.d_state, A2);
 #pragma unroll
     for (int n = 0; n < NS; ++n) A2[n] = rate2(A2[n]);
 }
 
 // A lane's states of sequence i from / to [num_seqs][channels][d_state].
-template <int NS, int S>
+template <bool PIECES = true, int NS, int S>
 __device__ __forceinline__ void load_state(const ScanArgs &a, const ScanLane<NS, S> &l, const float *s,
                                            int i, float (&h)[NS]) {
-    load_row(a, l, s + (static_cast<int64_t>(i) * a.channels + l.c) * a.d_state, h);
+    load_row<PIECES>(a, l, s + (static_cast<int64_t>(i) * a.channels + l.c) * a.d_state, h);
 }
 template <int NS, int S>
 __device__ __forceinline__ void store_state(const ScanArgs &a, const ScanLane<NS, S> &l, float *s, int i,

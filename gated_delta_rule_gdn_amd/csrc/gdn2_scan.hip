@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256, FINAL ? 3 : 4) void scan_fwd_kernel(ScanArgs a
             if constexpr (NS == kFew) walk_tiles(a, l, s, tile, A2, h);
             else load_tile(a, l, a.tiles_h, tile, h);
         } else if (s.starts && a.S0) {
-            load_state(a, l, a.S0, s.i, h);
+            load_state<S == 1 || NS == kFew>(a, l, a.S0, s.i, h);
         } else {
 #pragma unroll
             for (int n = 0; n < NS; ++n) h[n] = 0.f;

@@ -261,7 +261,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
         if (!s.ends) {
             load_tile(a, l, a.tiles_g, tile, g);
         } else if (a.dS_T) {
-            load_state(a, l, a.dS_T, s.i, g);
+            load_state<false>(a, l, a.dS_T, s.i, g);
         } else {
 #pragma unroll
             for (int n = 0; n < NS; ++n) g[n] = 0.f;
@@ -309,7 +309,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
             if (!s.starts) {
                 load_tile(a, l, a.tiles_h, tile, h);
             } else if (a.S0 && q == 0) {
-                load_state(a, l, a.S0, s.i, h);
+                load_state<false>(a, l, a.S0, s.i, h);
             } else {
 #pragma unroll
                 for (int n = 0; n < NS; ++n) h[n] = 0.f;
