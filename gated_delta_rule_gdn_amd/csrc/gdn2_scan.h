@@ -164,7 +164,8 @@ __device__ __forceinline__ void walk_tiles(const ScanArgs &a, const ScanLane<NS,
 #pragma unroll
     for (int n = 0; n < NS; ++n) h[n] = 0.f;
     constexpr int U = 8;       // tiles whose loads are in flight together
-    for (int64_t i0 = s.first / a.tile; i0 < tile; i0 += U) {
+    const int64_t first = s.first / a.tile;
+    for (int64_t i0 = first; i0 < tile; i0 += U) {
         float hl[U][NS], dl[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -179,7 +180,11 @@ __device__ __forceinline__ void walk_tiles(const ScanArgs &a, const ScanLane<NS,
         for (int k = 0; k < U; ++k)
             if (i0 + k < tile)
 #pragma unroll
-                for (int n = 0; n < NS; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(A2[n] * dl[k]), h[n], hl[k][n]);
+                for (int n = 0; n < NS; ++n) {
+                    // the first tile's sum of dt is also of sequences before this one
+                    const float on = fmaf(__builtin_amdgcn_exp2f(A2[n] * dl[k]), h[n], hl[k][n]);
+                    h[n] = i0 + k > first ? on : hl[k][n];
+                }
     }
 #pragma unroll
     for (int n = 0; n < NS; ++n) h[n] = l.on && l.n0 + n < a.d_state ? h[n] : 0.f;

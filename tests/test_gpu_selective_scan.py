@@ -311,3 +311,71 @@ def test_rates_of_minus_infinity_and_nan(T):
     keep = [c for c in range(10) if c != 5]
     assert torch.isnan(bad[0, :, 5]).all() and torch.isnan(Sb[0, 5]).any()
     assert torch.equal(bad[:, :, keep], o[:, :, keep]) and torch.equal(Sb[0, keep], S[0, keep])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ch,M,G", [(70, 5, 1), (66, 16, 2), (70, 20, 1), (20, 50, 1), (12, 100, 2)])
+def test_many_tiles(ch, M, G, dtype):
+    """More tiles than the last pass chains itself, at every number of lanes per channel, with
+    sequences that start and end inside tiles."""
+    lens = [333, 0, 1, 290, 7, 60, 0]
+    T = sum(lens)
+    h = make((1, T), ch, M, G, len(lens), dtype, seed=M)
+    o, S = call(gpu(h), cu_seqlens=cu_of(lens))
+    torch.cuda.synchronize()
+    r = ref(h, lens)
+    check("o", o[0], r["o"], r["o_b"], dtype)
+    check("S_T", S, r["S_T"], r["S_T_b"])
+
+
+@pytest.mark.parametrize("B,T,ch,M", [(900, 9, 70, 5), (900, 9, 70, 16), (600, 5, 70, 20),
+                                      (300, 17, 300, 50), (300, 17, 130, 100)])
+def test_whole_sequences_of_a_large_batch(B, T, ch, M):
+    """Batches that are not cut and give every SIMD its waves with 8 or 16 states per lane."""
+    h = make((B, T), ch, M, 1, B, torch.float32, seed=M)
+    o, S = call(gpu(h))
+    torch.cuda.synchronize()
+    r = ref(h, [T] * B)
+    check("o", o.reshape(B * T, ch), r["o"], r["o_b"])
+    check("S_T", S, r["S_T"], r["S_T_b"])
+
+
+@pytest.mark.parametrize("M", [4, 16, 32, 64, 128])
+def test_rows_of_states_at_odd_addresses(M):
+    """Rates and states that start four bytes behind a 16-byte boundary give the bits of the
+    aligned call, in calls of few tokens and of many tiles."""
+    for T in (40, 600):
+        h = make((1, T), 24, M, 1, 1, torch.float32, seed=T)
+        d = gpu(h)
+        o, S = call(d)
+
+        def off(t):
+            buf = torch.empty(t.numel() + 1, device="cuda")
+            v = buf[1:].view(t.shape)
+            return v.copy_(t)
+
+        e = {**d, "A": off(d["A"]), "S0": off(d["S0"])}
+        o2, S2 = call(e, final_state=off(torch.zeros_like(S)))
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
+@pytest.mark.parametrize("name", ["x", "dt", "B", "C", "gate", "S0"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("lens", [[41, 23, 50], [300, 90, 250]])
+def test_values_that_are_not_finite_stay_in_their_sequence(name, bad, lens):
+    """The middle one of three sequences, which meet inside tiles, holds NaN or infinities: the
+    bits of the others' outputs and states do not change, in calls of few tokens and of many."""
+    a, b = lens[0], lens[0] + lens[1]
+    h = make((1, sum(lens)), 24, 16, 1, 3, torch.float32, seed=14)
+    d = gpu(h)
+    o0, S0 = call(d, cu_seqlens=cu_of(lens))
+    if name == "S0":
+        d[name][1] = bad
+    else:
+        d[name][:, a:b] = bad
+    o, S = call(d, cu_seqlens=cu_of(lens))
+    torch.cuda.synchronize()
+    assert torch.equal(o[:, :a], o0[:, :a]) and torch.equal(o[:, b:], o0[:, b:])
+    assert torch.equal(S[[0, 2]], S0[[0, 2]])
+    assert not torch.equal(o, o0)

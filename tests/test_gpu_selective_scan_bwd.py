@@ -236,3 +236,30 @@ def test_rates_of_minus_infinity_and_nan():
     keep = [c for c in range(10) if c != 5]
     assert torch.isnan(bad["dx"][0, :100, 5]).all()
     assert torch.equal(bad["dx"][:, :, keep], o["dx"][:, :, keep])
+
+
+@pytest.mark.parametrize("ch,M", [(4096, 16), (2048, 17), (1024, 40), (512, 100)])
+def test_many_waves(ch, M):
+    """Sizes at which the tile pass takes sixteen states per lane, and tiles of 64 tokens."""
+    lens = [900, 3, 0, 1197]
+    h = make((1, 2100), ch, M, 1, 4, torch.float32, seed=M)
+    run_and_check(h, lens, torch.float32, torch.float32)
+
+
+@pytest.mark.parametrize("M", [4, 16, 32, 64, 128])
+def test_rows_of_states_at_odd_addresses(M):
+    """Rates and states that start four bytes behind a 16-byte boundary: the aligned call's bits."""
+    h = make((1, 100), 24, M, 1, 2, torch.float32, seed=M)
+    d = gpu(h)
+    q = Draw(7)
+    dO, dS = q.normal(1, 100, 24).cuda(), q.normal(2, 24, M).cuda()
+    a = call(d, dO, dS, cu_seqlens=cu_of([70, 30]))
+
+    def off(t):
+        buf = torch.empty(t.numel() + 1, device="cuda")
+        v = buf[1:].view(t.shape)
+        return v.copy_(t)
+
+    b = call({**d, "A": off(d["A"]), "S0": off(d["S0"])}, dO, off(dS), cu_seqlens=cu_of([70, 30]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[n], b[n]) for n in a)
