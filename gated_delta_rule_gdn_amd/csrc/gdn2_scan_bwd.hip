@@ -445,9 +445,9 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
     }
 }
 
-// Launch 4, over the tiles: a column per lane, four waves taking every fourth tile.
-// Columns: d_state * channels of dA, then channels of dD, then channels of ddt_bias.
-__global__ __launch_bounds__(256) void scan_bwd_params_kernel(ScanArgs a, int tiles) {
+// Over the tiles: a column per lane, four waves taking every fourth tile. Columns: d_state *
+// channels of dA, then channels of dD, then channels of ddt_bias.
+__device__ __forceinline__ void sum_tiles(const ScanArgs &a, int tiles) {
     __shared__ float s[4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t cols = static_cast<int64_t>(a.d_state) * a.channels;
@@ -475,14 +475,14 @@ __global__ __launch_bounds__(256) void scan_bwd_params_kernel(ScanArgs a, int ti
     }
 }
 
-// Launch 4, over the workgroups of a group's channels: dB and dC, one value per thread. Tokens
-// behind the last sequence are left as they were.
+// Over the workgroups of a group's channels: dB and dC, one value per thread. Tokens behind the
+// last sequence are left as they were. This is workgroup `wg` of `wgs`.
 template <typename TG>
-__global__ __launch_bounds__(256) void scan_bwd_bc_kernel(ScanArgs a, int blocks) {
+__device__ __forceinline__ void sum_blocks(const ScanArgs &a, int blocks, int wg, int wgs) {
     const int end = seq_begin(a.map, a.map.n);
     const int64_t row = 2 * static_cast<int64_t>(a.d_state), n = a.groups * row * end;
-    for (int64_t e = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x; e < n;
-         e += static_cast<int64_t>(gridDim.x) * 256) {
+    for (int64_t e = wg * static_cast<int64_t>(256) + threadIdx.x; e < n;
+         e += static_cast<int64_t>(wgs) * 256) {
         const int64_t tg = e / row;
         const int j = static_cast<int>(e - tg * row);
         const int64_t t = tg / a.groups;
@@ -493,6 +493,15 @@ __global__ __launch_bounds__(256) void scan_bwd_bc_kernel(ScanArgs a, int blocks
         TG *out = static_cast<TG *>(j < a.d_state ? a.dB : a.dC);
         io<TG>::st(out + tg * a.d_state + (j < a.d_state ? j : j - a.d_state), v);
     }
+}
+
+// Launch 4: the first `first` workgroups add over the tiles, the others over workgroups. (One
+// launch: as two they took 4.6 and 4.4 us behind each other, mostly latency.)
+template <typename TG>
+__global__ __launch_bounds__(256) void scan_bwd_sums_kernel(ScanArgs a, int tiles, int blocks, int first) {
+    const int wg = blockIdx.x;
+    if (wg < first) sum_tiles(a, tiles);
+    else sum_blocks<TG>(a, blocks, wg - first, static_cast<int>(gridDim.x) - first);
 }
 
 template <typename T, typename TG, int NS, int S>
@@ -525,14 +534,10 @@ hipError_t launch_bwd(const ScanArgs &a, hipStream_t st) {
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((scan_bwd_kernel<T, TG, NS, S>), grid, dim3(256), lds, st, a);
     const int64_t all = cols + 2 * static_cast<int64_t>(a.channels);
-    hipLaunchKernelGGL(scan_bwd_params_kernel, dim3(static_cast<unsigned>((all + 63) / 64)), dim3(256), 0, st,
-                       a, tiles);
     const int64_t n = 2 * static_cast<int64_t>(a.d_state) * a.groups * a.map.total;
-    if (n > 0) {
-        const int64_t wg = (n + 255) / 256;
-        hipLaunchKernelGGL(scan_bwd_bc_kernel<TG>, dim3(static_cast<unsigned>(wg < 4096 ? wg : 4096)),
-                           dim3(256), 0, st, a, blocks / a.groups);
-    }
+    const int first = static_cast<int>((all + 63) / 64), rest = static_cast<int>((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096);
+    hipLaunchKernelGGL(scan_bwd_sums_kernel<TG>, dim3(static_cast<unsigned>(first + rest)), dim3(256), 0, st, a,
+                       tiles, blocks / a.groups, first);
     return hipGetLastError();
 }
 
