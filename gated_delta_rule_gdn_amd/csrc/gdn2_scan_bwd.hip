@@ -20,7 +20,7 @@
 // each step sends half of a lane's values to the partner lane and adds the other half, so 8
 // values over 32 lanes cost about 19 operations instead of 40 (reduce_spread).
 //
-// Bound by the vector unit: 4,096 tokens x 2,048 channels x 16 states, bf16, 242-250 us (180 for
+// Bound by the vector unit: 4,096 tokens x 2,048 channels x 16 states, bf16, 239-250 us (180 for
 // launch 3, at 75 % of the unit's issue, 62 for launch 1, 11 for the chain when they are timed one
 // by one), against 120 us for the states' own operations and 23 us for the bytes.
 #include "gdn2_internal.h"
