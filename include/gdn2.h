@@ -577,7 +577,10 @@ gdn2_status gdn2_selective_scan_fwd(const void *x, const void *dt, const float *
                                     void *o, float *S_T, const gdn2_scan_dims *dims, void *workspace,
                                     size_t workspace_bytes, void *stream);
 
-/* Bytes of device workspace gdn2_selective_scan_bwd needs, or 0 if the dims are invalid. */
+/*
+ * Bytes of device workspace gdn2_selective_scan_bwd needs (mostly the state before every eighth
+ * token: channels * d_state / 2 bytes per token), or 0 if the dims are invalid.
+ */
 size_t gdn2_selective_scan_bwd_workspace_bytes(const gdn2_scan_dims *dims);
 
 /*
