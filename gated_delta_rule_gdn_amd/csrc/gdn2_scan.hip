@@ -359,9 +359,9 @@ int scan_blocks(int channels, int groups, int parts) {
 int scan_tiles(int total, int tile) { return total > tile ? (total + tile - 1) / tile : 1; }
 
 // Tokens per tile. A dense batch whose sequences alone give 1,024 waves (one per SIMD) is not
-// cut: its tile is a sequence (16 x 1,024 tokens x 4,096 channels, 1,024 waves: 450 us against
-// 483 us cut; 64 x 128 x 2,048, 2,048 waves: 87 against 150; but 12 x 512 x 4,096, 768 waves: 222
-// against 203). Otherwise about three waves per SIMD, 16 tokens at least.
+// cut: its tile is a sequence (16 x 1,024 tokens x 4,096 channels, 1,024 waves: 429 us against
+// 503 us cut; 64 x 128 x 2,048, 2,048 waves: 81 against 140; but 12 x 512 x 4,096, 768 waves: 215
+// against 182). Otherwise about three waves per SIMD, 16 tokens at least.
 int scan_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed) {
     const int64_t total = static_cast<int64_t>(batch) * seqlen;
     const int64_t waves = static_cast<int64_t>(kScanWaves) * scan_blocks(channels, groups, scan_parts(d_state));
