@@ -303,8 +303,7 @@ def _own_norm_bwd(s, case):
     import gated_delta_rule_gdn_amd as g
     return g.block_norm_bwd(s["x"], dh=s["dh"], dy=s["dy"], norm_weight=s["norm_weight"],
                             gate=s["gate"], residual=s["residual"], scale=s["scale"],
-                            next_weight=s["next_weight"],
-                            grad_dtype=_grad_type(case, s["x"].dtype))
+                            next_weight=s["next_weight"])
 
 
 def _where_tokens(s):
