@@ -133,28 +133,27 @@ __device__ __forceinline__ float silu_slope(float a) {
 
 // Offset of sequence i of a SeqMap (i = n: the end of the last one). Offsets are held inside
 // [0, total], so a wrong table never makes an access leave the tensors.
-__device__ __forceinline__ int seq_begin(const SeqMap &m, int i) {
+__host__ __device__ __forceinline__ int seq_begin(const SeqMap &m, int i) {
     if (!m.cu) return i * m.seqlen;
     const int v = m.cu[i];
     return v < 0 ? 0 : (v > m.total ? m.total : v);
 }
 
-// The first i in [0, n] with seq_begin(i) >= t, or n + 1. Called by whole waves: 64 offsets are
-// looked at a time, so a search takes one load per factor of 64 in n.
-__device__ __forceinline__ int seq_first_at(const SeqMap &m, int t) {
+// The first i in [0, n] with seq_begin(i) >= t, or n + 1. 64 offsets are looked at a time, so a
+// search takes one load per factor of 64 in n: count(lo, step, hi) says how many of the offsets
+// i = lo + l * step < hi, l < 64, are below t. (Split from seq_first_at so that it runs on a host.)
+template <typename Count>
+__host__ __device__ __forceinline__ int seq_search(const SeqMap &m, int t, Count &&count) {
     if (!m.cu) {
         if (t <= 0) return 0;
         if (m.seqlen <= 0) return m.n + 1;
         const int i = (t - 1) / m.seqlen + 1;
         return i > m.n ? m.n + 1 : i;
     }
-    const int lane = threadIdx.x & 63;
     int lo = 0, hi = m.n + 1;
     while (lo < hi) {
         const int step = (hi - lo + 63) >> 6;
-        const int64_t i = lo + static_cast<int64_t>(lane) * step;
-        const bool before = i < hi && seq_begin(m, static_cast<int>(i)) < t;
-        const int c = __popcll(__ballot(before));
+        const int c = count(lo, step, hi);
         if (c == 0) break;
         if (step == 1) return lo + c;
         const int64_t end = lo + static_cast<int64_t>(c) * step;
@@ -164,32 +163,49 @@ __device__ __forceinline__ int seq_first_at(const SeqMap &m, int t) {
     return lo;
 }
 
+// The search by a whole wave, an offset per lane.
+__device__ __forceinline__ int seq_first_at(const SeqMap &m, int t) {
+    const int lane = threadIdx.x & 63;
+    return seq_search(m, t, [&](int lo, int step, int hi) {
+        const int64_t i = lo + static_cast<int64_t>(lane) * step;
+        const bool before = i < hi && seq_begin(m, static_cast<int>(i)) < t;
+        return __popcll(__ballot(before));
+    });
+}
+
 // One sequence's share [lo, hi) of a tile: sequence i covers tokens [first, end).
 struct Span {
     int i, first, end, lo, hi;
     bool starts, ends;     // the tile holds the sequence's first position; its end
 };
 
-// Calls f(Span) for every sequence that has tokens in [t0, t1), in order. Empty sequences come
-// too, once each: with the tile that holds their position, those at the very end (t1 == total)
-// with the last tile. Tokens behind the last sequence belong to no span. Every lane of the wave
-// takes part, and everything in the span is the same in all of them.
+// Calls f(Span) for every sequence that has tokens in [t0, t1), in order, from i on, which
+// seq_search found for t0. Empty sequences come too, once each: with the tile that holds their
+// position, those at the very end (t1 == total) with the last tile. Tokens behind the last sequence
+// belong to no span. With offsets that decrease, spans are wrong, but 0 <= first <= lo <= hi <= total
+// and t0 <= lo, hi <= t1 hold for any table, which is what keeps every access inside the tensors.
 template <typename F>
-__device__ __forceinline__ void for_spans(const SeqMap &m, int t0, int t1, F &&f) {
-    int i = seq_first_at(m, t0);
+__host__ __device__ __forceinline__ void walk_spans(const SeqMap &m, int t0, int t1, int i, F &&f) {
     bool inside = i > 0 && i <= m.n && seq_begin(m, i) > t0;    // t0 lies inside sequence i - 1
     if (inside) --i;
-    for (i = __builtin_amdgcn_readfirstlane(i); i < m.n; ++i) {
+    for (; i < m.n; ++i) {
         const int first = seq_begin(m, i);
         if (!inside && first >= t1 && t1 < m.total) return;
         int end = seq_begin(m, i + 1);
         if (end < first) end = first;
-        // (first >= t0 where offsets do not decrease; a span never leaves its tile in any case)
         const int lo = inside || first < t0 ? t0 : first, hi = end < t1 ? end : t1;
-        f(Span{i, first, end, lo, hi < lo ? lo : hi, !inside, end <= t1});
+        // (first > lo: a sequence taken as entered that a decreasing table puts behind the tile's start)
+        f(Span{i, first < lo ? first : lo, end, lo, hi < lo ? lo : hi, !inside, end <= t1});
         if (end > t1) return;
         inside = false;
     }
+}
+
+// The same for a tile of a wave: every lane takes part, and everything in the span is the same in
+// all of them.
+template <typename F>
+__device__ __forceinline__ void for_spans(const SeqMap &m, int t0, int t1, F &&f) {
+    walk_spans(m, t0, t1, __builtin_amdgcn_readfirstlane(seq_first_at(m, t0)), static_cast<F &&>(f));
 }
 
 }  // namespace gdn2
