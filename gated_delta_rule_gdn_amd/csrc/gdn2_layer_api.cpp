@@ -59,7 +59,7 @@ gdn2::SeqMap seq_map(const int32_t *cu, int32_t batch, int32_t seqlen, int32_t n
 // A token stride: 0 means contiguous. False if it is too small or the tensor too large.
 bool take_stride(int64_t given, int64_t row, int64_t tokens, int64_t *out) {
     *out = given == 0 ? row : given;
-    return *out >= row && *out <= kMaxElems && tokens * *out <= kMaxElems;
+    return *out >= row && *out <= kMaxElems && (tokens <= 0 || *out <= kMaxElems / tokens);
 }
 
 // ---- short convolution -------------------------------------------------------------------
