@@ -384,7 +384,10 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanArgs a) {
                 }
                 sB = sum_parts<S>(sB);
                 float dd = fmaf(x[k], sB, sum_parts<S>(sA) * (1.f / kLog2e));
-                if (a.softplus) dd *= sigmoid_hw(raw[k]);
+                if (a.softplus) {       // a masked step, of no slope, takes none of a product beyond fp32
+                    const float slope = sigmoid_hw(raw[k]);
+                    dd = slope == 0.f ? 0.f : dd * slope;
+                }
                 dD = fmaf(dy, x[k], dD);
                 dbias += k < m ? dd : 0.f;
                 if (gated) {        // dgate, dx and ddt take the places of gate, dO and raw
