@@ -402,7 +402,9 @@ hipError_t launch_step(const ConvStepArgs &a, hipStream_t st) {
 // Tokens per tile: about six waves of the forward's 256 channels or three of the backward's 128 on
 // each SIMD, and at least 8 tokens, where the rows next to a tile are nearly half of what a wave
 // reads. On 4,096 tokens x 6,144 channels: 16 tokens forward (21.1 us; 24 tokens
-// 22.0, 48 tokens 25.4), 64 backward (39.0 us; 24 tokens 45.0).
+// 22.0, 48 tokens 25.4), 64 backward (39.0 us; 24 tokens 45.0). Where channels are taken one by one a
+// wave has 64, and there are four (backward two) times as many: 2,311 tokens x 1,537 bf16 channels
+// take 9.1 us forward, 1,536 channels 6.5.
 int conv_tile(int64_t tokens, int channels, bool backward) {
     const int per = backward ? 128 : 256;
     const int64_t waves = (static_cast<int64_t>(channels) + per - 1) / per;

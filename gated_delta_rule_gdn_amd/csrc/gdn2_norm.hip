@@ -18,7 +18,9 @@
 //
 // Measured: 8,192 x 2,048 bf16 with every stage 25.4 us of GPU time (134 MB, 5.3 TB/s, what a large
 // copy reaches); gradients of 4,096 x 2,048 bf16 with an fp32 residual 52.6 us (185 MB; 48 for the
-// pass, 3.9 TB/s behind four row sums with a barrier each, and 4.6 for the parameters' sums).
+// pass, 3.9 TB/s behind four row sums with a barrier each, and 4.6 for the parameters' sums). Far
+// from the bytes' time are gradients of short rows (see norm_reduce_kernel) and of rows above 4,096
+// columns (see launch_rows).
 #include "gdn2_internal.h"
 #include "gdn2_layer.h"
 
@@ -311,7 +313,9 @@ __global__ __launch_bounds__(norm_threads(L)) void norm_bwd_kernel(NormArgs a) {
 }
 
 // The parameter gradients: the rows of a.partial added in a fixed order. 32 columns per
-// workgroup, whose 32 halves of waves each take every 32nd row.
+// workgroup, whose 32 halves of waves each take every 32nd row. Rows of at most 128 columns leave 16
+// partial rows per workgroup of the pass for few columns: of 65,536 x 128 bf16 four workgroups add
+// 12,288 rows in 21 us, behind a pass of 20 us (84 MB, 16 us at a copy's rate).
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormArgs a, int parts) {
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, half = threadIdx.x >> 5;
@@ -334,7 +338,9 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(NormArgs a, int parts
 }
 
 constexpr int kNormGridX = 1 << 20;
-constexpr int kNormGroups = 768;      // workgroups of a backward pass: three per CU
+// Workgroups of a backward pass: three per CU, as many as bf16 rows' instances of 256 threads have
+// there (148-168 registers). fp32 rows (170-177) have two, so that their last third runs alone.
+constexpr int kNormGroups = 768;
 
 template <typename T, typename TR, typename TG, typename TGR, int L, int V, int P>
 hipError_t launch(const NormArgs &a, bool backward, hipStream_t st) {
@@ -357,8 +363,12 @@ hipError_t launch(const NormArgs &a, bool backward, hipStream_t st) {
 }
 
 // Eight values per lane: a lane's piece of a bf16 row is one 16-byte access, and the backward's
-// ten row-sized arrays fit the registers of four waves per SIMD. Rows above 8,192 columns take
-// 16 values in the largest workgroup.
+// row-sized arrays take 148-195 registers up to 4,096 columns (value by value up to 256, with 44-76
+// bytes spilled at 512 lanes), for two or three waves per SIMD. Rows above 4,096 columns take 1,024
+// threads, which have 128 registers: the backward spills 84-176 bytes per lane there (value by value
+// 284-320), and above 8,192 columns, where a lane has 16 values, 528-736 (968-1,040). With every
+// stage and an fp32 residual the pass over 4,096 rows of 5,120 bf16 columns takes 325 us against 90
+// for its bytes, 8,192 418 against 144, 16,384 1,585 against 288. The forward spills nothing.
 template <typename T, typename TR, typename TG, typename TGR, int V>
 hipError_t launch_rows(const NormArgs &a, bool backward, hipStream_t st) {
     constexpr int P = 8 / V;

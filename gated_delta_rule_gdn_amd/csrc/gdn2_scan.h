@@ -3,7 +3,9 @@
 // A wave holds CW = 64 / S channels: lane l owns channel l % CW and the NS states
 // [NS (l / CW), NS (l / CW) + NS) of it, so a channel's d_state <= NS * S states lie in S lanes.
 // The four waves of a workgroup take neighbouring channels of one group (which share B and C)
-// and the same tile of tokens.
+// and the same tile of tokens. Lanes past a group's last channel run along on its first one and
+// store nothing, so groups of fewer channels than a workgroup's cost a whole one each: gradients of
+// 64 x 512 tokens x 128 channels x 16 states, bf16, take 206 us in one group and 558 us in four.
 #pragma once
 #include "gdn2_internal.h"
 #include "gdn2_layer.h"
@@ -40,8 +42,9 @@ __device__ __forceinline__ float sum_parts(float x) {
 }
 
 // softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in [0, 1]. log(1 + e) / e is a polynomial of
-// degree 8, fitted for the least relative error on [0, 1] (3e-8; with fp32 Horner steps 2.8 * 2^-24),
-// so that a small e, a usual step of 0.001, keeps its relative precision.
+// degree 8, fitted for the least relative error on [0, 1], so that a small e, a usual step of 0.001,
+// keeps its relative precision. With its coefficients rounded to fp32 it is within 6.5e-8, and with
+// fp32 Horner steps within 1.4e-7 (2.3 * 2^-24), taken over every fp32 e from 1e-12 to 1.
 __device__ __forceinline__ float softplus(float x) {
     const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(x));
     float p = 0.005232692696154118f;

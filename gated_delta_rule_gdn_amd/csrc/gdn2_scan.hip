@@ -16,9 +16,10 @@
 // exp(A sum dt)), a second chains the tiles, a third runs them from their true states. That costs
 // the exp2 and three operations once more, so the rule takes it only when it is the faster.
 //
-// Measured: prompt of 4,096 tokens x 4,096 channels x 16 states, bf16, 131-146 us with the clock: 64
-// for the first pass, 8 for the chain, the rest for the last, which keep the vector unit 84 % busy
-// (86 us for the states' own operations, 26 us for the bytes). 16,384 x 2,048 packed 259-276 us.
+// Measured: prompt of 4,096 tokens x 4,096 channels x 16 states, bf16, 131-146 us with the clock (59
+// for the first pass, 8 for the chain, 78 for the last when they are timed one by one). The passes
+// keep the vector unit 84 % busy: the states' own operations take 47 us in a scan run once, 86 us
+// with the first pass, and the bytes 26 us. 16,384 x 2,048 packed 259-276 us.
 #include <type_traits>
 
 #include "gdn2_internal.h"
@@ -359,7 +360,8 @@ int scan_blocks(int channels, int groups, int parts) {
 int scan_tiles(int total, int tile) { return total > tile ? (total + tile - 1) / tile : 1; }
 
 // Tokens per tile. A dense batch whose sequences alone give 1,024 waves (one per SIMD) is not
-// cut: its tile is a sequence (16 x 1,024 tokens x 4,096 channels, 1,024 waves: 429 us against
+// cut, waves without a channel counted as the others, since they take as long (see ScanLane): its
+// tile is a sequence (16 x 1,024 tokens x 4,096 channels, 1,024 waves: 429 us against
 // 503 us cut; 64 x 128 x 2,048, 2,048 waves: 81 against 140; but 12 x 512 x 4,096, 768 waves: 215
 // against 182). Otherwise about three waves per SIMD, 16 tokens at least.
 int scan_tile(int channels, int groups, int d_state, int batch, int seqlen, bool packed) {

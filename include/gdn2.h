@@ -467,7 +467,8 @@ gdn2_status gdn2_map_gates_bwd(int32_t mode, const gdn2_dims *dims, const void *
  *     call's dtype. Gradients of parameters and states are fp32.
  *   - All sums, states and statistics are held in fp32. Every call gives the same bits for the
  *     same arguments (no atomics).
- *   - At most 2^30 tokens and 2^20 channels. Outputs must not overlap inputs, the workspace or
+ *   - At most 2^30 tokens and 2^20 channels; no tensor may reach over more than 2^40 elements,
+ *     strides included. Outputs must not overlap inputs, the workspace or
  *     each other (the same pointer twice is refused).
  */
 
@@ -578,8 +579,11 @@ gdn2_status gdn2_selective_scan_fwd(const void *x, const void *dt, const float *
                                     size_t workspace_bytes, void *stream);
 
 /*
- * Bytes of device workspace gdn2_selective_scan_bwd needs (mostly the state before every eighth
- * token: channels * d_state / 2 bytes per token), or 0 if the dims are invalid.
+ * Bytes of device workspace gdn2_selective_scan_bwd needs, or 0 if the dims are invalid. About, with
+ * c = channels and s = d_state: c (s + 1) / 2 bytes per token for the state before every eighth one;
+ * 8 c (s + 1) bytes per tile of 8 to 64 tokens; and 8 s bytes per token and workgroup of channels,
+ * of which a group has one per 256, 128, 64, 32 or 16 channels at up to 8, 16, 32, 64 or 128 states
+ * (4,096 tokens x 4,096 x 16: 0.2 GB; 16,384 x 8,192 x 128: 19.4 GB).
  */
 size_t gdn2_selective_scan_bwd_workspace_bytes(const gdn2_scan_dims *dims);
 
