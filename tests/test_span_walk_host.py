@@ -15,9 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 @pytest.fixture(scope="module")
 def walk(tmp_path_factory):
     exe = str(tmp_path_factory.mktemp("walk") / "span_walk")
-    subprocess.run([build._hipcc(), "-O1", "-std=c++17", f"--offload-arch={build.ARCH}",
-                    "-I", os.path.join(build.ROOT, "include"), "-I", build.CSRC,
-                    os.path.join(HERE, "span_walk.hip"), "-o", exe], check=True, capture_output=True)
+    subprocess.run([build._hipcc(), *build.FLAGS, "-I", build.CSRC, os.path.join(HERE, "span_walk.hip"), "-o", exe],
+                   check=True, capture_output=True)
 
     def run(tables):
         """tables of (offsets or sequence length, total, tile, n) -> their spans, as tuples."""
