@@ -11,8 +11,9 @@ are not on a GPU.
     o      = recurrent_fwd(q, k, v, log_alpha, b, w, state, state_idx=None)
                                       # T tokens per sequence against a state pool (fp32/bf16)
 
-The operators around the recurrence (short_conv_fwd and so on) are in ``layer`` and are
-functions of this package too.
+The operators around the recurrence (short_conv_fwd and so on) are in ``layer``, those of the
+attention layer of hybrid stacks (qk_rotary_fwd, paged_attention_step, pool_copy) in ``attention``;
+all are functions of this package too.
 
 Layouts: q, k [B,T,H_k,d_k]; v, w [B,T,H_v,d_v]; log_alpha, b [B,T,H_v,d_k];
 states [N,H_v,d_k,d_v] fp32. ``log_alpha`` is log of the decay (<= 0). Decode inputs drop
@@ -101,6 +102,7 @@ def lib() -> ctypes.CDLL:
         L.gdn2_chunk_bwd_states.restype = i32
         L.gdn2_chunk_bwd_states.argtypes = [vp] * 8 + [i32] + [vp] * 10 + [dp, vp, sz, vp]
         layer.declare(L)
+        attention.declare(L)
         _lib = L
     return _lib
 
@@ -631,3 +633,7 @@ from .layer import (block_norm_bwd, block_norm_bwd_workspace_bytes, block_norm_f
                     selective_scan_fwd, selective_scan_fwd_workspace_bytes,
                     selective_scan_step, short_conv_bwd, short_conv_bwd_workspace_bytes,
                     short_conv_fwd, short_conv_step)
+from . import attention  # noqa: E402
+from .attention import (paged_attention_step, paged_attention_step_workspace_bytes,  # noqa: E402,F401
+                        pool_copy, qk_rotary_append, qk_rotary_bwd,
+                        qk_rotary_bwd_workspace_bytes, qk_rotary_fwd, rotary_table)

@@ -223,6 +223,66 @@ int64_t norm_sets(int64_t rows, int d);       // workgroups that hold all rows
 int64_t norm_parts(int64_t rows, int d);      // rows of the partial sums
 hipError_t launch_norm(const NormArgs &a, bool backward, hipStream_t st);
 
+// Norms of queries and keys with the rotation by position (gdn2_qk_rotary_fwd, _bwd, _append).
+struct RotaryArgs {
+    const void *q, *k, *v = nullptr;
+    const float *cos_sin;            // [num_positions][d_rot]
+    const int32_t *positions;        // NULL: token t % seqlen
+    const float *q_weight, *k_weight;
+    void *q_out = nullptr, *k_out = nullptr;       // k_out, v_out: the pages with `slots`
+    void *v_out = nullptr;
+    const int32_t *slots = nullptr;
+    int64_t num_places = 0;          // num_pages * page_size
+    int page_size = 1;
+    const void *dq_out = nullptr, *dk_out = nullptr;
+    void *dq = nullptr, *dk = nullptr;
+    float *dq_weight = nullptr, *dk_weight = nullptr;
+    float *partial = nullptr;        // [rotary_parts()][2][d] sums of a backward call
+    int64_t q_stride, k_stride, v_stride = 0;
+    int tokens, seqlen, h_q, h_k, d, d_rot, num_positions;
+    float eps;
+    bool interleaved, bf16, grad_bf16 = false;
+};
+int rotary_parts(int tokens);                 // rows of the partial sums: workgroups of a backward call
+hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st);
+hipError_t launch_rotary_bwd(const RotaryArgs &a, hipStream_t st);
+
+// Attention of new tokens over a paged cache (gdn2_paged_attention_step).
+struct AttentionArgs {
+    const void *q, *k_pages, *v_pages;
+    const int32_t *page_table, *seq_lens;
+    void *o;
+    float *lse;
+    float *part_o = nullptr;         // [workgroups][rows of a workgroup][d]: sums of a part of a sequence
+    float *part_ml = nullptr;        // [workgroups][rows of a workgroup][2]: their maxima and totals
+    int64_t q_stride;
+    int num_seqs, new_tokens, h_q, h_k, d, num_pages, page_size, max_pages, window;
+    uint32_t page_mul;               // x / page_size = x * page_mul >> page_shift for x < 2^31
+    int page_shift;
+    float scale;
+    bool bf16;
+    bool q_whole;                    // rows of q can be taken in whole pieces of 16 bytes
+};
+struct AttentionPlan {
+    int row_tiles;                   // tiles of 16 rows that a workgroup takes
+    int row_blocks;                  // workgroups that share a (sequence, key head)'s rows
+    int max_parts;                   // most parts that all sequences together are cut into
+    bool split;                      // some sequence may be cut
+};
+int64_t attention_groups(const gdn2_attention_dims &d);      // workgroups of a call
+AttentionPlan attention_plan(const gdn2_attention_dims &d);
+hipError_t launch_attention(const AttentionArgs &a, const AttentionPlan &p, hipStream_t st);
+
+// Slots of pools copied (gdn2_pool_copy).
+constexpr int kCopyPools = 64;       // pools of one launch
+struct CopyArgs {
+    void *pool[kCopyPools];
+    int64_t bytes[kCopyPools];       // of a slot
+    const int32_t *src, *dst;
+    int num_pools, num_slots, count;
+};
+hipError_t launch_pool_copy(const CopyArgs &a, hipStream_t st);
+
 hipError_t launch_decode(const DecodeArgs &a, hipStream_t st);
 hipError_t launch_map_gates(const GateArgs &a, hipStream_t st);
 hipError_t launch_map_gates_bwd(const GateBwdArgs &a, hipStream_t st);

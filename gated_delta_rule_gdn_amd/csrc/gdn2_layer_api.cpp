@@ -6,37 +6,13 @@
 #include <initializer_list>
 
 #include "gdn2.h"
+#include "gdn2_checks.h"
 #include "gdn2_internal.h"
 
 namespace {
 
+using namespace gdn2::checks;
 using gdn2::report;
-using gdn2::report_hip;
-
-constexpr int64_t kMaxElems = (int64_t{1} << 40);    // bound on any tensor's element count
-constexpr int64_t kMaxTokens = (int64_t{1} << 30);   // token arithmetic stays in 32 bits
-constexpr int32_t kMaxChannels = 1 << 20;
-
-gdn2_status ok() { return report(GDN2_OK, ""); }
-
-gdn2_status done(hipError_t e, const char *where) {
-    return e == hipSuccess ? ok() : report_hip(e, where);
-}
-
-bool dtype_ok(int32_t t) { return t == GDN2_F32 || t == GDN2_BF16; }
-
-// An output that is the same buffer as an input or as another output. NULLs are not compared.
-template <int NO, int NI>
-bool aliases(const void *const (&outs)[NO], const void *const (&ins)[NI]) {
-    for (int i = 0; i < NO; ++i) {
-        if (!outs[i]) continue;
-        for (int j = 0; j < NI; ++j)
-            if (outs[i] == ins[j]) return true;
-        for (int j = i + 1; j < NO; ++j)
-            if (outs[i] == outs[j]) return true;
-    }
-    return false;
-}
 
 // The token layout shared by the prompt calls: dense, or packed with cu_seqlens.
 gdn2_status check_tokens(int32_t batch, int32_t seqlen, int32_t num_seqs, bool packed) {
@@ -54,12 +30,6 @@ gdn2_status check_tokens(int32_t batch, int32_t seqlen, int32_t num_seqs, bool p
 
 gdn2::SeqMap seq_map(const int32_t *cu, int32_t batch, int32_t seqlen, int32_t num_seqs) {
     return gdn2::SeqMap{cu, cu ? num_seqs : batch, seqlen, batch * seqlen};
-}
-
-// A token stride: 0 means contiguous. False if it is too small or the tensor too large.
-bool take_stride(int64_t given, int64_t row, int64_t tokens, int64_t *out) {
-    *out = given == 0 ? row : given;
-    return *out >= row && *out <= kMaxElems && (tokens <= 0 || *out <= kMaxElems / tokens);
 }
 
 // ---- short convolution -------------------------------------------------------------------
@@ -147,9 +117,6 @@ bool d_state_pieces(const gdn2_scan_dims *d, std::initializer_list<const float *
     return true;
 }
 
-constexpr size_t kAlign = 256;
-size_t padded(size_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
-
 // Sizes of the workspace: the tiles' states, sums and pass flags; backward also the states'
 // gradients, a second array of sums, and the workgroups' shares of dB and dC.
 struct ScanPlan {
@@ -173,15 +140,6 @@ struct ScanPlan {
     size_t fwd_bytes() const { return chained ? states + sums + flags : 0; }
     size_t bwd_bytes() const { return 2 * states + 2 * sums + flags + shares + kept_h + kept_dt; }
 };
-
-gdn2_status check_workspace(const void *ws, size_t bytes, size_t need) {
-    if (need == 0) return GDN2_OK;
-    if (!ws) return report(GDN2_ERR_WORKSPACE, "workspace is NULL");
-    if (bytes < need) return report(GDN2_ERR_WORKSPACE, "workspace is too small");
-    if (reinterpret_cast<uintptr_t>(ws) % kAlign != 0)
-        return report(GDN2_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    return GDN2_OK;
-}
 
 // ---- block norm --------------------------------------------------------------------------
 

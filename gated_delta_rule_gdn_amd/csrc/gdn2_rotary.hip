@@ -1,0 +1,381 @@
+// gdn2_rotary.hip -- norms of queries and keys per head with the rotation by position in one pass,
+// into plain tensors or into the pages of a cache, and their gradients.
+//
+// Per token at position p and per head, with r = 1 / sqrt(mean(x^2) + eps) and R = d_rot:
+//     y = x r w,   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s)  for the R/2 pairs (a, b),
+// c and s the cosine and sine of the pair's angle at p, taken from a table; pairs are (i, i + R/2)
+// or (2i, 2i + 1), values from R on stay. Without w there is no norm. Gradients, from g = dy turned
+// back by the same angles (a rotation's transpose):
+//     dw = sum over tokens and heads of g x r,     dx = r (g w - x r^2 mean(g w x)).
+//
+// Bound by memory: every value is read once and written once. A head's row lives in the registers
+// of L lanes. A lane holds P units of 2 V values, the two members of V pairs (V neighbours each, so
+// a unit is two accesses of up to 16 bytes), and the rotation needs no exchange between lanes; the
+// values that are not rotated are cut into pairs in the same way. A wave takes a token's heads,
+// 64 / L at a time, with the token's cosines and sines and the weights in registers. Sums and
+// rotation are fp32, rounded once at the store.
+#include "gdn2_internal.h"
+#include "gdn2_layer.h"
+
+namespace gdn2 {
+
+namespace {
+
+// Where a lane's units lie in a row: unit u = lane + i L holds values a(u) .. a(u) + V - 1 and
+// b(u) .. b(u) + V - 1, whose angles are the table's columns c(u) .. c(u) + V - 1.
+template <int V, int L, int P>
+struct Units {
+    int lane, d, half, rest;     // half = R / 2; rest = (d - R) / 2
+    bool interleaved;
+    __device__ __forceinline__ int pair(int i) const { return (lane + i * L) * V; }
+    __device__ __forceinline__ bool in(int i) const { return pair(i) < half + rest; }
+    __device__ __forceinline__ bool turns(int i) const { return pair(i) < half; }
+    // interleaved: one run of 2 V values
+    __device__ __forceinline__ int a(int i) const {
+        return interleaved ? 2 * pair(i) : turns(i) ? pair(i) : half + pair(i);
+    }
+    __device__ __forceinline__ int b(int i) const {
+        return interleaved ? 2 * pair(i) + V : turns(i) ? half + pair(i) : half + rest + pair(i);
+    }
+};
+
+// The two members of a lane's pairs: x[i][0][v] and x[i][1][v].
+template <int V, int P>
+using Pairs = float[P][2][V];
+
+// A unit in memory is two runs of V values at a and b. In the interleaved order they are the first
+// and the second V of 2 V neighbours, member m of pair v being value 2 v + m.
+template <typename T, int V, int L, int P>
+__device__ __forceinline__ void load_pairs(const T *row, const Units<V, L, P> &k, Pairs<V, P> &x) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        float lo[V] = {}, hi[V] = {};
+        if (k.in(i)) {
+            ldv<T, V>(row + k.a(i), lo);
+            ldv<T, V>(row + k.b(i), hi);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float p = 2 * v < V ? lo[2 * v % V] : hi[2 * v % V];
+            const float q = 2 * v + 1 < V ? lo[(2 * v + 1) % V] : hi[(2 * v + 1) % V];
+            x[i][0][v] = k.interleaved ? p : lo[v];
+            x[i][1][v] = k.interleaved ? q : hi[v];
+        }
+    }
+}
+
+template <typename T, int V, int L, int P>
+__device__ __forceinline__ void store_pairs(T *row, const Units<V, L, P> &k, const Pairs<V, P> &x) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        float lo[V], hi[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            lo[v] = k.interleaved ? x[i][v & 1][v / 2] : x[i][0][v];
+            hi[v] = k.interleaved ? x[i][(V + v) & 1][(V + v) / 2] : x[i][1][v];
+        }
+        if (k.in(i)) {
+            stv<T, V>(row + k.a(i), lo);
+            stv<T, V>(row + k.b(i), hi);
+        }
+    }
+}
+
+// Cosines and sines of a lane's pairs; 1 and 0 where nothing turns.
+template <int V, int L, int P>
+__device__ __forceinline__ void load_turn(const float *row, const Units<V, L, P> &k, Pairs<V, P> &t) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        if (k.turns(i)) {
+            ldv<float, V>(row + k.pair(i), t[i][0]);
+            ldv<float, V>(row + k.half + k.pair(i), t[i][1]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                t[i][0][v] = 1.f;
+                t[i][1][v] = 0.f;
+            }
+        }
+    }
+}
+
+// Sum over the L lanes of a row.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+    for (int m = 1; m < L; m <<= 1) x += __shfl_xor(x, m);
+    return x;
+}
+
+template <int V, int P>
+__device__ __forceinline__ float dot(const Pairs<V, P> &x, const Pairs<V, P> &y) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) s = fmaf(x[i][0][v], y[i][0][v], fmaf(x[i][1][v], y[i][1][v], s));
+    return s;
+}
+
+// The row of cos_sin of a token, or a negative number for padding.
+__device__ __forceinline__ int position_of(const RotaryArgs &a, int token) {
+    const int p = a.positions ? a.positions[token] : token % a.seqlen;
+    return p >= 0 && (p < a.num_positions || a.d_rot == 0) ? p : -1;
+}
+
+// A wave takes one token and every gridDim.y-th set of 64 / L of its heads; the sets are those of q,
+// then of k, then of v (which is copied).
+template <typename T, int V, int L, int P>
+__global__ __launch_bounds__(256) void rotary_fwd_kernel(RotaryArgs a) {
+    constexpr int H = 64 / L;
+    const int lane = threadIdx.x & 63;
+    const int64_t token = (static_cast<int64_t>(blockIdx.x) * 4) + (threadIdx.x >> 6);
+    if (token >= a.tokens) return;
+    const Units<V, L, P> k{lane % L, a.d, a.d_rot / 2, (a.d - a.d_rot) / 2, a.interleaved};
+    const int at = __builtin_amdgcn_readfirstlane(position_of(a, static_cast<int>(token)));
+    Pairs<V, P> turn;
+    if (at >= 0) load_turn<V, L, P>(a.cos_sin + static_cast<int64_t>(at) * a.d_rot, k, turn);
+    int64_t place = -1;
+    int64_t page = 0;
+    int within = 0;
+    if (a.slots && at >= 0) {
+        place = a.slots[token];
+        if (place >= a.num_places) place = -1;
+        page = place / a.page_size;
+        within = static_cast<int>(place % a.page_size);
+    }
+    const int sets_q = (a.h_q + H - 1) / H, sets_k = (a.h_k + H - 1) / H;
+    const int sets = sets_q + (a.slots ? 2 : 1) * sets_k;
+    for (int set = blockIdx.y; set < sets; set += gridDim.y) {
+        const int kind = set < sets_q ? 0 : set < sets_q + sets_k ? 1 : 2;
+        const int head = (set - (kind == 0 ? 0 : kind == 1 ? sets_q : sets_q + sets_k)) * H + lane / L;
+        const int heads = kind == 0 ? a.h_q : a.h_k;
+        if (kind && a.slots && place < 0) break;
+        const bool mine = head < heads;
+        const T *src = static_cast<const T *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                       token * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) +
+                       static_cast<int64_t>(head) * a.d;
+        T *dst = static_cast<T *>(kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out);
+        if (kind && a.slots) dst += ((page * a.h_k + head) * a.page_size + within) * a.d;
+        else dst += (token * heads + head) * a.d;
+        Pairs<V, P> x;
+        if (mine && at >= 0) {
+            load_pairs<T, V, L, P>(src, k, x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[i][0][v] = x[i][1][v] = 0.f;
+        }
+        if (kind < 2 && at >= 0) {
+            const float *weight = kind == 0 ? a.q_weight : a.k_weight;
+            if (weight) {
+                Pairs<V, P> w;
+                load_pairs<float, V, L, P>(weight, k, w);
+                const float r = rsqrtf(lanes_sum<L>(dot<V, P>(x, x)) / a.d + a.eps);
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        x[i][0][v] *= r * w[i][0][v];
+                        x[i][1][v] *= r * w[i][1][v];
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                if (k.turns(i))
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float c = turn[i][0][v], s = turn[i][1][v], p = x[i][0][v], q = x[i][1][v];
+                        x[i][0][v] = fmaf(p, c, -q * s);
+                        x[i][1][v] = fmaf(q, c, p * s);
+                    }
+        }
+        if (mine) store_pairs<T, V, L, P>(dst, k, x);
+    }
+}
+
+// A wave takes every 4 gridDim.x-th token with all its heads and keeps its columns' sums of the
+// weights' gradients in registers; a workgroup's leave as one row of a.partial, [2][d].
+template <typename T, typename TG, int V, int L, int P>
+__global__ __launch_bounds__(256) void rotary_bwd_kernel(RotaryArgs a) {
+    constexpr int H = 64 / L;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const Units<V, L, P> k{lane % L, a.d, a.d_rot / 2, (a.d - a.d_rot) / 2, a.interleaved};
+    Pairs<V, P> dw[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) dw[n][i][0][v] = dw[n][i][1][v] = 0.f;
+    for (int64_t token = static_cast<int64_t>(blockIdx.x) * 4 + wave; token < a.tokens;
+         token += static_cast<int64_t>(gridDim.x) * 4) {
+        const int at = __builtin_amdgcn_readfirstlane(position_of(a, static_cast<int>(token)));
+        Pairs<V, P> turn;
+        if (at >= 0) load_turn<V, L, P>(a.cos_sin + static_cast<int64_t>(at) * a.d_rot, k, turn);
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+            const int heads = kind ? a.h_k : a.h_q;
+            const float *weight = kind ? a.k_weight : a.q_weight;
+            const T *src = static_cast<const T *>(kind ? a.k : a.q) + token * (kind ? a.k_stride : a.q_stride);
+            const TG *dy = static_cast<const TG *>(kind ? a.dk_out : a.dq_out) + token * heads * a.d;
+            TG *dst = static_cast<TG *>(kind ? a.dk : a.dq) + token * heads * a.d;
+            for (int head = lane / L; head < heads + lane / L; head += H) {
+                const bool mine = head < heads;
+                Pairs<V, P> g, x;
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) g[i][0][v] = g[i][1][v] = x[i][0][v] = x[i][1][v] = 0.f;
+                if (mine && at >= 0) {
+                    load_pairs<TG, V, L, P>(dy + head * a.d, k, g);
+                    if (weight) load_pairs<T, V, L, P>(src + head * a.d, k, x);
+                }
+                if (at >= 0) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i)
+                        if (k.turns(i))
+#pragma unroll
+                            for (int v = 0; v < V; ++v) {
+                                const float c = turn[i][0][v], s = turn[i][1][v], p = g[i][0][v], q = g[i][1][v];
+                                g[i][0][v] = fmaf(p, c, q * s);
+                                g[i][1][v] = fmaf(q, c, -p * s);
+                            }
+                    if (weight) {
+                        Pairs<V, P> w;
+                        load_pairs<float, V, L, P>(weight, k, w);
+                        const float r = rsqrtf(lanes_sum<L>(dot<V, P>(x, x)) / a.d + a.eps);
+#pragma unroll
+                        for (int i = 0; i < P; ++i)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                for (int v = 0; v < V; ++v) {
+                                    if (mine) dw[kind][i][m][v] = fmaf(g[i][m][v], x[i][m][v] * r, dw[kind][i][m][v]);
+                                    g[i][m][v] *= w[i][m][v];
+                                }
+                        const float mean = lanes_sum<L>(dot<V, P>(g, x)) / a.d * r * r;
+#pragma unroll
+                        for (int i = 0; i < P; ++i)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                for (int v = 0; v < V; ++v) g[i][m][v] = r * (g[i][m][v] - x[i][m][v] * mean);
+                    }
+                }
+                if (mine) store_pairs<TG, V, L, P>(dst + head * a.d, k, g);
+            }
+        }
+    }
+    if (!a.q_weight && !a.k_weight) return;
+    // the lanes that hold the same columns, then the four waves
+    __shared__ float s_sum[4][2 * 512];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float x = dw[n][i][m][v];
+#pragma unroll
+                    for (int s = L; s < 64; s <<= 1) x += __shfl_xor(x, s);
+                    dw[n][i][m][v] = x;
+                }
+    if (lane < L)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) store_pairs<float, V, L, P>(s_sum[wave] + n * a.d, k, dw[n]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.d; c += 256)
+        a.partial[static_cast<int64_t>(blockIdx.x) * 2 * a.d + c] =
+            (s_sum[0][c] + s_sum[1][c]) + (s_sum[2][c] + s_sum[3][c]);
+}
+
+// The weights' gradients: the rows of a.partial added in a fixed order, 32 columns per workgroup,
+// whose 32 halves of waves each take every 32nd row.
+__global__ __launch_bounds__(1024) void rotary_reduce_kernel(RotaryArgs a, int parts) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, half = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + lane;
+    float sum = 0.f;
+    if (col < 2 * a.d)
+#pragma unroll 8
+        for (int i = half; i < parts; i += 32) sum += a.partial[static_cast<int64_t>(i) * 2 * a.d + col];
+    s[half][lane] = sum;
+    __syncthreads();
+    if (half != 0 || col >= 2 * a.d) return;
+#pragma unroll
+    for (int i = 1; i < 32; ++i) sum += s[i][lane];
+    if (col < a.d) {
+        if (a.q_weight) a.dq_weight[col] = sum;
+    } else if (a.k_weight) {
+        a.dk_weight[col - a.d] = sum;
+    }
+}
+
+template <typename T, typename TG, int V, int L, int P>
+hipError_t launch(const RotaryArgs &a, bool backward, hipStream_t st) {
+    if (!backward) {
+        hipLaunchKernelGGL((rotary_fwd_kernel<T, V, L, P>), dim3(static_cast<unsigned>((a.tokens + 3) / 4), 1),
+                           dim3(256), 0, st, a);
+        return hipGetLastError();
+    }
+    const int parts = rotary_parts(a.tokens);
+    hipLaunchKernelGGL((rotary_bwd_kernel<T, TG, V, L, P>), dim3(parts), dim3(256), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !(a.q_weight || a.k_weight)) return e;
+    hipLaunchKernelGGL(rotary_reduce_kernel, dim3((2 * a.d + 31) / 32), dim3(1024), 0, st, a, parts);
+    return hipGetLastError();
+}
+
+template <typename T, typename TG, int V>
+hipError_t launch_rows(const RotaryArgs &a, bool backward, hipStream_t st) {
+    const int units = a.d / (2 * V);
+    if constexpr (V == 1) {
+        if (units <= 64) return launch<T, TG, 1, 16, 4>(a, backward, st);
+        return launch<T, TG, 1, 64, 4>(a, backward, st);
+    } else {
+        if (units <= 4) return launch<T, TG, V, 4, 1>(a, backward, st);
+        if (units <= 8) return launch<T, TG, V, 8, 1>(a, backward, st);
+        if (units <= 16) return launch<T, TG, V, 16, 1>(a, backward, st);
+        if (units <= 32) return launch<T, TG, V, 32, 1>(a, backward, st);
+        return launch<T, TG, V, 64, 1>(a, backward, st);
+    }
+}
+
+bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Whether every run of V pairs' members can be taken in whole accesses.
+bool whole(const RotaryArgs &a, int V) {
+    const int half = a.d_rot / 2, rest = (a.d - a.d_rot) / 2;
+    return half % V == 0 && rest % V == 0 && a.q_stride % V == 0 && a.k_stride % V == 0 &&
+           a.v_stride % V == 0 && al16(a.q) && al16(a.k) && al16(a.v) && al16(a.cos_sin) && al16(a.q_weight) &&
+           al16(a.k_weight) && al16(a.q_out) && al16(a.k_out) && al16(a.v_out) && al16(a.dq_out) &&
+           al16(a.dk_out) && al16(a.dq) && al16(a.dk);
+}
+
+template <typename T, typename TG>
+hipError_t launch_types(const RotaryArgs &a, bool backward, hipStream_t st) {
+    constexpr int V = sizeof(T) == 2 ? 8 : 4;
+    return whole(a, V) ? launch_rows<T, TG, V>(a, backward, st) : launch_rows<T, TG, 1>(a, backward, st);
+}
+
+}  // namespace
+
+int rotary_parts(int tokens) {
+    const int groups = tokens / 4 + (tokens % 4 != 0);
+    return groups < 1 ? 1 : groups < 1024 ? groups : 1024;
+}
+
+hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st) {
+    return a.bf16 ? launch_types<bf16_t, bf16_t>(a, false, st) : launch_types<float, float>(a, false, st);
+}
+
+hipError_t launch_rotary_bwd(const RotaryArgs &a, hipStream_t st) {
+    if (!a.bf16) return launch_types<float, float>(a, true, st);
+    return a.grad_bf16 ? launch_types<bf16_t, bf16_t>(a, true, st) : launch_types<bf16_t, float>(a, true, st);
+}
+
+}  // namespace gdn2

@@ -36,7 +36,13 @@
  *                               prompts, its gradients, and for single tokens;
  *   - gdn2_block_norm_fwd, gdn2_block_norm_bwd
  *                               the norms after and before a block, fused with its gate, the
- *                               residual and its scale, and their gradients.
+ *                               residual and its scale, and their gradients;
+ *   - gdn2_qk_rotary_fwd, gdn2_qk_rotary_bwd, gdn2_qk_rotary_append
+ *                               the attention layer that hybrid stacks put beside the recurrent
+ *                               ones: norms of queries and keys per head with the rotation by
+ *                               position, their gradients, and into the pages of a cache;
+ *   - gdn2_paged_attention_step the attention of new tokens over that cache;
+ *   - gdn2_pool_copy            slots of pools copied: pages of a cache, states of sequences.
  * Calls added since version 9 of the ABI change none of its calls, so the number stays.
  *
  * Conventions (the pages are silent on these; this is the reading the library implements):
@@ -675,6 +681,148 @@ gdn2_status gdn2_block_norm_bwd(const void *x, const void *gate, const void *res
                                 void *dgate, void *dresidual, float *dnorm_weight, float *dscale,
                                 float *dnext_weight, const gdn2_norm_dims *dims, void *workspace,
                                 size_t workspace_bytes, void *stream);
+
+/*
+ * ---- The attention layer of hybrid stacks ------------------------------------------------
+ *
+ * Stacks of recurrent layers keep a softmax attention layer every few layers. The calls below
+ * are what such a layer needs beside its projections: its queries and keys normed per head and
+ * rotated by position, in training and in front of a cache; the attention of new tokens over the
+ * cache; and copies of slots, for the cache's pages and for the state pools of the recurrent
+ * layers. Layouts:
+ *   q, q_out, o        [B, T, h_q, d];   k, v  [B, T, h_k, d]      (q head j reads k head j / (h_q / h_k))
+ *   k_pages, v_pages   [num_pages][h_k][page_size][d]: a page holds page_size consecutive tokens of
+ *                      one sequence, each head's rows contiguous. Place `slot` of a pool of pages is
+ *                      row slot % page_size of page slot / page_size.
+ * Strides, types, sums, sizes and overlaps are as around the recurrence above: token strides of
+ * column slices (0: contiguous), fp32 sums and statistics, the same bits at every call (no
+ * atomics), outputs that overlap nothing else.
+ */
+
+typedef struct gdn2_rotary_dims {
+    int32_t batch, seqlen;             /* B, T >= 0 */
+    int32_t h_q, h_k;                  /* heads, h_q >= 1; h_k = 0: no keys (fwd and bwd) */
+    int32_t d;                         /* values per head: even, 2 .. 512 */
+    int32_t d_rot;                     /* the first d_rot of them are rotated: even, 0 .. d */
+    int32_t interleaved;               /* 0: pairs (i, i + d_rot/2); nonzero: pairs (2i, 2i + 1) */
+    int32_t num_positions;             /* rows of cos_sin, >= 1 (>= 0 with d_rot = 0) */
+    int32_t dtype;                     /* gdn2_dtype of q, k, v, their outputs and the pages */
+    int32_t grad_dtype;                /* of dq_out, dk_out, dq, dk (backward only) */
+    float eps;                         /* >= 0; with 0 a row of zeros gives NaN */
+    int64_t q_stride, k_stride, v_stride;   /* elements between tokens, or 0 */
+} gdn2_rotary_dims;
+
+/*
+ * Per token and head: y = x / sqrt(mean(x^2) + eps) weight (without a weight y = x), then pair i
+ * of the first d_rot values turns by the angle of the token's position p,
+ *     y_a' = y_a cos[p][i] - y_b sin[p][i],   y_b' = y_b cos[p][i] + y_a sin[p][i],
+ * all in fp32 and rounded once.
+ *   q            device [B, T, h_q, d];  k  device [B, T, h_k, d], or NULL with h_k = 0
+ *   cos_sin      device fp32 [num_positions][d_rot]: d_rot/2 cosines, then d_rot/2 sines (NULL with
+ *                d_rot = 0)
+ *   positions    device int32 [B, T], or NULL: token t of each sequence is at position t. A position
+ *                outside [0, num_positions) marks a padding token: zero rows come out. (With
+ *                d_rot = 0 only negative ones do.)
+ *   q_weight, k_weight   device fp32 [d], each may be NULL
+ *   q_out, k_out contiguous. May be q's and k's own buffers, if those are contiguous.
+ */
+gdn2_status gdn2_qk_rotary_fwd(const void *q, const void *k, const float *cos_sin,
+                               const int32_t *positions, const float *q_weight, const float *k_weight,
+                               void *q_out, void *k_out, const gdn2_rotary_dims *dims, void *stream);
+
+/* Bytes of device workspace gdn2_qk_rotary_bwd needs, or 0 if the dims are invalid. */
+size_t gdn2_qk_rotary_bwd_workspace_bytes(const gdn2_rotary_dims *dims);
+
+/*
+ * Gradients of gdn2_qk_rotary_fwd, which is formed again from its inputs.
+ *   dq_out, dk_out   device, contiguous (grad_dtype): dL/dq_out, dL/dk_out
+ *   dq, dk           device, contiguous (grad_dtype); rows of padding tokens come out zero, and give
+ *                    nothing to the weights' gradients
+ *   dq_weight, dk_weight   device fp32 [d], each required with its weight
+ *   workspace        at least gdn2_qk_rotary_bwd_workspace_bytes() bytes, 256-byte aligned; not
+ *                    needed without weights
+ */
+gdn2_status gdn2_qk_rotary_bwd(const void *q, const void *k, const float *cos_sin,
+                               const int32_t *positions, const float *q_weight, const float *k_weight,
+                               const void *dq_out, const void *dk_out, void *dq, void *dk,
+                               float *dq_weight, float *dk_weight, const gdn2_rotary_dims *dims,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn2_qk_rotary_fwd in front of a cache: q_out is written as there, the keys and the values (as
+ * they are) go to the pages. For whole prompts, packed or not, and for single tokens: a token's
+ * place is given by its slot.
+ *   positions        device int32 [B, T], required
+ *   slots            device int32 [B, T]: the place of each token in the pages, distinct. Outside
+ *                    [0, num_pages * page_size): the token is not put anywhere (its q row is
+ *                    written all the same). A padding token (by its position) is not put anywhere
+ *                    either.
+ *   q_out            contiguous. May be q's own buffer, if that is contiguous.
+ *   k_pages, v_pages num_pages * page_size <= 2^31 - 1
+ */
+gdn2_status gdn2_qk_rotary_append(const void *q, const void *k, const void *v, const float *cos_sin,
+                                  const int32_t *positions, const float *q_weight,
+                                  const float *k_weight, const int32_t *slots, void *q_out,
+                                  void *k_pages, void *v_pages, int32_t num_pages, int32_t page_size,
+                                  const gdn2_rotary_dims *dims, void *stream);
+
+typedef struct gdn2_attention_dims {
+    int32_t num_seqs;                  /* N >= 0 */
+    int32_t new_tokens;                /* T >= 1: query tokens per sequence */
+    int32_t h_q, h_k;                  /* h_q a multiple of h_k */
+    int32_t d;                         /* 64, 128 or 256 */
+    int32_t num_pages, page_size;      /* num_pages * h_k * page_size <= 2^31 - 1 */
+    int32_t max_pages;                 /* columns of page_table; max_pages * page_size <= 2^30 */
+    int32_t window;                    /* a query sees this many keys at most, its own among them;
+                                          0: all before it */
+    int32_t dtype;                     /* gdn2_dtype of q, the pages and o */
+    float scale;                       /* of the products of queries and keys; finite */
+    int64_t q_stride;                  /* elements between tokens of q, or 0 */
+} gdn2_attention_dims;
+
+/*
+ * Bytes of device workspace gdn2_paged_attention_step needs for these dims (0 too where it needs
+ * none, and if the dims are invalid). They do not depend on the lengths.
+ */
+size_t gdn2_paged_attention_step_workspace_bytes(const gdn2_attention_dims *dims);
+
+/*
+ * The last T tokens of each of N sequences attend to the sequence's cached tokens, themselves among
+ * them (gdn2_qk_rotary_append puts them there first). Token t of sequence n stands at place
+ * p = seq_lens[n] - T + t and sees the places j <= p, with a window those with j > p - window:
+ *     s_j = scale q . k_j,   o = sum_j softmax(s)_j v_j,   lse = log sum_j e^(s_j)
+ * A token that sees nothing (an empty sequence; more new tokens than the sequence has) gives o = 0
+ * and lse = -inf. What lies in the pages at places that no token sees is never used, NaN included.
+ *   q            device [N, T, h_q, d]
+ *   k_pages, v_pages   device [num_pages][h_k][page_size][d], 16-byte aligned
+ *   page_table   device int32 [N][max_pages]: the page of each page_size tokens of a sequence. Only
+ *                entries of places that are seen are used; held inside [0, num_pages). Sequences may
+ *                share pages.
+ *   seq_lens     device int32 [N], the cached tokens of each sequence with the new ones; held inside
+ *                [0, max_pages * page_size]
+ *   o            device [N, T, h_q, d], contiguous, 16-byte aligned
+ *   lse          device fp32 [N, T, h_q], or NULL
+ *   workspace    at least gdn2_paged_attention_step_workspace_bytes() bytes, 256-byte aligned
+ */
+gdn2_status gdn2_paged_attention_step(const void *q, const void *k_pages, const void *v_pages,
+                                      const int32_t *page_table, const int32_t *seq_lens, void *o,
+                                      float *lse, const gdn2_attention_dims *dims, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/*
+ * Copies slots inside each of several pools: slot dst[i] takes the bytes of slot src[i], for every
+ * i < count and every pool. The pages of a cache are slots of two pools per layer, a recurrent
+ * layer's states, conv states and scan states slots of one each; a forked sequence, or a pool
+ * whose sequences are moved together, is one call over all layers.
+ *   pools        HOST array of num_pools device pointers, pool p being [num_slots] slots of
+ *                slot_bytes[p] bytes (HOST array, each >= 1)
+ *   src, dst     device int32 [count]. A pair with an entry outside [0, num_slots) is skipped. One
+ *                source may have many destinations. The destinations have to be distinct, and none
+ *                may be the source of another pair.
+ */
+gdn2_status gdn2_pool_copy(void *const *pools, const int64_t *slot_bytes, int32_t num_pools,
+                           int32_t num_slots, const int32_t *src, const int32_t *dst, int32_t count,
+                           void *stream);
 
 /*
  * Host helper: checks a HOST copy of cu_seqlens (N+1 entries) against total tokens T.
