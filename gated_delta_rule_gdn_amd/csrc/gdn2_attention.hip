@@ -29,8 +29,6 @@ constexpr int kWaves = 4;
 constexpr int kTargetGroups = 1024;
 constexpr int kLeastSteps = 4;
 
-constexpr int tile_keys(bool bf16) { return bf16 ? 32 : 16; }
-
 __device__ __forceinline__ int wave_sum(int x) {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
@@ -97,36 +95,39 @@ __device__ __forceinline__ Part find_part(const AttentionArgs &a, int per, int i
     return Part{-1, 0, 0, 0};
 }
 
-// The weights of a tile of keys as B operands of the second product. bf16 holds a weight as the sum
-// of two (8 bits each, 2^-17 of the weight off at most): one alone would put an error of the size of
-// the output's own rounding into every weight.
+// Weights of keys as B operands of the second product. bf16 holds a weight as the sum of two (8 bits
+// each, 2^-17 of the weight off at most): one alone would put an error of the size of the output's
+// own rounding into every weight.
+template <typename O>
 struct Split {
-    u32x4 hi, lo;
+    O hi, lo;
 };
-__device__ __forceinline__ Split operand(const f32x4 (&p)[2]) {
-    Split b;
-    b.hi = dpair_to_b32(p[0], p[1]);
-    f32x4 rest[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = b.hi[2 * t + i / 2];
-            rest[t][i] = p[t][i] - (i % 2 ? bf16_hi(w) : bf16_lo(w));
-        }
-    b.lo = dpair_to_b32(rest[0], rest[1]);
-    return b;
+__device__ __forceinline__ f32x4 rest_of(f32x4 p, uint32_t a, uint32_t b) {
+    return f32x4{p.x - bf16_lo(a), p.y - bf16_hi(a), p.z - bf16_lo(b), p.w - bf16_hi(b)};
 }
-__device__ __forceinline__ f32x4 operand(const f32x4 (&p)[1]) { return p[0]; }
+__device__ __forceinline__ Split<u32x4> operand(const f32x4 (&p)[2], bf16_t) {
+    const u32x4 hi = dpair_to_b32(p[0], p[1]);
+    return Split<u32x4>{hi, dpair_to_b32(rest_of(p[0], hi.x, hi.y), rest_of(p[1], hi.z, hi.w))};
+}
+__device__ __forceinline__ Split<u32x2> operand(const f32x4 (&p)[1], bf16_t) {
+    const u32x2 hi = f4_to_b16(p[0]);
+    return Split<u32x2>{hi, f4_to_b16(rest_of(p[0], hi.x, hi.y))};
+}
+__device__ __forceinline__ f32x4 operand(const f32x4 (&p)[1], float) { return p[0]; }
 
-// The operand types of the two products.
+// Keys of a tile: what a wave holds of keys and values at once, 64 registers (fp32 of 256 values: 128).
+template <typename T> constexpr int tile_keys(int d) { return sizeof(T) == 2 && d <= 128 ? 32 : 16; }
+
+// Waves per SIMD that the registers are held to.
+template <typename T, int D, int MT> constexpr int waves_per_simd() {
+    return sizeof(T) == 4 && D == 256 ? 1 : D == 128 && MT == 1 ? 3 : 2;
+}
+
+// The first product: QW values of a head per operand of a lane's 16 bytes.
 template <typename T> struct Ops;
-
-// bf16: 32 keys per tile, one instruction per 32 values of a head.
 template <> struct Ops<bf16_t> {
-    static constexpr int KT = 32, QW = 32;       // keys of a tile; values of a head per product
+    static constexpr int QW = 32;
     typedef u32x4 Frag;                          // 8 values of a q or k row
-    typedef Split Weights;
     static __device__ __forceinline__ f32x4 qk(Frag k, Frag q, f32x4 c) { return mma_k32(k, q, c); }
     static __device__ __forceinline__ Frag each(const bf16_t *p) {      // value by value
         Frag f;
@@ -135,11 +136,9 @@ template <> struct Ops<bf16_t> {
         return f;
     }
 };
-// fp32: 16 keys per tile, four instructions per 16 values.
 template <> struct Ops<float> {
-    static constexpr int KT = 16, QW = 16;
+    static constexpr int QW = 16;
     typedef f32x4 Frag;
-    typedef f32x4 Weights;
     static __device__ __forceinline__ f32x4 qk(Frag k, Frag q, f32x4 c) { return mma_k16_f32(k, q, c); }
     static __device__ __forceinline__ Frag each(const float *p) { return Frag{p[0], p[1], p[2], p[3]}; }
 };
@@ -148,18 +147,14 @@ template <> struct Ops<float> {
 template <typename T, int D> struct VRows;
 
 template <int D> struct VRows<bf16_t, D> {
-    static constexpr int VR = 8, VE = D < 128 ? D / 16 : 8, S = D / (16 * VE), W = VE / 2;
+    static constexpr int VR = tile_keys<bf16_t>(D) / 4, VE = D < 128 ? D / 16 : 8, S = D / (16 * VE), W = VE / 2;
     typedef uint32_t words __attribute__((ext_vector_type(W)));
+    typedef uint32_t Oper __attribute__((ext_vector_type(VR / 2)));
+    typedef Split<Oper> Weights;
     words w[VR][S];
     __device__ __forceinline__ void load(int r, const bf16_t *row, int li) {
 #pragma unroll
         for (int s = 0; s < S; ++s) w[r][s] = *reinterpret_cast<const words *>(row + (s * 16 + li) * VE);
-    }
-    __device__ __forceinline__ void clear(int r) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int i = 0; i < W; ++i) w[r][s][i] = 0;
     }
     __device__ __forceinline__ bool finite() const {
         bool f = true;
@@ -174,26 +169,32 @@ template <int D> struct VRows<bf16_t, D> {
     }
     // the key of a lane's row r within the tile: those of the output tiles' rows
     static __device__ __forceinline__ int key(int lg, int r) { return perm_k<true>(lg, r); }
-    // o += V^T P^T for value j of set s
-    __device__ __forceinline__ f32x4 pv(int s, int j, const Split &p, f32x4 o) const {
-        u32x4 v;
+    // bits of the operand that belong to row r, if it is seen
+    static __device__ __forceinline__ void see(int r, bool seen, Oper &bits) {
+        if (r % 2 == 0) bits[r / 2] = 0;
+        if (seen) bits[r / 2] |= r % 2 ? 0xffff0000u : 0xffffu;
+    }
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) { return mma_k32(a, b, c); }
+    static __device__ __forceinline__ f32x4 mma(u32x2 a, u32x2 b, f32x4 c) { return mma_k16_bf16(a, b, c); }
+    // o += V^T P^T for value j of set s, of the rows in `bits`
+    __device__ __forceinline__ f32x4 pv(int s, int j, const Weights &p, f32x4 o, const Oper *bits = nullptr) const {
+        Oper v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)      // the same half of two rows' words
+        for (int i = 0; i < VR / 2; ++i)      // the same half of two rows' words
             v[i] = __builtin_amdgcn_perm(w[2 * i + 1][s][j / 2], w[2 * i][s][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
-        return mma_k32(v, p.lo, mma_k32(v, p.hi, o));
+        if (bits) v &= *bits;
+        return mma(v, p.lo, mma(v, p.hi, o));
     }
 };
 
 template <int D> struct VRows<float, D> {
     static constexpr int VR = 4, VE = 4, S = D / 64;
+    typedef u32x4 Oper;
+    typedef f32x4 Weights;
     f32x4 w[VR][S];
     __device__ __forceinline__ void load(int r, const float *row, int li) {
 #pragma unroll
         for (int s = 0; s < S; ++s) w[r][s] = *reinterpret_cast<const f32x4 *>(row + (s * 16 + li) * VE);
-    }
-    __device__ __forceinline__ void clear(int r) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) w[r][s] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     __device__ __forceinline__ bool finite() const {
         bool f = true;
@@ -206,20 +207,26 @@ template <int D> struct VRows<float, D> {
         return f;
     }
     static __device__ __forceinline__ int key(int lg, int r) { return 4 * lg + r; }
-    __device__ __forceinline__ f32x4 pv(int s, int j, f32x4 p, f32x4 o) const {
-        return mma_k16_f32(f32x4{w[0][s][j], w[1][s][j], w[2][s][j], w[3][s][j]}, p, o);
+    static __device__ __forceinline__ void see(int r, bool seen, u32x4 &bits) { bits[r] = seen ? ~0u : 0u; }
+    __device__ __forceinline__ f32x4 pv(int s, int j, f32x4 p, f32x4 o, const u32x4 *bits = nullptr) const {
+        f32x4 v = {w[0][s][j], w[1][s][j], w[2][s][j], w[3][s][j]};
+        if (bits) v = __builtin_bit_cast(f32x4, __builtin_bit_cast(u32x4, v) & *bits);
+        return mma_k16_f32(v, p, o);
     }
 };
 
 template <typename T, int D, int MT>
-__global__ __launch_bounds__(64 * kWaves) void paged_attention_kernel(AttentionArgs a, int row_blocks) {
+__global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void paged_attention_kernel(AttentionArgs a, int row_blocks) {
     using Op = Ops<T>;
     using V = VRows<T, D>;
-    constexpr int KT = Op::KT, ST = KT / 16, QF = D / Op::QW, ROWS = 16 * MT;
+    constexpr int KT = tile_keys<T>(D), ST = KT / 16, QF = D / Op::QW, ROWS = 16 * MT;
     constexpr int LV = 16 / sizeof(T);           // values of a 16-byte access
+    typedef typename Op::Frag Frag;
+    __shared__ Frag s_q[MT * QF * 64];
     __shared__ float s_ml[kWaves][2][ROWS];
-    __shared__ f32x4 s_o[2][MT * V::S * V::VE * 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lg = lane >> 4, li = lane & 15;
+    __shared__ f32x4 s_o[2][V::S * V::VE * 64];
+    const int lane = threadIdx.x & 63, lg = lane >> 4, li = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = a.h_k * row_blocks;
     const int sub = static_cast<int>(blockIdx.x % heads), h = sub / row_blocks, rb = sub % row_blocks;
     const int G = a.h_q / a.h_k, R = a.new_tokens * G;
@@ -247,7 +254,7 @@ __global__ __launch_bounds__(64 * kWaves) void paged_attention_kernel(AttentionA
     // between these, every row sees every key
     const int lo_all = first_of(t1), hi_all = end_of(t0);
 
-    typename Op::Frag q[MT][QF];
+    // q as the first product's B operands, in LDS: [MT][QF][64 lanes]
     int row_t[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -256,12 +263,12 @@ __global__ __launch_bounds__(64 * kWaves) void paged_attention_kernel(AttentionA
         const T *p = static_cast<const T *>(a.q) +
                      (static_cast<int64_t>(part.n) * a.new_tokens + row_t[mt]) * a.q_stride +
                      static_cast<int64_t>(h * G + rr % G) * D;
-#pragma unroll
-        for (int f = 0; f < QF; ++f) {
+        for (int f = wave; f < QF; f += kWaves) {
             const T *at = p + f * Op::QW + lg * LV;
-            q[mt][f] = a.q_whole ? *reinterpret_cast<const typename Op::Frag *>(at) : Op::each(at);
+            s_q[(mt * QF + f) * 64 + lane] = a.q_whole ? *reinterpret_cast<const Frag *>(at) : Op::each(at);
         }
     }
+    __syncthreads();
 
     f32x4 o[MT][V::S][V::VE];
     float m[MT], l[MT];                          // l: this lane's keys only
@@ -275,13 +282,10 @@ __global__ __launch_bounds__(64 * kWaves) void paged_attention_kernel(AttentionA
             for (int j = 0; j < V::VE; ++j) o[mt][s][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // Row of the pools that holds the lane's key of a tile; keys outside [lo, hi) take the nearest
-    // one inside, which is read instead and masked.
     const int32_t *table = a.page_table + static_cast<int64_t>(part.n) * a.max_pages;
-    auto pool_row = [&](int tile) {
-        int j = tile + lane % KT;
-        j = j < hi ? j : hi - 1;
-        j = j > lo ? j : lo;
+    const T *const kp = static_cast<const T *>(a.k_pages), *const vp = static_cast<const T *>(a.v_pages);
+    // the row of the pools that holds place j of the sequence
+    auto pool_row = [&](int j) {
         const int pg = static_cast<int>((static_cast<uint64_t>(j) * a.page_mul) >> a.page_shift);
         int id = table[pg];
         id = id < a.num_pages ? id : a.num_pages - 1;
@@ -289,98 +293,177 @@ __global__ __launch_bounds__(64 * kWaves) void paged_attention_kernel(AttentionA
         return static_cast<uint32_t>((id * a.h_k + h) * a.page_size + (j - pg * a.page_size));
     };
     const float to2 = a.scale * kLog2e;
-    for (int tile = lo < hi ? lo / KT * KT + wave * KT : hi; tile < hi; tile += kWaves * KT) {
-        const uint32_t row = pool_row(tile);
-        typename Op::Frag k[ST][QF];
+    Frag k[ST][QF];
+    V v;
+    f32x4 s[MT][ST];
+    typename V::Weights pb[MT];
+
+    auto products = [&]() {
 #pragma unroll
-        for (int t = 0; t < ST; ++t) {
-            const T *p = static_cast<const T *>(a.k_pages) + static_cast<int64_t>(__shfl(row, t * 16 + li)) * D;
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int f = 0; f < QF; ++f)
-                k[t][f] = *reinterpret_cast<const typename Op::Frag *>(p + f * Op::QW + lg * LV);
-        }
-        V v;
+            for (int t = 0; t < ST; ++t) s[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < V::VR; ++r)
-            v.load(r, static_cast<const T *>(a.v_pages) + static_cast<int64_t>(__shfl(row, V::key(lg, r))) * D, li);
-        const bool all = tile >= lo && tile + KT <= hi && tile >= lo_all && tile + KT <= hi_all;
-        typename Op::Weights pb[MT];
+        for (int f = 0; f < QF; ++f)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            f32x4 s[ST];
-            float top = -INFINITY;
+            for (int mt = 0; mt < MT; ++mt) {
+                const Frag q = s_q[(mt * QF + f) * 64 + lane];
 #pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int f = 0; f < QF; ++f) s[t] = Op::qk(k[t][f], q[mt][f], s[t]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[t][i] *= to2;
+                for (int t = 0; t < ST; ++t) s[mt][t] = Op::qk(k[t][f], q, s[mt][t]);
             }
-            if (!all) {
-                const int first = max(lo, first_of(row_t[mt])), end = min(hi, end_of(row_t[mt]));
+    };
+    auto softmax = [&](int mt) {
+        float top = -INFINITY;
 #pragma unroll
-                for (int t = 0; t < ST; ++t)
+        for (int t = 0; t < ST; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = tile + t * 16 + 4 * lg + i;
-                        s[t][i] = j >= first && j < end ? s[t][i] : -INFINITY;
-                    }
-            }
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[mt][t][i]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        top = fmaxf(top, m[mt]);
+        const float at = top == -INFINITY ? 0.f : top;      // nothing seen so far: all weights 0
+        const float keep = __builtin_amdgcn_exp2f(m[mt] - at);
+        m[mt] = top;
 #pragma unroll
-            for (int t = 0; t < ST; ++t)
+        for (int t = 0; t < ST; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            top = fmaxf(top, m[mt]);
-            const float at = top == -INFINITY ? 0.f : top;      // nothing seen so far: all weights 0
-            const float keep = __builtin_amdgcn_exp2f(m[mt] - at);
-            m[mt] = top;
+            for (int i = 0; i < 4; ++i) s[mt][t][i] = __builtin_amdgcn_exp2f(s[mt][t][i] - at);
+        l[mt] *= keep;
 #pragma unroll
-            for (int t = 0; t < ST; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[t][i] = __builtin_amdgcn_exp2f(s[t][i] - at);
-            l[mt] *= keep;
-#pragma unroll
-            for (int t = 0; t < ST; ++t) l[mt] += (s[t].x + s[t].y) + (s[t].z + s[t].w);
-            pb[mt] = operand(s);
+        for (int t = 0; t < ST; ++t) l[mt] += (s[mt][t].x + s[mt][t].y) + (s[mt][t].z + s[mt][t].w);
+        pb[mt] = operand(s[mt], T{});
+        if (!__all(keep == 1.f))
 #pragma unroll
             for (int c = 0; c < V::S; ++c)
 #pragma unroll
                 for (int j = 0; j < V::VE; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[mt][c][j][i] *= keep;
+    };
+    auto add_values = [&]() {
+#pragma unroll
+        for (int c = 0; c < V::S; ++c)
+#pragma unroll
+            for (int j = 0; j < V::VE; ++j)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) o[mt][c][j] = v.pv(c, j, pb[mt], o[mt][c][j]);
+    };
+
+    // A tile whose keys every row sees, in pages of whole sixteens: each 16 keys lie in one page, so
+    // their rows are the same for all lanes but for a fixed offset.
+    const int k_at = li * D + lg * LV, v_at = 4 * lg * D + li * V::VE;
+    uint32_t row[ST];
+    auto find_rows = [&](int tile, uint32_t (&to)[ST]) {
+#pragma unroll
+        for (int t = 0; t < ST; ++t) to[t] = __builtin_amdgcn_readfirstlane(pool_row(tile + 16 * t));
+    };
+    auto load_keys = [&]() {
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+            const T *p = kp + static_cast<int64_t>(row[t]) * D;
+#pragma unroll
+            for (int f = 0; f < QF; ++f) k[t][f] = *reinterpret_cast<const Frag *>(p + k_at + f * Op::QW);
+        }
+    };
+    auto load_values = [&]() {
+#pragma unroll
+        for (int r = 0; r < V::VR; ++r)
+            v.load(r, vp + static_cast<int64_t>(row[r / 4]) * D + v_at + r % 4 * D, 0);
+    };
+    // Any other tile. Keys outside [lo, hi) take the nearest one inside, which is read instead and masked.
+    auto edge = [&](int tile) {
+        int at = tile + lane % KT;
+        at = at < hi ? at : hi - 1;
+        at = at > lo ? at : lo;
+        const uint32_t mine = pool_row(at);
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+            const T *p = kp + static_cast<int64_t>(__shfl(mine, t * 16 + li)) * D + lg * LV;
+#pragma unroll
+            for (int f = 0; f < QF; ++f) k[t][f] = *reinterpret_cast<const Frag *>(p + f * Op::QW);
+        }
+#pragma unroll
+        for (int r = 0; r < V::VR; ++r) v.load(r, vp + static_cast<int64_t>(__shfl(mine, V::key(lg, r))) * D, li);
+        products();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int first = max(lo, first_of(row_t[mt])), end = min(hi, end_of(row_t[mt]));
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = tile + t * 16 + 4 * lg + i;
+                    s[mt][t][i] = j >= first && j < end ? s[mt][t][i] * to2 : -INFINITY;
+                }
+            softmax(mt);
         }
         // Where rows see different keys of a tile, a weight of zero would still take in a value that
-        // is not finite (0 * NaN): token by token then, with the values it does not see at zero.
-        if (all || __all(v.finite())) {
+        // is not finite (0 * NaN): token by token then, without the values it does not see.
+        const bool once = t0 == t1 || __all(v.finite());
+        for (int t = once ? t1 : t0; t <= t1; ++t) {
+            const int first = max(lo, first_of(t)), end = min(hi, end_of(t));
+            typename V::Oper bits;
+#pragma unroll
+            for (int r = 0; r < V::VR; ++r) {
+                const int j = tile + V::key(lg, r);
+                V::see(r, once || (j >= first && j < end), bits);
+            }
 #pragma unroll
             for (int c = 0; c < V::S; ++c)
 #pragma unroll
-                for (int j = 0; j < V::VE; ++j)
+                for (int j = 0; j < V::VE; ++j) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) o[mt][c][j] = v.pv(c, j, pb[mt], o[mt][c][j]);
-        } else {
-            for (int t = t0; t <= t1; ++t) {
-                const int first = max(lo, first_of(t)), end = min(hi, end_of(t));
-                V seen = v;
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const f32x4 x = v.pv(c, j, pb[mt], o[mt][c][j], &bits);
 #pragma unroll
-                for (int r = 0; r < V::VR; ++r) {
-                    const int j = tile + V::key(lg, r);
-                    if (j < first || j >= end) seen.clear(r);
+                        for (int i = 0; i < 4; ++i)
+                            o[mt][c][j][i] = once || row_t[mt] == t ? x[i] : o[mt][c][j][i];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);      // one product's registers at a time
                 }
-#pragma unroll
-                for (int c = 0; c < V::S; ++c)
-#pragma unroll
-                    for (int j = 0; j < V::VE; ++j)
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            const f32x4 x = seen.pv(c, j, pb[mt], o[mt][c][j]);
-                            if (row_t[mt] == t) o[mt][c][j] = x;
-                        }
-            }
         }
+    };
+
+    constexpr int NEXT = kWaves * KT;
+    const int full_lo = max(lo, lo_all), full_hi = min(hi, hi_all);
+    const bool whole_pages = a.page_size % 16 == 0;
+    int tile = lo < hi ? lo / KT * KT + wave * KT : hi;
+    while (tile < hi) {
+        if (!whole_pages || tile < full_lo || tile + KT > full_hi) {
+            edge(tile);
+            tile += NEXT;
+            continue;
+        }
+        // The next tile's keys are under way while this one's weights and values are worked on, its
+        // values while its products are. (The last tile loads its own keys again instead: a load that
+        // is not always made would have to be waited for at once.)
+        find_rows(tile, row);
+        load_keys();
+        bool more;
+        do {
+            more = tile + NEXT + KT <= full_hi;
+            uint32_t ahead[ST];
+            find_rows(more ? tile + NEXT : tile, ahead);
+            load_values();
+            __builtin_amdgcn_sched_barrier(0);
+            products();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < ST; ++t) row[t] = ahead[t];
+            load_keys();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int t = 0; t < ST; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[mt][t][i] *= to2;
+                softmax(mt);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            add_values();
+            tile += NEXT;
+        } while (more);
     }
 
     // the waves' rows join: every wave scales its sums to the common maximum, then 2 + 2 and 1 + 1
@@ -414,25 +497,22 @@ __global__ __launch_bounds__(64 * kWaves) void paged_attention_kernel(AttentionA
         l[mt] = sum;
     }
 #pragma unroll
-    for (int half = kWaves / 2; half > 0; half >>= 1) {
-        if (wave >= half && wave < 2 * half)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int c = 0; c < V::S; ++c)
-#pragma unroll
-                    for (int j = 0; j < V::VE; ++j)
-                        s_o[wave - half][((mt * V::S + c) * V::VE + j) * 64 + lane] = o[mt][c][j];
-        __syncthreads();
-        if (wave < half)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+        for (int half = kWaves / 2; half > 0; half >>= 1) {
+            if (wave >= half && wave < 2 * half)
 #pragma unroll
                 for (int c = 0; c < V::S; ++c)
 #pragma unroll
-                    for (int j = 0; j < V::VE; ++j) o[mt][c][j] += s_o[wave][((mt * V::S + c) * V::VE + j) * 64 + lane];
-        __syncthreads();
-    }
+                    for (int j = 0; j < V::VE; ++j) s_o[wave - half][(c * V::VE + j) * 64 + lane] = o[mt][c][j];
+            __syncthreads();
+            if (wave < half)
+#pragma unroll
+                for (int c = 0; c < V::S; ++c)
+#pragma unroll
+                    for (int j = 0; j < V::VE; ++j) o[mt][c][j] += s_o[wave][(c * V::VE + j) * 64 + lane];
+            __syncthreads();
+        }
     if (wave != 0) return;
 
     // value j of row i of set c's product j is value (16 c + 4 lg + i) VE + j of the head
@@ -479,7 +559,7 @@ __global__ __launch_bounds__(64 * kWaves) void paged_attention_kernel(AttentionA
 // threads that take every JW-th part.
 template <typename T, int D, int MT>
 __global__ __launch_bounds__(256) void paged_attention_join_kernel(AttentionArgs a, int row_blocks) {
-    constexpr int KT = Ops<T>::KT, ROWS = 16 * MT, LANES = D / 4, JW = 256 / LANES;
+    constexpr int KT = tile_keys<T>(D), ROWS = 16 * MT, LANES = D / 4, JW = 256 / LANES;
     __shared__ f32x4 s_o[JW][LANES];
     __shared__ float s_l[JW];
     const int G = a.h_q / a.h_k, heads = a.h_k * row_blocks;
@@ -559,7 +639,7 @@ hipError_t launch_dims(const AttentionArgs &a, const AttentionPlan &p, hipStream
 static int row_tiles(int64_t rows) { return rows <= 16 ? 1 : 2; }
 static int64_t row_blocks(int64_t rows) { return (rows + 16 * row_tiles(rows) - 1) / (16 * row_tiles(rows)); }
 static bool may_split(const gdn2_attention_dims &d) {
-    const int step = kWaves * tile_keys(d.dtype == GDN2_BF16);
+    const int step = kWaves * (d.dtype == GDN2_BF16 ? tile_keys<bf16_t>(d.d) : tile_keys<float>(d.d));
     return static_cast<int64_t>(d.max_pages) * d.page_size > kLeastSteps * step;
 }
 
