@@ -23,24 +23,31 @@ namespace gdn2 {
 
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;           // of a workgroup: as many as an output tile has rows in a lane
 
-// Workgroups that a call is cut into, about, and steps (a tile per wave) below which a part is not cut.
-constexpr int kTargetGroups = 1024;
-constexpr int kLeastSteps = 4;
+// Steps (a tile per wave) of a call that is never cut, and of the shortest part that a sequence is cut
+// into.
+constexpr int kWholeSteps = 4;
+constexpr int kLeastSteps = 1;
 
-__device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
+// Inclusive sum over the lanes of a wave, by the rows of 16 that DPP shifts in and across them.
+__device__ __forceinline__ int lane_sums(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);     // row_shr 1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);    // lane 15 to row 1, 47 to row 3
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);    // lane 31 to rows 2 and 3
     return x;
 }
+__device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, 63); }
 
 __device__ __forceinline__ int seq_len(const AttentionArgs &a, int n) {
     const int most = a.max_pages * a.page_size, len = a.seq_lens[n];
     return len < 0 ? 0 : len > most ? most : len;
 }
 
-// Steps of a workgroup (kWaves tiles) over the places that a sequence's new tokens see.
+// Steps of a workgroup over the places that a sequence's new tokens see.
 template <int KT>
 __device__ __forceinline__ int seq_steps(const AttentionArgs &a, int len) {
     const int64_t first = static_cast<int64_t>(len) - a.new_tokens - a.window + 1;
@@ -48,21 +55,8 @@ __device__ __forceinline__ int seq_steps(const AttentionArgs &a, int len) {
     return (len - lo + kWaves * KT - 1) / (kWaves * KT);
 }
 
-// Steps of a part: all parts together come to at most groups / heads + num_seqs.
-template <int KT>
-__device__ __forceinline__ int part_steps(const AttentionArgs &a, int heads) {
-    const int lane = threadIdx.x & 63;
-    int64_t all = 0;
-    for (int base = 0; base < a.num_seqs; base += 64)
-        if (base + lane < a.num_seqs) all += seq_steps<KT>(a, seq_len(a, base + lane));
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) all += __shfl_xor(all, m);
-    const int64_t per = (all * heads + kTargetGroups - 1) / kTargetGroups;
-    return per > kLeastSteps ? static_cast<int>(per) : kLeastSteps;
-}
-
 __device__ __forceinline__ int num_parts(int steps, int per) {
-    const int n = (steps + per - 1) / per;
+    const int n = static_cast<int>((static_cast<unsigned>(steps) + per - 1) / static_cast<unsigned>(per));
     return n > 1 ? n : 1;
 }
 
@@ -71,29 +65,84 @@ struct Part {
     int n, part, parts, before;
 };
 
-// The sequence that holds part `id`, or n < 0 behind the last.
+// How a call's sequences are cut. Workgroups that run at once, a.budget parts of a sequence with all
+// its heads, end together if no part is longer than another's and none has to wait, so `per`, the
+// steps of a part, is the smallest that gives at most `budget` parts. More sequences than that run
+// in turn, and only those longer than a share of the whole are cut. (64 sequences of 262,144 tokens
+// together, 4 key heads of 128: 108 us with about 1,024 parts for 768 places, [..] with 768 at most.)
 template <int KT>
-__device__ __forceinline__ Part find_part(const AttentionArgs &a, int per, int id) {
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int base = 0; base < a.num_seqs; base += 64) {
-        const int mine = base + lane < a.num_seqs ? num_parts(seq_steps<KT>(a, seq_len(a, base + lane)), per) : 0;
-        int sum = mine;                              // inclusive sum over the lanes
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const int x = __shfl_up(sum, m);
-            if (lane >= m) sum += x;
-        }
-        const uint64_t hit = __ballot(mine > 0 && id < before + sum);
-        if (hit) {
-            const int l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-            const int parts = __shfl(mine, l), first = before + __shfl(sum, l) - parts;
-            return Part{base + l, id - first, parts, first};
-        }
-        before += __shfl(sum, 63);
+struct Cut {
+    int len[4], steps[4];        // of sequences lane, 64 + lane, .. where there are no more than 256
+    int per;
+    const AttentionArgs &a;
+
+    __device__ __forceinline__ int steps_of(int n) const {
+        return n < a.num_seqs ? seq_steps<KT>(a, seq_len(a, n)) : 0;
     }
-    return Part{-1, 0, 0, 0};
-}
+    __device__ __forceinline__ Cut(const AttentionArgs &args) : a(args) {
+        const int lane = threadIdx.x & 63;
+        // (256 sequences of 2^29 keys have at most 2^31 steps)
+        int64_t all = 0;
+        if (a.num_seqs <= 256) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) len[i] = 64 * i + lane < a.num_seqs ? seq_len(a, 64 * i + lane) : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                steps[i] = 64 * i < a.num_seqs ? seq_steps<KT>(a, len[i]) : 0;
+                if (64 * i < a.num_seqs) all += last_lane(lane_sums(steps[i]));
+            }
+        } else {
+            for (int base = 0; base < a.num_seqs; base += 64) all += last_lane(lane_sums(steps_of(base + lane)));
+        }
+        auto share = [&](int among) {
+            const int64_t n = a.num_seqs <= 256 ? (static_cast<uint32_t>(all) + static_cast<uint32_t>(among) - 1) / static_cast<uint32_t>(among)
+                                                : (all + among - 1) / among;
+            return n > kLeastSteps ? static_cast<int>(n) : kLeastSteps;
+        };
+        int low = per = share(a.budget);
+        if (a.budget <= a.num_seqs) return;
+        per = share(a.budget - a.num_seqs);
+        if (a.num_seqs > 256) return;
+        // per always gives few enough parts, low - 1 is too short
+        for (int i = 0; i < 8 && low < per; ++i) {
+            const int mid = (low + per) / 2;
+            int parts = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (64 * j < a.num_seqs) parts += last_lane(lane_sums(64 * j + lane < a.num_seqs ? num_parts(steps[j], mid) : 0));
+            if (parts <= a.budget) per = mid;
+            else low = mid + 1;
+        }
+    }
+    // The sequence that holds part `id`, or n < 0 behind the last.
+    __device__ __forceinline__ Part find(int id) const {
+        const int lane = threadIdx.x & 63;
+        int before = 0;
+        auto look = [&](int base, int mine, Part *at) {
+            const int sum = lane_sums(mine);
+            const uint64_t hit = __ballot(mine > 0 && id < before + sum);
+            if (hit) {
+                const int l = __builtin_ctzll(hit);
+                const int parts = __builtin_amdgcn_readlane(mine, l);
+                const int first = before + __builtin_amdgcn_readlane(sum, l) - parts;
+                *at = Part{base + l, id - first, parts, first};
+                return true;
+            }
+            before += last_lane(sum);
+            return false;
+        };
+        Part at{-1, 0, 0, 0};
+        if (a.num_seqs <= 256) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (64 * i < a.num_seqs && look(64 * i, 64 * i + lane < a.num_seqs ? num_parts(steps[i], per) : 0, &at)) break;
+        } else {
+            for (int base = 0; base < a.num_seqs; base += 64)
+                if (look(base, base + lane < a.num_seqs ? num_parts(steps_of(base + lane), per) : 0, &at)) break;
+        }
+        return at;
+    }
+};
 
 // Weights of keys as B operands of the second product. bf16 holds a weight as the sum of two (8 bits
 // each, 2^-17 of the weight off at most): one alone would put an error of the size of the output's
@@ -120,7 +169,8 @@ template <typename T> constexpr int tile_keys(int d) { return sizeof(T) == 2 && 
 
 // Waves per SIMD that the registers are held to.
 template <typename T, int D, int MT> constexpr int waves_per_simd() {
-    return sizeof(T) == 4 && D == 256 ? 1 : D == 128 && MT == 1 ? 3 : 2;
+    if (D == 64) return sizeof(T) == 2 && MT == 2 ? 3 : 4;
+    return D == 128 ? (MT == 1 ? 3 : 2) : sizeof(T) == 4 ? 1 : 2;
 }
 
 // The first product: QW values of a head per operand of a lane's 16 bytes.
@@ -222,18 +272,31 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
     constexpr int KT = tile_keys<T>(D), ST = KT / 16, QF = D / Op::QW, ROWS = 16 * MT;
     constexpr int LV = 16 / sizeof(T);           // values of a 16-byte access
     typedef typename Op::Frag Frag;
-    __shared__ Frag s_q[MT * QF * 64];
+    // q while the keys are worked on, one tile of rows of the waves' sums after that
+    constexpr int QB = MT * QF * 64 * sizeof(Frag), OB = kWaves * 4 * V::S * V::VE * 64 * sizeof(float);
+    __shared__ __align__(16) char s_mem[QB > OB ? QB : OB];
     __shared__ float s_ml[kWaves][2][ROWS];
-    __shared__ f32x4 s_o[2][V::S * V::VE * 64];
+    Frag *const s_q = reinterpret_cast<Frag *>(s_mem);
+    float *const s_o = reinterpret_cast<float *>(s_mem);
     const int lane = threadIdx.x & 63, lg = lane >> 4, li = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = a.h_k * row_blocks;
     const int sub = static_cast<int>(blockIdx.x % heads), h = sub / row_blocks, rb = sub % row_blocks;
     const int G = a.h_q / a.h_k, R = a.new_tokens * G;
-    const int per = part_steps<KT>(a, heads);
-    const Part part = find_part<KT>(a, per, static_cast<int>(blockIdx.x / heads));
-    if (part.n < 0) return;
-    const int len = seq_len(a, part.n);
+    const int id = static_cast<int>(blockIdx.x / heads);
+    Part part{id, 0, 1, id};
+    if (a.budget > 0) {
+        part = Cut<KT>(a).find(id);
+        if (part.n < 0) return;
+        if (part.part == 0 && sub == 0 && threadIdx.x == 0) {
+            a.part_info[2 * part.n] = part.before;
+            a.part_info[2 * part.n + 1] = part.parts;
+        }
+    }
+    part.n = __builtin_amdgcn_readfirstlane(part.n);
+    part.part = __builtin_amdgcn_readfirstlane(part.part);
+    part.parts = __builtin_amdgcn_readfirstlane(part.parts);
+    const int len = __builtin_amdgcn_readfirstlane(seq_len(a, part.n));
 
     // the places that this workgroup's rows see: row r those of [lo_r, hi_r)
     const int r0 = rb * ROWS, r1 = r0 + ROWS < R ? r0 + ROWS : R;
@@ -254,21 +317,25 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
     // between these, every row sees every key
     const int lo_all = first_of(t1), hi_all = end_of(t0);
 
-    // q as the first product's B operands, in LDS: [MT][QF][64 lanes]
+    // q as the first product's B operands: in LDS as [MT][QF][64 lanes], a share per wave
+    constexpr int QS = (MT * QF + kWaves - 1) / kWaves;
+    Frag q[QS];
     int row_t[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const int r = r0 + mt * 16 + li, rr = r < R ? r : R - 1;
-        row_t[mt] = rr / G;
-        const T *p = static_cast<const T *>(a.q) +
-                     (static_cast<int64_t>(part.n) * a.new_tokens + row_t[mt]) * a.q_stride +
-                     static_cast<int64_t>(h * G + rr % G) * D;
-        for (int f = wave; f < QF; f += kWaves) {
-            const T *at = p + f * Op::QW + lg * LV;
-            s_q[(mt * QF + f) * 64 + lane] = a.q_whole ? *reinterpret_cast<const Frag *>(at) : Op::each(at);
-        }
+        const int r = r0 + mt * 16 + li;
+        row_t[mt] = (r < R ? r : R - 1) / G;
     }
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < QS; ++i) {
+        const int f = wave + i * kWaves, mt = f / QF;
+        if (f >= MT * QF) continue;
+        const int t = MT == 1 || mt == 0 ? row_t[0] : row_t[MT - 1], r = r0 + mt * 16 + li;
+        const T *p = static_cast<const T *>(a.q) +
+                     (static_cast<int64_t>(part.n) * a.new_tokens + t) * a.q_stride +
+                     static_cast<int64_t>(h * G + (r < R ? r : R - 1) - t * G) * D + f % QF * Op::QW + lg * LV;
+        q[i] = a.q_whole ? *reinterpret_cast<const Frag *>(p) : Op::each(p);
+    }
 
     f32x4 o[MT][V::S][V::VE];
     float m[MT], l[MT];                          // l: this lane's keys only
@@ -399,8 +466,9 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
         }
         // Where rows see different keys of a tile, a weight of zero would still take in a value that
         // is not finite (0 * NaN): token by token then, without the values it does not see.
-        const bool once = t0 == t1 || __all(v.finite());
+        int once = t0 == t1 || __all(v.finite());
         for (int t = once ? t1 : t0; t <= t1; ++t) {
+            asm volatile("" : "+v"(once));       // else the loop is built twice, with the sums copied between
             const int first = max(lo, first_of(t)), end = min(hi, end_of(t));
             typename V::Oper bits;
 #pragma unroll
@@ -424,49 +492,51 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
         }
     };
 
+    // This wave's tiles are first, first + NEXT .. below hi; those in [whole, whole_end) are such tiles.
     constexpr int NEXT = kWaves * KT;
+    const int first = lo < hi ? lo / KT * KT + wave * KT : hi;
     const int full_lo = max(lo, lo_all), full_hi = min(hi, hi_all);
-    const bool whole_pages = a.page_size % 16 == 0;
-    int tile = lo < hi ? lo / KT * KT + wave * KT : hi;
-    while (tile < hi) {
-        if (!whole_pages || tile < full_lo || tile + KT > full_hi) {
-            edge(tile);
-            tile += NEXT;
-            continue;
-        }
-        // The next tile's keys are under way while this one's weights and values are worked on, its
-        // values while its products are. (The last tile loads its own keys again instead: a load that
-        // is not always made would have to be waited for at once.)
-        find_rows(tile, row);
+    const int skip = full_lo > first ? (full_lo - first + NEXT - 1) / NEXT * NEXT : 0;
+    const int whole = a.page_size % 16 == 0 && first + skip + KT <= full_hi ? first + skip : hi;
+    const int whole_end = whole < hi ? whole + (full_hi - KT - whole) / NEXT * NEXT + NEXT : hi;
+    if (whole < hi) {
+        find_rows(whole, row);
         load_keys();
-        bool more;
-        do {
-            more = tile + NEXT + KT <= full_hi;
-            uint32_t ahead[ST];
-            find_rows(more ? tile + NEXT : tile, ahead);
-            load_values();
-            __builtin_amdgcn_sched_barrier(0);
-            products();
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int t = 0; t < ST; ++t) row[t] = ahead[t];
-            load_keys();
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int t = 0; t < ST; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[mt][t][i] *= to2;
-                softmax(mt);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            add_values();
-            tile += NEXT;
-        } while (more);
     }
+#pragma unroll
+    for (int i = 0; i < QS; ++i)
+        if (wave + i * kWaves < MT * QF) s_q[(wave + i * kWaves) * 64 + lane] = q[i];
+    __syncthreads();
+    // The next tile's keys are under way while this one's weights and values are worked on, its values
+    // while its products are. (The last tile loads its own keys again instead: a load that is not
+    // always made would have to be waited for at once.)
+    for (int tile = whole; tile < whole_end; tile += NEXT) {
+        uint32_t ahead[ST];
+        find_rows(tile + NEXT < whole_end ? tile + NEXT : tile, ahead);
+        load_values();
+        __builtin_amdgcn_sched_barrier(0);
+        products();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < ST; ++t) row[t] = ahead[t];
+        load_keys();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[mt][t][i] *= to2;
+            softmax(mt);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        add_values();
+    }
+    for (int tile = first == whole ? whole_end : first; tile < hi; tile = tile + NEXT == whole ? whole_end : tile + NEXT)
+        edge(tile);
 
-    // the waves' rows join: every wave scales its sums to the common maximum, then 2 + 2 and 1 + 1
+    // The waves' rows join: every wave scales its sums to the common maximum, then wave i adds row i of
+    // every output tile over the waves, and writes it.
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         l[mt] += __shfl_xor(l[mt], 16);
@@ -476,9 +546,9 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
             s_ml[wave][1][mt * 16 + li] = l[mt];
         }
     }
-    __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+        __syncthreads();                         // the first: all waves have done with q
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_ml[w][0][mt * 16 + li]);
@@ -492,133 +562,111 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
 #pragma unroll
             for (int j = 0; j < V::VE; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[mt][c][j][i] *= keep;
-        m[mt] = top;
-        l[mt] = sum;
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int half = kWaves / 2; half > 0; half >>= 1) {
-            if (wave >= half && wave < 2 * half)
-#pragma unroll
-                for (int c = 0; c < V::S; ++c)
-#pragma unroll
-                    for (int j = 0; j < V::VE; ++j) s_o[wave - half][(c * V::VE + j) * 64 + lane] = o[mt][c][j];
-            __syncthreads();
-            if (wave < half)
-#pragma unroll
-                for (int c = 0; c < V::S; ++c)
-#pragma unroll
-                    for (int j = 0; j < V::VE; ++j) o[mt][c][j] += s_o[wave][(c * V::VE + j) * 64 + lane];
-            __syncthreads();
-        }
-    if (wave != 0) return;
-
-    // value j of row i of set c's product j is value (16 c + 4 lg + i) VE + j of the head
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+                for (int i = 0; i < 4; ++i)
+                    s_o[(((wave * 4 + i) * V::S + c) * V::VE + j) * 64 + lane] = o[mt][c][j][i] * keep;
+        __syncthreads();
         const int r = r0 + mt * 16 + li;
-        if (r >= R) continue;
-        if (part.parts == 1) {
-            const int64_t at = (static_cast<int64_t>(part.n) * a.new_tokens + row_t[mt]) * a.h_q + h * G + r % G;
-            const float inv = l[mt] == 0.f ? 0.f : 1.f / l[mt];
-            T *out = static_cast<T *>(a.o) + at * D;
+        const bool cut = part.parts > 1;
+        const float inv = cut ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        const int64_t part_at = static_cast<int64_t>(blockIdx.x) * ROWS + mt * 16 + li;
+        const int64_t row_at = (static_cast<int64_t>(part.n) * a.new_tokens + row_t[mt]) * a.h_q + h * G + r - row_t[mt] * G;
 #pragma unroll
-            for (int c = 0; c < V::S; ++c)
+        for (int c = 0; c < V::S; ++c) {
+            float x[V::VE];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x[V::VE];
+            for (int j = 0; j < V::VE; ++j) {
+                x[j] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < V::VE; ++j) x[j] = o[mt][c][j][i] * inv;
-                    stv<T, V::VE>(out + (16 * c + 4 * lg + i) * V::VE, x);
-                }
-            if (a.lse && lg == 0)
-                a.lse[at] = l[mt] == 0.f ? -INFINITY : (m[mt] + log2f(l[mt])) * (1.f / kLog2e);
-        } else {
-            const int64_t at = static_cast<int64_t>(blockIdx.x) * ROWS + mt * 16 + li;
-            float *out = a.part_o + at * D;
-#pragma unroll
-            for (int c = 0; c < V::S; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x[V::VE];
-#pragma unroll
-                    for (int j = 0; j < V::VE; ++j) x[j] = o[mt][c][j][i];
-                    stv<float, V::VE>(out + (16 * c + 4 * lg + i) * V::VE, x);
-                }
-            if (lg == 0) {
-                a.part_ml[2 * at] = m[mt];
-                a.part_ml[2 * at + 1] = l[mt];
+                for (int w = 0; w < kWaves; ++w) x[j] += s_o[(((w * 4 + wave) * V::S + c) * V::VE + j) * 64 + lane];
+                x[j] *= inv;
             }
+            // value j of row i of set c's product j is value (16 c + 4 lg + i) VE + j of the head
+            const int to = (16 * c + 4 * lg + wave) * V::VE;
+            if (r >= R) continue;
+            if (cut) stv<float, V::VE>(a.part_o + part_at * D + to, x);
+            else stv<T, V::VE>(static_cast<T *>(a.o) + row_at * D + to, x);
+        }
+        if (r < R && lg == 0 && wave == 0) {
+            if (cut) *reinterpret_cast<float2 *>(a.part_ml + 2 * part_at) = float2{top, sum};
+            else if (a.lse) a.lse[row_at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * (1.f / kLog2e);
         }
     }
 }
 
-// Joins the parts of a sequence: a workgroup per row, its D / 4 lanes per value times JW groups of
-// threads that take every JW-th part.
-template <typename T, int D, int MT>
+// Joins the parts of a sequence: a row has D / 4 lanes per part, and the rest of its THREADS other
+// parts. Many rows take a wave each (256 sequences of one part each, 32 heads: [..] us in place of 15),
+// few a workgroup.
+template <typename T, int D, int MT, int THREADS>
 __global__ __launch_bounds__(256) void paged_attention_join_kernel(AttentionArgs a, int row_blocks) {
-    constexpr int KT = tile_keys<T>(D), ROWS = 16 * MT, LANES = D / 4, JW = 256 / LANES;
-    __shared__ f32x4 s_o[JW][LANES];
-    __shared__ float s_l[JW];
+    constexpr int ROWS = 16 * MT, LANES = D / 4, JW = THREADS / LANES, PER = 256 / THREADS;
+    __shared__ f32x4 s_o[PER][JW][LANES];
+    __shared__ float s_l[PER][JW];
     const int G = a.h_q / a.h_k, heads = a.h_k * row_blocks;
-    const int64_t at = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-    if (at >= static_cast<int64_t>(a.num_seqs) * a.new_tokens * a.h_q) return;
-    const int n = static_cast<int>(at / (static_cast<int64_t>(a.new_tokens) * a.h_q));
-    const int t = static_cast<int>(at / a.h_q % a.new_tokens), hq = static_cast<int>(at % a.h_q);
-    const int per = part_steps<KT>(a, heads);
-    const int parts = num_parts(seq_steps<KT>(a, seq_len(a, n)), per);
-    if (parts == 1) return;                      // written by the first kernel
-    int before = 0;
-    for (int base = 0; base < n; base += 64) {
-        const int i = base + static_cast<int>(threadIdx.x & 63);
-        before += wave_sum(i < n ? num_parts(seq_steps<KT>(a, seq_len(a, i)), per) : 0);
+    const int slot = threadIdx.x / THREADS, thread = threadIdx.x % THREADS;
+    const int64_t at = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * PER + slot;
+    const bool mine = at < static_cast<int64_t>(a.num_seqs) * a.new_tokens * a.h_q;
+    int parts = 1, before = 0, n = 0;
+    if (mine) {
+        n = static_cast<int>(at / (static_cast<int64_t>(a.new_tokens) * a.h_q));
+        before = a.part_info[2 * n];
+        parts = a.part_info[2 * n + 1];
     }
-    const int h = hq / G, r = t * G + hq % G;
-    const int64_t step = static_cast<int64_t>(heads) * ROWS;
-    const int64_t first = (static_cast<int64_t>(before) * heads + h * row_blocks + r / ROWS) * ROWS + r % ROWS;
-    float top = -INFINITY;
-    for (int p = threadIdx.x & 63; p < parts; p += 64) top = fmaxf(top, a.part_ml[2 * (first + p * step)]);
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-    const float ref = top == -INFINITY ? 0.f : top;
-    const int c = threadIdx.x % LANES, g = threadIdx.x / LANES;
+    const bool cut = parts > 1;                  // whole sequences are written by the first kernel
+    const int c = thread % LANES, g = thread / LANES;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
+    float l = 0.f, top = -INFINITY;
+    if (cut) {
+        const int t = static_cast<int>(at / a.h_q % a.new_tokens), hq = static_cast<int>(at % a.h_q);
+        const int h = hq / G, r = t * G + hq % G;
+        const int64_t step = static_cast<int64_t>(heads) * ROWS;
+        const int64_t first = (static_cast<int64_t>(before) * heads + h * row_blocks + r / ROWS) * ROWS + r % ROWS;
+        for (int p = threadIdx.x & 63; p < parts; p += 64) top = fmaxf(top, a.part_ml[2 * (first + p * step)]);
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+        const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
-    for (int p = g; p < parts; p += JW) {
-        const int64_t i = first + p * step;
-        const float w = __builtin_amdgcn_exp2f(a.part_ml[2 * i] - ref);
-        l = fmaf(w, a.part_ml[2 * i + 1], l);
-        const f32x4 x = *reinterpret_cast<const f32x4 *>(a.part_o + i * D + 4 * c);
+        for (int p = g; p < parts; p += JW) {
+            const int64_t i = first + p * step;
+            const float w = __builtin_amdgcn_exp2f(a.part_ml[2 * i] - ref);
+            l = fmaf(w, a.part_ml[2 * i + 1], l);
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(a.part_o + i * D + 4 * c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = fmaf(w, x[e], o[e]);
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(w, x[e], o[e]);
+        }
     }
-    s_o[g][c] = o;
-    if (c == 0) s_l[g] = l;
-    __syncthreads();
-    if (g != 0) return;
+    if constexpr (JW > 1) {
+        s_o[slot][g][c] = o;
+        if (c == 0) s_l[slot][g] = l;
+        __syncthreads();
+        if (g != 0) return;
 #pragma unroll
-    for (int x = 1; x < JW; ++x) {
-        o += s_o[x][c];
-        l += s_l[x];
+        for (int x = 1; x < JW; ++x) {
+            o += s_o[slot][x][c];
+            l += s_l[slot][x];
+        }
     }
+    if (!cut) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     io<T>::st4(static_cast<T *>(a.o) + at * D + 4 * c, o * inv);
     if (a.lse && c == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * (1.f / kLog2e);
 }
 
+constexpr int kJoinRows = 2048;      // most rows that take a workgroup each
+
 template <typename T, int D, int MT>
 hipError_t launch(const AttentionArgs &a, const AttentionPlan &p, hipStream_t st) {
-    const unsigned groups = static_cast<unsigned>(p.max_parts) * static_cast<unsigned>(a.h_k * p.row_blocks);
-    hipLaunchKernelGGL((paged_attention_kernel<T, D, MT>), dim3(groups), dim3(64 * kWaves), 0, st, a, p.row_blocks);
+    const unsigned groups = static_cast<unsigned>(p.max_parts * p.row_blocks * a.h_k);
+    hipLaunchKernelGGL((paged_attention_kernel<T, D, MT>), dim3(groups), dim3(64 * kWaves), 0, st, a, static_cast<int>(p.row_blocks));
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.split) return e;
+    if (e != hipSuccess || p.budget == 0) return e;
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.new_tokens * a.h_q;
-    const unsigned gx = static_cast<unsigned>(rows < (1 << 20) ? rows : (1 << 20));
-    hipLaunchKernelGGL((paged_attention_join_kernel<T, D, MT>), dim3(gx, static_cast<unsigned>((rows + gx - 1) / gx)),
-                       dim3(256), 0, st, a, p.row_blocks);
+    const int64_t blocks = rows <= kJoinRows ? rows : (rows + 3) / 4;
+    const unsigned gx = static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20));
+    const dim3 grid(gx, static_cast<unsigned>((blocks + gx - 1) / gx));
+    if (rows <= kJoinRows)
+        hipLaunchKernelGGL((paged_attention_join_kernel<T, D, MT, 256>), grid, dim3(256), 0, st, a, static_cast<int>(p.row_blocks));
+    else
+        hipLaunchKernelGGL((paged_attention_join_kernel<T, D, MT, 64>), grid, dim3(256), 0, st, a, static_cast<int>(p.row_blocks));
     return hipGetLastError();
 }
 
@@ -638,23 +686,29 @@ hipError_t launch_dims(const AttentionArgs &a, const AttentionPlan &p, hipStream
 // Tiles of 16 rows per workgroup, and blocks of them, for a key head's rows.
 static int row_tiles(int64_t rows) { return rows <= 16 ? 1 : 2; }
 static int64_t row_blocks(int64_t rows) { return (rows + 16 * row_tiles(rows) - 1) / (16 * row_tiles(rows)); }
-static bool may_split(const gdn2_attention_dims &d) {
-    const int step = kWaves * (d.dtype == GDN2_BF16 ? tile_keys<bf16_t>(d.d) : tile_keys<float>(d.d));
-    return static_cast<int64_t>(d.max_pages) * d.page_size > kLeastSteps * step;
+static int step_keys(const gdn2_attention_dims &d) {
+    return kWaves * (d.dtype == GDN2_BF16 ? tile_keys<bf16_t>(d.d) : tile_keys<float>(d.d));
 }
-
-int64_t attention_groups(const gdn2_attention_dims &d) {
-    const int64_t heads = d.h_k * row_blocks(static_cast<int64_t>(d.new_tokens) * (d.h_q / d.h_k));
-    return (d.num_seqs + (may_split(d) ? kTargetGroups / heads : 0)) * heads;
+// Workgroups that the chip holds at once.
+static int places(const gdn2_attention_dims &d, int tiles) {
+    auto of = [&](auto type) {
+        using T = decltype(type);
+        return d.d == 64 ? (tiles == 1 ? waves_per_simd<T, 64, 1>() : waves_per_simd<T, 64, 2>())
+             : d.d == 128 ? (tiles == 1 ? waves_per_simd<T, 128, 1>() : waves_per_simd<T, 128, 2>())
+                          : (tiles == 1 ? waves_per_simd<T, 256, 1>() : waves_per_simd<T, 256, 2>());
+    };
+    return kSimds / 4 * (d.dtype == GDN2_BF16 ? of(bf16_t{}) : of(float{}));
 }
 
 AttentionPlan attention_plan(const gdn2_attention_dims &d) {
     const int64_t rows = static_cast<int64_t>(d.new_tokens) * (d.h_q / d.h_k);
     AttentionPlan p;
     p.row_tiles = row_tiles(rows);
-    p.row_blocks = static_cast<int>(row_blocks(rows));
-    p.split = may_split(d);
-    p.max_parts = static_cast<int>(attention_groups(d) / (static_cast<int64_t>(d.h_k) * p.row_blocks));
+    p.row_blocks = row_blocks(rows);
+    const int64_t heads = d.h_k * p.row_blocks, keys = static_cast<int64_t>(d.max_pages) * d.page_size;
+    p.budget = keys > static_cast<int64_t>(kWholeSteps) * step_keys(d) ? places(d, p.row_tiles) / heads : 0;
+    if (p.budget == 1 && d.num_seqs >= 1) p.budget = 0;      // every sequence whole
+    p.max_parts = p.budget > d.num_seqs ? p.budget : d.num_seqs + p.budget;
     return p;
 }
 

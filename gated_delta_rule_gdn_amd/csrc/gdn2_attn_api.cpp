@@ -87,8 +87,8 @@ gdn2_status check_attention(const gdn2_attention_dims *d) {
     // (the first quotient keeps the product inside 64 bits)
     if (d->num_pages > kMaxPlaces / d->page_size || static_cast<int64_t>(d->num_pages) * d->page_size > kMaxPlaces / d->h_k)
         return report(GDN2_ERR_BAD_SHAPE, "num_pages * h_k * page_size must be at most 2^31 - 1");
-    if (static_cast<int64_t>(d->max_pages) * d->page_size > (int64_t{1} << 30))
-        return report(GDN2_ERR_BAD_SHAPE, "max_pages * page_size must be at most 2^30");
+    if (static_cast<int64_t>(d->max_pages) * d->page_size > (int64_t{1} << 29))
+        return report(GDN2_ERR_BAD_SHAPE, "max_pages * page_size must be at most 2^29");
     if (static_cast<int64_t>(d->num_seqs) * d->max_pages > kMaxElems)
         return report(GDN2_ERR_BAD_SHAPE, "page_table is too large");
     if (d->window < 0) return report(GDN2_ERR_BAD_SHAPE, "window must be >= 0");
@@ -96,22 +96,25 @@ gdn2_status check_attention(const gdn2_attention_dims *d) {
     int64_t s;
     if (!take_stride(d->q_stride, static_cast<int64_t>(d->h_q) * d->d, tokens, &s))
         return report(GDN2_ERR_BAD_SHAPE, "q_stride is smaller than a token's heads or q too large");
-    if (gdn2::attention_groups(*d) > (int64_t{1} << 23))
+    const gdn2::AttentionPlan p = gdn2::attention_plan(*d);
+    if (p.max_parts > (int64_t{1} << 23) || p.max_parts * d->h_k * p.row_blocks > (int64_t{1} << 23))
         return report(GDN2_ERR_BAD_SHAPE, "more than 2^23 workgroups: too many sequences, heads or new tokens");
     return GDN2_OK;
 }
 
 bool al16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// Sizes of the workspace: the parts' sums, their maxima and totals, and the sequences' numbers of them.
 struct AttentionBytes {
-    size_t o = 0, ml = 0;
+    size_t o = 0, ml = 0, info = 0;
     AttentionBytes(const gdn2_attention_dims *d, const gdn2::AttentionPlan &p) {
-        if (!p.split) return;
-        const size_t rows = static_cast<size_t>(p.max_parts) * d->h_k * p.row_blocks * p.row_tiles * 16;
+        if (p.budget == 0) return;
+        const size_t rows = static_cast<size_t>(p.max_parts * d->h_k * p.row_blocks) * p.row_tiles * 16;
         o = padded(rows * d->d * sizeof(float));
         ml = padded(rows * 2 * sizeof(float));
+        info = padded(static_cast<size_t>(d->num_seqs) * 2 * sizeof(int32_t));
     }
-    size_t total() const { return o + ml; }
+    size_t total() const { return o + ml + info; }
 };
 
 }  // namespace
@@ -228,9 +231,12 @@ gdn2_status gdn2_paged_attention_step(const void *q, const void *k_pages, const 
     gdn2::AttentionArgs a;
     a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.page_table = page_table; a.seq_lens = seq_lens;
     a.o = o; a.lse = lse;
-    if (p.split) {
-        a.part_o = static_cast<float *>(workspace);
-        a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + bytes.o);
+    a.budget = static_cast<int>(p.budget);
+    if (a.budget > 0) {
+        char *w = static_cast<char *>(workspace);
+        a.part_o = reinterpret_cast<float *>(w);
+        a.part_ml = reinterpret_cast<float *>(w + bytes.o);
+        a.part_info = reinterpret_cast<int32_t *>(w + bytes.o + bytes.ml);
     }
     a.num_seqs = dims->num_seqs; a.new_tokens = dims->new_tokens; a.h_q = dims->h_q; a.h_k = dims->h_k;
     a.d = dims->d; a.num_pages = dims->num_pages; a.page_size = dims->page_size;

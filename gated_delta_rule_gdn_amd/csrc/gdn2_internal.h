@@ -255,6 +255,8 @@ struct AttentionArgs {
     float *lse;
     float *part_o = nullptr;         // [workgroups][rows of a workgroup][d]: sums of a part of a sequence
     float *part_ml = nullptr;        // [workgroups][rows of a workgroup][2]: their maxima and totals
+    int32_t *part_info = nullptr;    // [num_seqs][2]: a sequence's first part, and its number of parts
+    int budget = 0;                  // of the plan
     int64_t q_stride;
     int num_seqs, new_tokens, h_q, h_k, d, num_pages, page_size, max_pages, window;
     uint32_t page_mul;               // x / page_size = x * page_mul >> page_shift for x < 2^31
@@ -265,11 +267,10 @@ struct AttentionArgs {
 };
 struct AttentionPlan {
     int row_tiles;                   // tiles of 16 rows that a workgroup takes
-    int row_blocks;                  // workgroups that share a (sequence, key head)'s rows
-    int max_parts;                   // most parts that all sequences together are cut into
-    bool split;                      // some sequence may be cut
+    int64_t row_blocks;              // workgroups that share a (sequence, key head)'s rows
+    int64_t budget;                  // parts of sequences that run at once; 0: no sequence is cut
+    int64_t max_parts;               // most parts that all sequences together are cut into
 };
-int64_t attention_groups(const gdn2_attention_dims &d);      // workgroups of a call
 AttentionPlan attention_plan(const gdn2_attention_dims &d);
 hipError_t launch_attention(const AttentionArgs &a, const AttentionPlan &p, hipStream_t st);
 

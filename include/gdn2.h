@@ -772,7 +772,7 @@ typedef struct gdn2_attention_dims {
     int32_t h_q, h_k;                  /* h_q a multiple of h_k */
     int32_t d;                         /* 64, 128 or 256 */
     int32_t num_pages, page_size;      /* num_pages * h_k * page_size <= 2^31 - 1 */
-    int32_t max_pages;                 /* columns of page_table; max_pages * page_size <= 2^30 */
+    int32_t max_pages;                 /* columns of page_table; max_pages * page_size <= 2^29 */
     int32_t window;                    /* a query sees this many keys at most, its own among them;
                                           0: all before it */
     int32_t dtype;                     /* gdn2_dtype of q, the pages and o */
