@@ -55,10 +55,19 @@ __device__ __forceinline__ int seq_steps(const AttentionArgs &a, int len) {
     return (len - lo + kWaves * KT - 1) / (kWaves * KT);
 }
 
-__device__ __forceinline__ int num_parts(int steps, int per) {
-    const int n = static_cast<int>((static_cast<unsigned>(steps) + per - 1) / static_cast<unsigned>(per));
-    return n > 1 ? n : 1;
-}
+// Parts of at most `per` steps, about: the quotient is taken with a reciprocal that is held too small
+// (by 2^-21, where its errors and the product's come to 2^-22), so that there is never a part more
+// than steps / per rounded up.
+struct Parts {
+    float inv;
+    int less;
+    __device__ __forceinline__ explicit Parts(int per)
+        : inv(__builtin_amdgcn_rcpf(static_cast<float>(per)) * (1.f - 0x1p-21f)), less(per - 1) {}
+    __device__ __forceinline__ int of(int steps) const {
+        const int n = static_cast<int>(static_cast<float>(static_cast<uint32_t>(steps) + less) * inv);
+        return n > 1 ? n : 1;
+    }
+};
 
 // A part of a sequence: number `part` of `parts`, of which `before` belong to earlier sequences.
 struct Part {
@@ -66,83 +75,66 @@ struct Part {
 };
 
 // How a call's sequences are cut. Workgroups that run at once, a.budget parts of a sequence with all
-// its heads, end together if no part is longer than another's and none has to wait, so `per`, the
-// steps of a part, is the smallest that gives at most `budget` parts. More sequences than that run
+// its heads, end together if no part is longer than another's and none has to wait, so the steps of a
+// part are the fewest that give at most `budget` parts, or near them. More sequences than that run
 // in turn, and only those longer than a share of the whole are cut. (64 sequences of 262,144 tokens
-// together, 4 key heads of 128: 108 us with about 1,024 parts for 768 places, [..] with 768 at most.)
+// together, 4 key heads of 128: 103 us with at most 768 parts for 768 places, 106 with about 1,024.)
+// Every workgroup works this out by itself, in loops: what is not repeated has its code fetched
+// first, which takes longer than running it (four tries side by side: 0.6 us more than in turn).
 template <int KT>
-struct Cut {
-    int len[4], steps[4];        // of sequences lane, 64 + lane, .. where there are no more than 256
-    int per;
-    const AttentionArgs &a;
-
-    __device__ __forceinline__ int steps_of(int n) const {
-        return n < a.num_seqs ? seq_steps<KT>(a, seq_len(a, n)) : 0;
-    }
-    __device__ __forceinline__ Cut(const AttentionArgs &args) : a(args) {
-        const int lane = threadIdx.x & 63;
-        // (256 sequences of 2^29 keys have at most 2^31 steps)
-        int64_t all = 0;
-        if (a.num_seqs <= 256) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) len[i] = 64 * i + lane < a.num_seqs ? seq_len(a, 64 * i + lane) : 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                steps[i] = 64 * i < a.num_seqs ? seq_steps<KT>(a, len[i]) : 0;
-                if (64 * i < a.num_seqs) all += last_lane(lane_sums(steps[i]));
-            }
+__device__ __forceinline__ Part find_part(const AttentionArgs &a, int id) {
+    const int lane = threadIdx.x & 63;
+    auto steps_of = [&](int n) { return n < a.num_seqs ? seq_steps<KT>(a, seq_len(a, n)) : 0; };
+    const int mine = steps_of(lane);
+    const float shares = static_cast<float>(a.budget - a.num_seqs);
+    int low = 0, per = 0, next = 0;
+#pragma unroll 1
+    for (int tries = 0; tries < 5; ++tries) {
+        // first all steps, then the parts that `next` steps give
+        const Parts p(next);
+        int64_t sum = 0;
+#pragma unroll 1
+        for (int base = 0; base < a.num_seqs; base += 64) {
+            const int steps = base == 0 ? mine : steps_of(base + lane);
+            sum += last_lane(lane_sums(next == 0 ? steps : base + lane < a.num_seqs ? p.of(steps) : 0));
+        }
+        if (next == 0) {
+            // Steps per part that are enough in any case: all / (budget - num_seqs), rounded up. In
+            // fp32, held too large by 2^-20 and one.
+            const float all = static_cast<float>(sum);
+            auto share = [&](float among) {
+                const float x = all * __builtin_amdgcn_rcpf(among);
+                return x < 0x1p24f ? static_cast<int>(x * (1.f + 0x1p-20f)) : 1 << 24;
+            };
+            low = share(static_cast<float>(a.budget));
+            low = low > kLeastSteps ? low : kLeastSteps;
+            per = shares > 0.f ? share(shares) + 1 : low + 1;
+            if (shares <= 0.f || a.num_seqs > 256) break;
+        } else if (sum <= a.budget) {
+            per = next;
         } else {
-            for (int base = 0; base < a.num_seqs; base += 64) all += last_lane(lane_sums(steps_of(base + lane)));
+            low = next + 1;
         }
-        auto share = [&](int among) {
-            const int64_t n = a.num_seqs <= 256 ? (static_cast<uint32_t>(all) + static_cast<uint32_t>(among) - 1) / static_cast<uint32_t>(among)
-                                                : (all + among - 1) / among;
-            return n > kLeastSteps ? static_cast<int>(n) : kLeastSteps;
-        };
-        int low = per = share(a.budget);
-        if (a.budget <= a.num_seqs) return;
-        per = share(a.budget - a.num_seqs);
-        if (a.num_seqs > 256) return;
-        // per always gives few enough parts, low - 1 is too short
-        for (int i = 0; i < 8 && low < per; ++i) {
-            const int mid = (low + per) / 2;
-            int parts = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (64 * j < a.num_seqs) parts += last_lane(lane_sums(64 * j + lane < a.num_seqs ? num_parts(steps[j], mid) : 0));
-            if (parts <= a.budget) per = mid;
-            else low = mid + 1;
-        }
+        if (low >= per) break;
+        next = (low + per) / 2;
     }
-    // The sequence that holds part `id`, or n < 0 behind the last.
-    __device__ __forceinline__ Part find(int id) const {
-        const int lane = threadIdx.x & 63;
-        int before = 0;
-        auto look = [&](int base, int mine, Part *at) {
-            const int sum = lane_sums(mine);
-            const uint64_t hit = __ballot(mine > 0 && id < before + sum);
-            if (hit) {
-                const int l = __builtin_ctzll(hit);
-                const int parts = __builtin_amdgcn_readlane(mine, l);
-                const int first = before + __builtin_amdgcn_readlane(sum, l) - parts;
-                *at = Part{base + l, id - first, parts, first};
-                return true;
-            }
-            before += last_lane(sum);
-            return false;
-        };
-        Part at{-1, 0, 0, 0};
-        if (a.num_seqs <= 256) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (64 * i < a.num_seqs && look(64 * i, 64 * i + lane < a.num_seqs ? num_parts(steps[i], per) : 0, &at)) break;
-        } else {
-            for (int base = 0; base < a.num_seqs; base += 64)
-                if (look(base, base + lane < a.num_seqs ? num_parts(steps_of(base + lane), per) : 0, &at)) break;
+    const Parts p(per);
+    int before = 0;
+#pragma unroll 1
+    for (int base = 0; base < a.num_seqs; base += 64) {
+        const int steps = base == 0 ? mine : steps_of(base + lane);
+        const int parts = base + lane < a.num_seqs ? p.of(steps) : 0;
+        const int sum = lane_sums(parts);
+        const uint64_t hit = __ballot(parts > 0 && id < before + sum);
+        if (hit) {
+            const int l = __builtin_ctzll(hit), n = __builtin_amdgcn_readlane(parts, l);
+            const int first = before + __builtin_amdgcn_readlane(sum, l) - n;
+            return Part{base + l, id - first, n, first};
         }
-        return at;
+        before += last_lane(sum);
     }
-};
+    return Part{-1, 0, 0, 0};
+}
 
 // Weights of keys as B operands of the second product. bf16 holds a weight as the sum of two (8 bits
 // each, 2^-17 of the weight off at most): one alone would put an error of the size of the output's
@@ -280,15 +272,20 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
     float *const s_o = reinterpret_cast<float *>(s_mem);
     const int lane = threadIdx.x & 63, lg = lane >> 4, li = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int heads = a.h_k * row_blocks;
-    const int sub = static_cast<int>(blockIdx.x % heads), h = sub / row_blocks, rb = sub % row_blocks;
+    // The blocks of rows that share keys are 8 apart: workgroups go round the 8 XCDs, so they find them in
+    // one XCD's cache. `group` is the workgroup's number without that.
+    const int eight = static_cast<int>(blockIdx.x) / (8 * row_blocks), among = static_cast<int>(blockIdx.x) % (8 * row_blocks);
+    const int rb = among / 8, pair = 8 * eight + among % 8, group = pair * row_blocks + rb;
+    const int h = pair % a.h_k;
     const int G = a.h_q / a.h_k, R = a.new_tokens * G;
-    const int id = static_cast<int>(blockIdx.x / heads);
+    const int id = pair / a.h_k;
     Part part{id, 0, 1, id};
-    if (a.budget > 0) {
-        part = Cut<KT>(a).find(id);
+    if (a.budget == 0) {
+        if (id >= a.num_seqs) return;
+    } else {
+        part = find_part<KT>(a, id);
         if (part.n < 0) return;
-        if (part.part == 0 && sub == 0 && threadIdx.x == 0) {
+        if (part.part == 0 && h == 0 && rb == 0 && threadIdx.x == 0) {
             a.part_info[2 * part.n] = part.before;
             a.part_info[2 * part.n + 1] = part.parts;
         }
@@ -568,7 +565,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
         const int r = r0 + mt * 16 + li;
         const bool cut = part.parts > 1;
         const float inv = cut ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t part_at = static_cast<int64_t>(blockIdx.x) * ROWS + mt * 16 + li;
+        const int64_t part_at = static_cast<int64_t>(group) * ROWS + mt * 16 + li;
         const int64_t row_at = (static_cast<int64_t>(part.n) * a.new_tokens + row_t[mt]) * a.h_q + h * G + r - row_t[mt] * G;
 #pragma unroll
         for (int c = 0; c < V::S; ++c) {
@@ -600,7 +597,7 @@ template <typename T, int D, int MT, int THREADS>
 __global__ __launch_bounds__(256) void paged_attention_join_kernel(AttentionArgs a, int row_blocks) {
     constexpr int ROWS = 16 * MT, LANES = D / 4, JW = THREADS / LANES, PER = 256 / THREADS;
     __shared__ f32x4 s_o[PER][JW][LANES];
-    __shared__ float s_l[PER][JW];
+    __shared__ float2 s_ml[PER][JW];
     const int G = a.h_q / a.h_k, heads = a.h_k * row_blocks;
     const int slot = threadIdx.x / THREADS, thread = threadIdx.x % THREADS;
     const int64_t at = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * PER + slot;
@@ -620,29 +617,54 @@ __global__ __launch_bounds__(256) void paged_attention_join_kernel(AttentionArgs
         const int h = hq / G, r = t * G + hq % G;
         const int64_t step = static_cast<int64_t>(heads) * ROWS;
         const int64_t first = (static_cast<int64_t>(before) * heads + h * row_blocks + r / ROWS) * ROWS + r % ROWS;
-        for (int p = threadIdx.x & 63; p < parts; p += 64) top = fmaxf(top, a.part_ml[2 * (first + p * step)]);
+        // parts g, JW + g .., four of them under way at a time, with a running maximum as in a part
+        constexpr int U = 4;
+        for (int p = g; p < parts; p += U * JW) {
+            float2 ml[U];
+            f32x4 x[U];
 #pragma unroll
-        for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-        const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-        for (int p = g; p < parts; p += JW) {
-            const int64_t i = first + p * step;
-            const float w = __builtin_amdgcn_exp2f(a.part_ml[2 * i] - ref);
-            l = fmaf(w, a.part_ml[2 * i + 1], l);
-            const f32x4 x = *reinterpret_cast<const f32x4 *>(a.part_o + i * D + 4 * c);
+            for (int u = 0; u < U; ++u) {
+                const int64_t i = first + (p + u * JW < parts ? p + u * JW : p) * step;
+                ml[u] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * i);
+                x[u] = *reinterpret_cast<const f32x4 *>(a.part_o + i * D + 4 * c);
+            }
+            float high = top;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = fmaf(w, x[e], o[e]);
+            for (int u = 0; u < U; ++u) {
+                if (p + u * JW >= parts) ml[u].x = -INFINITY;
+                high = fmaxf(high, ml[u].x);
+            }
+            const float ref = high == -INFINITY ? 0.f : high, keep = __builtin_amdgcn_exp2f(top - ref);
+            top = high;
+            l *= keep;
+            o *= keep;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float w = __builtin_amdgcn_exp2f(ml[u].x - ref);
+                l = fmaf(w, ml[u].y, l);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(w, x[u][e], o[e]);
+            }
         }
     }
     if constexpr (JW > 1) {
         s_o[slot][g][c] = o;
-        if (c == 0) s_l[slot][g] = l;
+        if (c == 0) s_ml[slot][g] = float2{top, l};
         __syncthreads();
         if (g != 0) return;
+        float high = top;
+#pragma unroll
+        for (int x = 1; x < JW; ++x) high = fmaxf(high, s_ml[slot][x].x);
+        const float ref = high == -INFINITY ? 0.f : high, keep = __builtin_amdgcn_exp2f(top - ref);
+        top = high;
+        l *= keep;
+        o *= keep;
 #pragma unroll
         for (int x = 1; x < JW; ++x) {
-            o += s_o[slot][x][c];
-            l += s_l[slot][x];
+            const float w = __builtin_amdgcn_exp2f(s_ml[slot][x].x - ref);
+            l = fmaf(w, s_ml[slot][x].y, l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(w, s_o[slot][x][c][e], o[e]);
         }
     }
     if (!cut) return;
@@ -655,7 +677,7 @@ constexpr int kJoinRows = 2048;      // most rows that take a workgroup each
 
 template <typename T, int D, int MT>
 hipError_t launch(const AttentionArgs &a, const AttentionPlan &p, hipStream_t st) {
-    const unsigned groups = static_cast<unsigned>(p.max_parts * p.row_blocks * a.h_k);
+    const unsigned groups = static_cast<unsigned>((p.max_parts * a.h_k + 7) / 8 * 8 * p.row_blocks);
     hipLaunchKernelGGL((paged_attention_kernel<T, D, MT>), dim3(groups), dim3(64 * kWaves), 0, st, a, static_cast<int>(p.row_blocks));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.budget == 0) return e;
