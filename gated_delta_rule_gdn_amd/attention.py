@@ -17,12 +17,13 @@ Gradients are returned in a dict, ``d`` before each input's name.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import _dtype_code, _ptr, lib
-from .layer import _call, _check, _fits, _gpu_of, _grad_code, _tokens, _whole, _workspace
+from .layer import _call, _check, _gpu_of, _grad_code, _tokens, _workspace
 
 _i32, _i64, _f32, _vp, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p,
                               ctypes.c_size_t)
@@ -56,6 +57,44 @@ def declare(L: ctypes.CDLL) -> None:
         f.restype, f.argtypes = restype, argtypes
 
 
+_MOST = (1 << 31) - 1             # what the C structs hold in 32 bits
+_CONTIGUOUS = torch.contiguous_format
+
+
+def _small(**sizes) -> None:
+    """Refuses sizes that the C structs cannot hold; the C ABI checks everything smaller."""
+    for name, value in sizes.items():
+        if value > _MOST:
+            raise ValueError(f"{name} is {value}, at most {_MOST}")
+
+
+def _whole(name: str, t: Optional[torch.Tensor], dev, dtype, shape) -> Optional[int]:
+    """Checks a contiguous tensor of one type and shape (None is let through); its pointer. (One
+    comparison per property: a call of single tokens takes as long on the host as on the GPU.)"""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev.index or t.shape != shape:
+        _check(name, t, dev, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _heads(name: str, t: torch.Tensor, dev, dtype, shape) -> int:
+    """Checks a token input [B,T,H,d] that may be a column slice. Returns the elements from one
+    token to the next."""
+    if t.dtype is not dtype or t.get_device() != dev.index or t.shape != shape:
+        _check(name, t, dev, dtype, shape)
+    B, T, H, d = shape
+    row = H * d
+    sb, st, sh, sd = t.stride()
+    if T > 1 and sd == 1 and sh == d and st >= row and sb == T * st:
+        return st
+    if T == 1 and sd == 1 and sh == d and sb >= row:
+        return sb
+    return _tokens(name, t, dev, dtype, shape, row)
+
+
 # ---- norms and rotation ------------------------------------------------------------------
 
 
@@ -71,36 +110,41 @@ def rotary_table(num_positions: int, d_rot: int, base: float = 10000.0, device=N
     return torch.cat((angle.cos(), angle.sin()), 1).float()
 
 
-def _rotary_dims(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, eps, grad_code
-                 ) -> RotaryDims:
-    """The checked dims of a rotary call."""
+def _rotary_dims(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, eps, grad_code):
+    """The checked dims of a rotary call and the pointers of its inputs, without v."""
     dev, dtype = _gpu_of("q", q), q.dtype
     if q.dim() != 4:
         raise ValueError("q must be [B,T,h_q,d]")
-    B, T, hq, d = q.shape
-    _fits("the number of tokens", B * T)
-    _fits("a token's values", hq * d)
+    B, T, hq, d = shape = q.shape
     code = _dtype_code(dtype)
-    qs = _tokens("q", q, dev, dtype, q.shape, hq * d)
-    hk, ks, vs = 0, 0, 0
+    qs = _heads("q", q, dev, dtype, shape)
+    hk = ks = vs = 0
+    pk = None
     if k is not None:
         if k.dim() != 4:
             raise ValueError("k must be [B,T,h_k,d]")
         hk = k.shape[2]
-        _fits("a token's values", hk * d)
-        ks = _tokens("k", k, dev, dtype, (B, T, hk, d), hk * d)
+        ks = _heads("k", k, dev, dtype, (B, T, hk, d))
+        pk = k.data_ptr()
     if v is not None:
-        vs = _tokens("v", v, dev, dtype, (B, T, hk, d), hk * d)
+        vs = _heads("v", v, dev, dtype, (B, T, hk, d))
     f32 = torch.float32
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be fp32 [num_positions,d_rot]")
     P, rot = cos_sin.shape
-    _whole("cos_sin", cos_sin, dev, f32, (P, rot))
-    _whole("positions", positions, dev, torch.int32, (B, T))
-    _whole("q_weight", q_weight, dev, f32, (d,))
-    _whole("k_weight", k_weight, dev, f32, (d,))
-    return RotaryDims(B, T, hq, hk, d, _fits("d_rot", rot), 1 if interleaved else 0,
-                      _fits("num_positions", P), code, grad_code, eps, qs, ks, vs)
+    if B * T > _MOST or hq * d > _MOST or hk * d > _MOST or P > _MOST or rot > _MOST:
+        _small(tokens=B * T, values=max(hq, hk) * d, num_positions=P, d_rot=rot)
+    ptrs = (q.data_ptr(), pk, _whole("cos_sin", cos_sin, dev, f32, (P, rot)),
+            _whole("positions", positions, dev, torch.int32, (B, T)),
+            _whole("q_weight", q_weight, dev, f32, (d,)),
+            _whole("k_weight", k_weight, dev, f32, (d,)))
+    return RotaryDims(B, T, hq, hk, d, rot, 1 if interleaved else 0, P, code, grad_code, eps, qs,
+                      ks, vs), ptrs
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A new contiguous tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=_CONTIGUOUS)
 
 
 def qk_rotary_fwd(q, k: Optional[torch.Tensor], cos_sin, positions: Optional[torch.Tensor] = None,
@@ -116,18 +160,17 @@ def qk_rotary_fwd(q, k: Optional[torch.Tensor], cos_sin, positions: Optional[tor
     positions int32 [B,T] (None: 0 .. T-1 in every sequence), one outside the table marking a padding
     token (zero rows); q_weight, k_weight fp32 [d]. Returns (q_out, k_out), which may be given and
     may be contiguous q and k themselves."""
-    d = _rotary_dims(q, k, None, cos_sin, positions, q_weight, k_weight, interleaved, eps, 0)
+    d, ptrs = _rotary_dims(q, k, None, cos_sin, positions, q_weight, k_weight, interleaved, eps, 0)
     dev = q.device
-    qo = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+    qo = _like(q) if q_out is None else q_out
     pq = _whole("q_out", qo, dev, q.dtype, q.shape)
-    ko = None
+    ko = pk = None
     if k is not None:
-        ko = torch.empty(k.shape, dtype=k.dtype, device=dev) if k_out is None else k_out
-        _whole("k_out", ko, dev, k.dtype, k.shape)
+        ko = _like(k) if k_out is None else k_out
+        pk = _whole("k_out", ko, dev, k.dtype, k.shape)
     elif k_out is not None:
         raise ValueError("k_out needs k")
-    _call(dev, lib().gdn2_qk_rotary_fwd, q.data_ptr(), _ptr(k), cos_sin.data_ptr(), _ptr(positions),
-          _ptr(q_weight), _ptr(k_weight), pq, _ptr(ko), ctypes.byref(d))
+    _call(dev, lib().gdn2_qk_rotary_fwd, *ptrs, pq, pk, ctypes.byref(d))
     return qo, ko
 
 
@@ -141,23 +184,30 @@ def qk_rotary_bwd(q, k: Optional[torch.Tensor], cos_sin, dq_out,
     weights given."""
     if (dk_out is None) != (k is None):
         raise ValueError("k and dk_out go together")
-    gt = dq_out.dtype
-    d = _rotary_dims(q, k, None, cos_sin, positions, q_weight, k_weight, interleaved, eps,
-                     _grad_code("dq_out", dq_out, q.dtype))
-    dev, f32 = q.device, torch.float32
-    pdq = _whole("dq_out", dq_out, dev, gt, q.shape)
-    pdk = None if k is None else _whole("dk_out", dk_out, dev, gt, k.shape)
     if k is None:
         k_weight = None
-    new = lambda like, dtype: None if like is None else torch.empty(  # noqa: E731
-        like.shape, dtype=dtype, device=dev)
-    out = {"dq": new(q, gt), "dk": new(k, gt), "dq_weight": new(q_weight, f32),
-           "dk_weight": new(k_weight, f32)}
-    ws = _workspace(workspace, lib().gdn2_qk_rotary_bwd_workspace_bytes(ctypes.byref(d)), dev)
-    _call(dev, lib().gdn2_qk_rotary_bwd, q.data_ptr(), _ptr(k), cos_sin.data_ptr(), _ptr(positions),
-          _ptr(q_weight), _ptr(k_weight), pdq, pdk, *(_ptr(t) for t in out.values()),
-          ctypes.byref(d), ws.data_ptr(), ws.numel())
-    return {n: t for n, t in out.items() if t is not None}
+    gt = dq_out.dtype
+    d, ptrs = _rotary_dims(q, k, None, cos_sin, positions, q_weight, k_weight, interleaved, eps,
+                           _grad_code("dq_out", dq_out, q.dtype))
+    dev = q.device
+    pdq = _whole("dq_out", dq_out, dev, gt, q.shape)
+    out = {"dq": torch.empty_like(dq_out)}
+    pdk = None
+    if k is not None:
+        pdk = _whole("dk_out", dk_out, dev, gt, k.shape)
+        out["dk"] = torch.empty_like(dk_out)
+    if q_weight is not None:
+        out["dq_weight"] = torch.empty_like(q_weight)
+    if k_weight is not None:
+        out["dk_weight"] = torch.empty_like(k_weight)
+    dims = ctypes.byref(d)
+    pw = nw = 0
+    if q_weight is not None or k_weight is not None or workspace is not None:
+        ws = _workspace(workspace, lib().gdn2_qk_rotary_bwd_workspace_bytes(dims), dev)
+        pw, nw = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call(dev, lib().gdn2_qk_rotary_bwd, *ptrs, pdq, pdk, out["dq"].data_ptr(), _ptr(out.get("dk")),
+          _ptr(out.get("dq_weight")), _ptr(out.get("dk_weight")), dims, pw, nw)
+    return out
 
 
 def qk_rotary_bwd_workspace_bytes(batch: int, seqlen: int, d: int) -> int:
@@ -172,7 +222,9 @@ def _pages(k_pages, v_pages, dev, dtype, hk: int, d: int) -> Tuple[int, int]:
     n, size = k_pages.shape[0], k_pages.shape[2]
     _whole("k_pages", k_pages, dev, dtype, (n, hk, size, d))
     _whole("v_pages", v_pages, dev, dtype, (n, hk, size, d))
-    return _fits("num_pages", n), _fits("page_size", size)
+    if n > _MOST or size > _MOST:
+        _small(num_pages=n, page_size=size)
+    return n, size
 
 
 def qk_rotary_append(q, k, v, cos_sin, positions, k_pages, v_pages, slots,
@@ -184,14 +236,14 @@ def qk_rotary_append(q, k, v, cos_sin, positions, k_pages, v_pages, slots,
     [B,T]: the place of each token, page * page_size + row; distinct; outside the pool the token is
     not put anywhere, and neither is a padding token (a position outside the table). For prompts,
     packed or not, and for single tokens alike. Returns q_out [B,T,h_q,d]."""
-    d = _rotary_dims(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, eps, 0)
-    dev = q.device
-    pages, size = _pages(k_pages, v_pages, dev, q.dtype, d.h_k, d.d)
-    ps = _whole("slots", slots, dev, torch.int32, q.shape[:2])
-    qo = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
-    pq = _whole("q_out", qo, dev, q.dtype, q.shape)
-    _call(dev, lib().gdn2_qk_rotary_append, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          cos_sin.data_ptr(), positions.data_ptr(), _ptr(q_weight), _ptr(k_weight), ps, pq,
+    d, ptrs = _rotary_dims(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, eps, 0)
+    dev, dtype, shape = q.device, q.dtype, q.shape
+    pages, size = _pages(k_pages, v_pages, dev, dtype, d.h_k, d.d)
+    ps = _whole("slots", slots, dev, torch.int32, shape[:2])
+    qo = _like(q) if q_out is None else q_out
+    pq = _whole("q_out", qo, dev, dtype, shape)
+    pq_in, pk, pcs, ppos, pqw, pkw = ptrs
+    _call(dev, lib().gdn2_qk_rotary_append, pq_in, pk, v.data_ptr(), pcs, ppos, pqw, pkw, ps, pq,
           k_pages.data_ptr(), v_pages.data_ptr(), pages, size, ctypes.byref(d))
     return qo
 
@@ -214,33 +266,32 @@ def paged_attention_step(q, k_pages, v_pages, page_table, seq_lens, scale: Optio
     dev, dtype = _gpu_of("q", q), q.dtype
     if q.dim() != 4:
         raise ValueError("q must be [N,T,h_q,d]")
-    N, T, hq, d = q.shape
-    _fits("the number of tokens", N * T)
-    _fits("a token's values", hq * d)
+    N, T, hq, d = shape = q.shape
     code = _dtype_code(dtype)
-    step = _tokens("q", q, dev, dtype, q.shape, hq * d)
+    step = _heads("q", q, dev, dtype, shape)
     if k_pages.dim() != 4:
         raise ValueError(f"k_pages must be [num_pages,h_k,page_size,{d}]")
-    hk = _fits("h_k", k_pages.shape[1])
+    hk = k_pages.shape[1]
     pages, size = _pages(k_pages, v_pages, dev, dtype, hk, d)
     if page_table.dim() != 2:
         raise ValueError(f"page_table must be int32 [{N},max_pages]")
-    most = _fits("max_pages", page_table.shape[1])
+    most = page_table.shape[1]
+    if N * T > _MOST or hq * d > _MOST or hk > _MOST or most > _MOST or window > _MOST:
+        _small(tokens=N * T, values=hq * d, h_k=hk, max_pages=most, window=window)
     pt = _whole("page_table", page_table, dev, torch.int32, (N, most))
     pl = _whole("seq_lens", seq_lens, dev, torch.int32, (N,))
-    dims = AttentionDims(N, T, hq, hk, d, pages, size, most, _fits("window", window), code,
+    dims = AttentionDims(N, T, hq, hk, d, pages, size, most, window, code,
                          d ** -0.5 if scale is None else scale, step)
-    o = torch.empty(q.shape, dtype=dtype, device=dev) if out is None else out
-    po = _whole("out", o, dev, dtype, q.shape)
+    o = _like(q) if out is None else out
+    po = _whole("out", o, dev, dtype, shape)
     if return_lse and lse is None:
         lse = torch.empty((N, T, hq), dtype=torch.float32, device=dev)
     ple = _whole("lse", lse, dev, torch.float32, (N, T, hq))
     need = lib().gdn2_paged_attention_step_workspace_bytes(ctypes.byref(dims))
+    pw = nw = 0
     if workspace is not None or need:
         ws = _workspace(workspace, need, dev)
         pw, nw = ws.data_ptr(), ws.numel() * ws.element_size()
-    else:
-        pw, nw = None, 0
     _call(dev, lib().gdn2_paged_attention_step, q.data_ptr(), k_pages.data_ptr(),
           v_pages.data_ptr(), pt, pl, po, ple, ctypes.byref(dims), pw, nw)
     return (o, lse) if return_lse else o
@@ -267,22 +318,23 @@ def pool_copy(pools: Union[torch.Tensor, Sequence[torch.Tensor]], src, dst) -> N
     dev = _gpu_of("src", src)
     if src.dim() != 1:
         raise ValueError("src must be int32 [count]")
-    count = _fits("count", src.numel())
+    count = src.numel()
     ps = _whole("src", src, dev, torch.int32, (count,))
     pd = _whole("dst", dst, dev, torch.int32, (count,))
     if not pools:
         return
-    if pools[0].dim() < 1:
-        raise ValueError("a pool must be [num_slots,...]")
-    slots = _fits("the number of slots", pools[0].shape[0])
-    ptrs, sizes = [], []
+    index = dev.index
+    slots = pools[0].shape[0] if pools[0].dim() else -1
+    if slots > _MOST or count > _MOST:
+        _small(num_slots=slots, count=count)
+    ptrs, sizes = array("q"), array("q")
     for t in pools:
-        if t.device != dev or t.dim() < 1 or t.shape[0] != slots or not t.is_contiguous():
+        if t.get_device() != index or t.dim() < 1 or t.size(0) != slots or not t.is_contiguous():
             if t.dim() >= 1:
                 _check("a pool", t, dev, t.dtype, (slots, *t.shape[1:]))
             raise ValueError("a pool must be a contiguous [num_slots,...]")
-        if t.numel():
+        if t.nbytes:
             ptrs.append(t.data_ptr())
-            sizes.append(t.numel() // slots * t.element_size())
-    n = len(ptrs)
-    _call(dev, lib().gdn2_pool_copy, (_vp * n)(*ptrs), (_i64 * n)(*sizes), n, slots, ps, pd, count)
+            sizes.append(t.nbytes // slots)
+    _call(dev, lib().gdn2_pool_copy, ptrs.buffer_info()[0], sizes.buffer_info()[0], len(ptrs), slots,
+          ps, pd, count)
