@@ -240,10 +240,11 @@ struct RotaryArgs {
     float *partial = nullptr;        // [rotary_parts()][2][d] sums of a backward call
     int64_t q_stride, k_stride, v_stride = 0;
     int tokens, seqlen, h_q, h_k, d, d_rot, num_positions;
-    float eps;
+    int row_heads = 0;               // heads of a token that a wave takes at once: a power of two
+    float eps, inv_d = 0.f;
     bool interleaved, bf16, grad_bf16 = false;
 };
-int rotary_parts(int tokens);                 // rows of the partial sums: workgroups of a backward call
+int rotary_parts(int tokens);                 // most rows of the partial sums: workgroups of a backward call
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st);
 hipError_t launch_rotary_bwd(const RotaryArgs &a, hipStream_t st);
 

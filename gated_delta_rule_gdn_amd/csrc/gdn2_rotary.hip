@@ -22,20 +22,21 @@ namespace gdn2 {
 namespace {
 
 // Where a lane's units lie in a row: unit u = lane + i L holds values a(u) .. a(u) + V - 1 and
-// b(u) .. b(u) + V - 1, whose angles are the table's columns c(u) .. c(u) + V - 1.
-template <int V, int L, int P>
+// b(u) .. b(u) + V - 1, whose angles are the table's columns pair(u) .. pair(u) + V - 1. INTER: pairs
+// (2i, 2i + 1), a unit being 2 V neighbours.
+template <int V, int L, int P, bool INTER>
 struct Units {
-    int lane, d, half, rest;     // half = R / 2; rest = (d - R) / 2
-    bool interleaved;
+    int lane, half, rest;        // half = R / 2; rest = (d - R) / 2
+    __device__ __forceinline__ explicit Units(const RotaryArgs &r)
+        : lane(static_cast<int>(threadIdx.x) % L), half(r.d_rot / 2), rest((r.d - r.d_rot) / 2) {}
     __device__ __forceinline__ int pair(int i) const { return (lane + i * L) * V; }
     __device__ __forceinline__ bool in(int i) const { return pair(i) < half + rest; }
     __device__ __forceinline__ bool turns(int i) const { return pair(i) < half; }
-    // interleaved: one run of 2 V values
     __device__ __forceinline__ int a(int i) const {
-        return interleaved ? 2 * pair(i) : turns(i) ? pair(i) : half + pair(i);
+        return INTER ? 2 * pair(i) : turns(i) ? pair(i) : half + pair(i);
     }
     __device__ __forceinline__ int b(int i) const {
-        return interleaved ? 2 * pair(i) + V : turns(i) ? half + pair(i) : half + rest + pair(i);
+        return INTER ? 2 * pair(i) + V : turns(i) ? half + pair(i) : half + rest + pair(i);
     }
 };
 
@@ -43,10 +44,19 @@ struct Units {
 template <int V, int P>
 using Pairs = float[P][2][V];
 
-// A unit in memory is two runs of V values at a and b. In the interleaved order they are the first
-// and the second V of 2 V neighbours, member m of pair v being value 2 v + m.
-template <typename T, int V, int L, int P>
-__device__ __forceinline__ void load_pairs(const T *row, const Units<V, L, P> &k, Pairs<V, P> &x) {
+// Two runs of V neighbours, as they are in memory, into members: in the interleaved order member m
+// of pair v is value 2 v + m of both runs together.
+template <int V, bool INTER>
+__device__ __forceinline__ void to_members(const float (&lo)[V], const float (&hi)[V], float (&x)[2][V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        x[0][v] = !INTER ? lo[v] : 2 * v < V ? lo[2 * v % V] : hi[2 * v % V];
+        x[1][v] = !INTER ? hi[v] : 2 * v + 1 < V ? lo[(2 * v + 1) % V] : hi[(2 * v + 1) % V];
+    }
+}
+
+template <typename T, int V, int L, int P, bool INTER>
+__device__ __forceinline__ void load_pairs(const T *row, const Units<V, L, P, INTER> &k, Pairs<V, P> &x) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         float lo[V] = {}, hi[V] = {};
@@ -54,25 +64,19 @@ __device__ __forceinline__ void load_pairs(const T *row, const Units<V, L, P> &k
             ldv<T, V>(row + k.a(i), lo);
             ldv<T, V>(row + k.b(i), hi);
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float p = 2 * v < V ? lo[2 * v % V] : hi[2 * v % V];
-            const float q = 2 * v + 1 < V ? lo[(2 * v + 1) % V] : hi[(2 * v + 1) % V];
-            x[i][0][v] = k.interleaved ? p : lo[v];
-            x[i][1][v] = k.interleaved ? q : hi[v];
-        }
+        to_members<V, INTER>(lo, hi, x[i]);
     }
 }
 
-template <typename T, int V, int L, int P>
-__device__ __forceinline__ void store_pairs(T *row, const Units<V, L, P> &k, const Pairs<V, P> &x) {
+template <typename T, int V, int L, int P, bool INTER>
+__device__ __forceinline__ void store_pairs(T *row, const Units<V, L, P, INTER> &k, const Pairs<V, P> &x) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         float lo[V], hi[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            lo[v] = k.interleaved ? x[i][v & 1][v / 2] : x[i][0][v];
-            hi[v] = k.interleaved ? x[i][(V + v) & 1][(V + v) / 2] : x[i][1][v];
+            lo[v] = INTER ? x[i][v & 1][v / 2] : x[i][0][v];
+            hi[v] = INTER ? x[i][(V + v) & 1][(V + v) / 2] : x[i][1][v];
         }
         if (k.in(i)) {
             stv<T, V>(row + k.a(i), lo);
@@ -81,12 +85,42 @@ __device__ __forceinline__ void store_pairs(T *row, const Units<V, L, P> &k, con
     }
 }
 
+// The same loads in two steps: what is in memory now, its members when they are used.
+template <typename T, int V, int P>
+struct RawPairs {
+    Raw<T, V> lo[P], hi[P];
+    template <int L, bool INTER>
+    __device__ __forceinline__ void load(const T *row, const Units<V, L, P, INTER> &k) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (k.in(i)) {
+                lo[i].load(row + k.a(i));
+                hi[i].load(row + k.b(i));
+            }
+    }
+    template <int L, bool INTER>
+    __device__ __forceinline__ void get(const Units<V, L, P, INTER> &k, bool used, Pairs<V, P> &x) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float a[V], b[V];
+            lo[i].get(a);
+            hi[i].get(b);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                a[v] = used && k.in(i) ? a[v] : 0.f;
+                b[v] = used && k.in(i) ? b[v] : 0.f;
+            }
+            to_members<V, INTER>(a, b, x[i]);
+        }
+    }
+};
+
 // Cosines and sines of a lane's pairs; 1 and 0 where nothing turns.
-template <int V, int L, int P>
-__device__ __forceinline__ void load_turn(const float *row, const Units<V, L, P> &k, Pairs<V, P> &t) {
+template <int V, int L, int P, bool INTER>
+__device__ __forceinline__ void load_turn(const float *row, const Units<V, L, P, INTER> &k, bool used, Pairs<V, P> &t) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        if (k.turns(i)) {
+        if (used && k.turns(i)) {
             ldv<float, V>(row + k.pair(i), t[i][0]);
             ldv<float, V>(row + k.half + k.pair(i), t[i][1]);
         } else {
@@ -123,20 +157,34 @@ __device__ __forceinline__ int position_of(const RotaryArgs &a, int token) {
     return p >= 0 && (p < a.num_positions || a.d_rot == 0) ? p : -1;
 }
 
-// A wave takes one token and every gridDim.y-th set of 64 / L of its heads; the sets are those of q,
-// then of k, then of v (which is copied).
-template <typename T, int V, int L, int P>
+// The rows that a wave takes at once: 64 / L of them, a.row_heads heads of as many tokens as that leaves
+// room for. They come in sets: all heads of q, then of k, then (in front of a cache) of v.
+template <int L>
+struct Rows {
+    int head, token;             // the lane's first head, and its token among the wave's
+    int sets_q, sets;
+    __device__ __forceinline__ explicit Rows(const RotaryArgs &a) {
+        const int row = (threadIdx.x & 63) / L;
+        head = row & (a.row_heads - 1);
+        token = row / a.row_heads;
+        sets_q = (a.h_q + a.row_heads - 1) / a.row_heads;
+        sets = sets_q + (a.slots ? 2 : 1) * ((a.h_k + a.row_heads - 1) / a.row_heads);
+    }
+    static __device__ __forceinline__ int tokens(const RotaryArgs &a) { return 64 / L / a.row_heads; }
+};
+
+// A wave takes its tokens and every gridDim.y-th set of their rows; v is copied.
+template <typename T, int V, int L, int P, bool INTER>
 __global__ __launch_bounds__(256) void rotary_fwd_kernel(RotaryArgs a) {
-    constexpr int H = 64 / L;
-    const int lane = threadIdx.x & 63;
-    const int64_t token = (static_cast<int64_t>(blockIdx.x) * 4) + (threadIdx.x >> 6);
-    if (token >= a.tokens) return;
-    const Units<V, L, P> k{lane % L, a.d, a.d_rot / 2, (a.d - a.d_rot) / 2, a.interleaved};
-    const int at = __builtin_amdgcn_readfirstlane(position_of(a, static_cast<int>(token)));
+    const Rows<L> rows(a);
+    const int64_t block = static_cast<int64_t>(blockIdx.z) * gridDim.x + blockIdx.x;
+    const int64_t token = (block * 4 + (threadIdx.x >> 6)) * Rows<L>::tokens(a) + rows.token;
+    const bool real = token < a.tokens;
+    const Units<V, L, P, INTER> k(a);
+    const int at = real ? position_of(a, static_cast<int>(token)) : -1;
     Pairs<V, P> turn;
-    if (at >= 0) load_turn<V, L, P>(a.cos_sin + static_cast<int64_t>(at) * a.d_rot, k, turn);
-    int64_t place = -1;
-    int64_t page = 0;
+    load_turn<V, L, P, INTER>(a.cos_sin + static_cast<int64_t>(at) * a.d_rot, k, at >= 0, turn);
+    int64_t place = -1, page = 0;
     int within = 0;
     if (a.slots && at >= 0) {
         place = a.slots[token];
@@ -144,35 +192,30 @@ __global__ __launch_bounds__(256) void rotary_fwd_kernel(RotaryArgs a) {
         page = place / a.page_size;
         within = static_cast<int>(place % a.page_size);
     }
-    const int sets_q = (a.h_q + H - 1) / H, sets_k = (a.h_k + H - 1) / H;
-    const int sets = sets_q + (a.slots ? 2 : 1) * sets_k;
-    for (int set = blockIdx.y; set < sets; set += gridDim.y) {
-        const int kind = set < sets_q ? 0 : set < sets_q + sets_k ? 1 : 2;
-        const int head = (set - (kind == 0 ? 0 : kind == 1 ? sets_q : sets_q + sets_k)) * H + lane / L;
+    const int sets_k = rows.sets_q + (a.h_k + a.row_heads - 1) / a.row_heads;      // where k's sets end
+    for (int set = blockIdx.y; set < rows.sets; set += gridDim.y) {
+        const int kind = set < rows.sets_q ? 0 : set < sets_k ? 1 : 2;
+        const int head = (set - (kind == 0 ? 0 : kind == 1 ? rows.sets_q : sets_k)) * a.row_heads + rows.head;
         const int heads = kind == 0 ? a.h_q : a.h_k;
-        if (kind && a.slots && place < 0) break;
-        const bool mine = head < heads;
+        const bool cached = kind && a.slots;
+        const bool mine = real && head < heads && !(cached && place < 0);
         const T *src = static_cast<const T *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
                        token * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) +
                        static_cast<int64_t>(head) * a.d;
-        T *dst = static_cast<T *>(kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out);
-        if (kind && a.slots) dst += ((page * a.h_k + head) * a.page_size + within) * a.d;
-        else dst += (token * heads + head) * a.d;
+        T *dst = static_cast<T *>(kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out) +
+                 (cached ? (page * a.h_k + head) * a.page_size + within : token * heads + head) * a.d;
         Pairs<V, P> x;
-        if (mine && at >= 0) {
-            load_pairs<T, V, L, P>(src, k, x);
-        } else {
 #pragma unroll
-            for (int i = 0; i < P; ++i)
+        for (int i = 0; i < P; ++i)
 #pragma unroll
-                for (int v = 0; v < V; ++v) x[i][0][v] = x[i][1][v] = 0.f;
-        }
-        if (kind < 2 && at >= 0) {
+            for (int v = 0; v < V; ++v) x[i][0][v] = x[i][1][v] = 0.f;
+        if (mine && at >= 0) load_pairs<T, V, L, P, INTER>(src, k, x);
+        if (kind < 2) {
             const float *weight = kind == 0 ? a.q_weight : a.k_weight;
             if (weight) {
                 Pairs<V, P> w;
-                load_pairs<float, V, L, P>(weight, k, w);
-                const float r = rsqrtf(lanes_sum<L>(dot<V, P>(x, x)) / a.d + a.eps);
+                load_pairs<float, V, L, P, INTER>(weight, k, w);
+                const float r = rsqrtf(lanes_sum<L>(dot<V, P>(x, x)) * a.inv_d + a.eps);
 #pragma unroll
                 for (int i = 0; i < P; ++i)
 #pragma unroll
@@ -181,27 +224,37 @@ __global__ __launch_bounds__(256) void rotary_fwd_kernel(RotaryArgs a) {
                         x[i][1][v] *= r * w[i][1][v];
                     }
             }
+            if (at < 0) {        // (0 / 0 with an eps of 0)
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) x[i][0][v] = x[i][1][v] = 0.f;
+            }
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                if (k.turns(i))
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float c = turn[i][0][v], s = turn[i][1][v], p = x[i][0][v], q = x[i][1][v];
-                        x[i][0][v] = fmaf(p, c, -q * s);
-                        x[i][1][v] = fmaf(q, c, p * s);
-                    }
+                for (int v = 0; v < V; ++v) {
+                    const float c = turn[i][0][v], s = turn[i][1][v], p = x[i][0][v], q = x[i][1][v];
+                    // (what does not turn is kept as it is: 0 * an infinite partner would be NaN)
+                    x[i][0][v] = k.turns(i) ? fmaf(p, c, -q * s) : p;
+                    x[i][1][v] = k.turns(i) ? fmaf(q, c, p * s) : q;
+                }
         }
-        if (mine) store_pairs<T, V, L, P>(dst, k, x);
+        if (mine) store_pairs<T, V, L, P, INTER>(dst, k, x);
     }
 }
 
-// A wave takes every 4 gridDim.x-th token with all its heads and keeps its columns' sums of the
+// A wave takes its tokens, then those 4 gridDim.x waves on, with all their sets of rows one after the
+// other, the next set's rows under way while one is worked on. It keeps its columns' sums of the
 // weights' gradients in registers; a workgroup's leave as one row of a.partial, [2][d].
-template <typename T, typename TG, int V, int L, int P>
-__global__ __launch_bounds__(256) void rotary_bwd_kernel(RotaryArgs a) {
-    constexpr int H = 64 / L;
+template <typename T, typename TG, int V, int L, int P, bool INTER>
+__global__ __launch_bounds__(256, 3) void rotary_bwd_kernel(RotaryArgs a) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Units<V, L, P> k{lane % L, a.d, a.d_rot / 2, (a.d - a.d_rot) / 2, a.interleaved};
+    const Rows<L> rows(a);
+    const Units<V, L, P, INTER> k(a);
+    const int per = Rows<L>::tokens(a);
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * per + rows.token;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 4 * per;
     Pairs<V, P> dw[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -209,64 +262,80 @@ __global__ __launch_bounds__(256) void rotary_bwd_kernel(RotaryArgs a) {
         for (int i = 0; i < P; ++i)
 #pragma unroll
             for (int v = 0; v < V; ++v) dw[n][i][0][v] = dw[n][i][1][v] = 0.f;
-    for (int64_t token = static_cast<int64_t>(blockIdx.x) * 4 + wave; token < a.tokens;
-         token += static_cast<int64_t>(gridDim.x) * 4) {
-        const int at = __builtin_amdgcn_readfirstlane(position_of(a, static_cast<int>(token)));
-        Pairs<V, P> turn;
-        if (at >= 0) load_turn<V, L, P>(a.cos_sin + static_cast<int64_t>(at) * a.d_rot, k, turn);
-#pragma unroll
-        for (int kind = 0; kind < 2; ++kind) {
-            const int heads = kind ? a.h_k : a.h_q;
+
+    RawPairs<T, V, P> nx;
+    RawPairs<TG, V, P> ng;
+    Pairs<V, P> turn, nturn;
+    // the rows of a set of the tokens, if they are there
+    auto fetch = [&](int64_t token, bool real, int set) {
+        const int kind = set < rows.sets_q ? 0 : 1, heads = kind ? a.h_k : a.h_q;
+        const int head = (set - (kind ? rows.sets_q : 0)) * a.row_heads + rows.head;
+        if (!real || head >= heads) return;
+        ng.load(static_cast<const TG *>(kind ? a.dk_out : a.dq_out) + (token * heads + head) * a.d, k);
+        if (kind ? a.k_weight : a.q_weight)
+            nx.load(static_cast<const T *>(kind ? a.k : a.q) + token * (kind ? a.k_stride : a.q_stride) +
+                        static_cast<int64_t>(head) * a.d, k);
+    };
+    int at = first < a.tokens ? position_of(a, static_cast<int>(first)) : -1;
+    load_turn<V, L, P, INTER>(a.cos_sin + static_cast<int64_t>(at) * a.d_rot, k, at >= 0, turn);
+    fetch(first, at >= 0, 0);
+    for (int64_t base = 0; first - rows.token + base < a.tokens; base += stride) {
+        const int64_t token = first + base, next = token + stride;
+        const bool real = token < a.tokens;
+        const int next_at = next < a.tokens ? position_of(a, static_cast<int>(next)) : -1;
+        for (int set = 0; set < rows.sets; ++set) {
+            const int kind = set < rows.sets_q ? 0 : 1, heads = kind ? a.h_k : a.h_q;
+            const int head = (set - (kind ? rows.sets_q : 0)) * a.row_heads + rows.head;
+            const bool mine = real && head < heads, used = mine && at >= 0;
             const float *weight = kind ? a.k_weight : a.q_weight;
-            const T *src = static_cast<const T *>(kind ? a.k : a.q) + token * (kind ? a.k_stride : a.q_stride);
-            const TG *dy = static_cast<const TG *>(kind ? a.dk_out : a.dq_out) + token * heads * a.d;
-            TG *dst = static_cast<TG *>(kind ? a.dk : a.dq) + token * heads * a.d;
-            for (int head = lane / L; head < heads + lane / L; head += H) {
-                const bool mine = head < heads;
-                Pairs<V, P> g, x;
+            Pairs<V, P> g, x;
+            ng.get(k, used, g);
+            if (weight) nx.get(k, used, x);
+            const bool last = set + 1 == rows.sets;
+            fetch(last ? next : token, last ? next_at >= 0 : at >= 0, last ? 0 : set + 1);
+            if (last) load_turn<V, L, P, INTER>(a.cos_sin + static_cast<int64_t>(next_at) * a.d_rot, k, next_at >= 0, nturn);
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float c = turn[i][0][v], s = turn[i][1][v], p = g[i][0][v], q = g[i][1][v];
+                    g[i][0][v] = k.turns(i) ? fmaf(p, c, q * s) : p;
+                    g[i][1][v] = k.turns(i) ? fmaf(q, c, -p * s) : q;
+                }
+            if (weight) {
+                Pairs<V, P> w;
+                load_pairs<float, V, L, P, INTER>(weight, k, w);
+                // (a row that is not there has a sum of 0, and no gradient even with an eps of 0)
+                const float r = used ? rsqrtf(lanes_sum<L>(dot<V, P>(x, x)) * a.inv_d + a.eps) : 0.f;
 #pragma unroll
                 for (int i = 0; i < P; ++i)
 #pragma unroll
-                    for (int v = 0; v < V; ++v) g[i][0][v] = g[i][1][v] = x[i][0][v] = x[i][1][v] = 0.f;
-                if (mine && at >= 0) {
-                    load_pairs<TG, V, L, P>(dy + head * a.d, k, g);
-                    if (weight) load_pairs<T, V, L, P>(src + head * a.d, k, x);
-                }
-                if (at >= 0) {
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < P; ++i)
-                        if (k.turns(i))
+                        for (int v = 0; v < V; ++v) {
+                            const float e = g[i][m][v] * (x[i][m][v] * r);
+                            if (kind) dw[1][i][m][v] += e;
+                            else dw[0][i][m][v] += e;
+                            g[i][m][v] *= w[i][m][v];
+                        }
+                const float mean = lanes_sum<L>(dot<V, P>(g, x)) * a.inv_d * r * r;
 #pragma unroll
-                            for (int v = 0; v < V; ++v) {
-                                const float c = turn[i][0][v], s = turn[i][1][v], p = g[i][0][v], q = g[i][1][v];
-                                g[i][0][v] = fmaf(p, c, q * s);
-                                g[i][1][v] = fmaf(q, c, -p * s);
-                            }
-                    if (weight) {
-                        Pairs<V, P> w;
-                        load_pairs<float, V, L, P>(weight, k, w);
-                        const float r = rsqrtf(lanes_sum<L>(dot<V, P>(x, x)) / a.d + a.eps);
+                for (int i = 0; i < P; ++i)
 #pragma unroll
-                        for (int i = 0; i < P; ++i)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                                for (int v = 0; v < V; ++v) {
-                                    if (mine) dw[kind][i][m][v] = fmaf(g[i][m][v], x[i][m][v] * r, dw[kind][i][m][v]);
-                                    g[i][m][v] *= w[i][m][v];
-                                }
-                        const float mean = lanes_sum<L>(dot<V, P>(g, x)) / a.d * r * r;
-#pragma unroll
-                        for (int i = 0; i < P; ++i)
-#pragma unroll
-                            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                                for (int v = 0; v < V; ++v) g[i][m][v] = r * (g[i][m][v] - x[i][m][v] * mean);
-                    }
-                }
-                if (mine) store_pairs<TG, V, L, P>(dst + head * a.d, k, g);
+                        for (int v = 0; v < V; ++v) g[i][m][v] = r * (g[i][m][v] - x[i][m][v] * mean);
             }
+            if (mine)
+                store_pairs<TG, V, L, P, INTER>(static_cast<TG *>(kind ? a.dk : a.dq) + (token * heads + head) * a.d, k, g);
         }
+        at = next_at;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int v = 0; v < V; ++v) turn[i][m][v] = nturn[i][m][v];
     }
     if (!a.q_weight && !a.k_weight) return;
     // the lanes that hold the same columns, then the four waves
@@ -286,7 +355,7 @@ __global__ __launch_bounds__(256) void rotary_bwd_kernel(RotaryArgs a) {
                 }
     if (lane < L)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) store_pairs<float, V, L, P>(s_sum[wave] + n * a.d, k, dw[n]);
+        for (int n = 0; n < 2; ++n) store_pairs<float, V, L, P, INTER>(s_sum[wave] + n * a.d, k, dw[n]);
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * a.d; c += 256)
         a.partial[static_cast<int64_t>(blockIdx.x) * 2 * a.d + c] =
@@ -315,33 +384,54 @@ __global__ __launch_bounds__(1024) void rotary_reduce_kernel(RotaryArgs a, int p
     }
 }
 
-template <typename T, typename TG, int V, int L, int P>
-hipError_t launch(const RotaryArgs &a, bool backward, hipStream_t st) {
+// Waves of a forward call up to which a token's sets of rows go to waves of their own.
+constexpr int kRotaryWaves = 4096;
+// Workgroups of a backward call: three per CU.
+constexpr int kRotaryGroups = 768;
+
+int next_pow2(int x) {
+    int p = 1;
+    while (p < x) p *= 2;
+    return p;
+}
+
+template <typename T, typename TG, int V, int L, int P, bool INTER>
+hipError_t launch(RotaryArgs a, bool backward, hipStream_t st) {
+    const int most = next_pow2(a.h_q > a.h_k ? a.h_q : a.h_k);
+    a.row_heads = most < 64 / L ? most : 64 / L;
+    a.inv_d = 1.f / a.d;
+    const int per = 4 * (64 / L / a.row_heads);          // tokens of a workgroup
+    const int groups = a.tokens / per + (a.tokens % per != 0);
     if (!backward) {
-        hipLaunchKernelGGL((rotary_fwd_kernel<T, V, L, P>), dim3(static_cast<unsigned>((a.tokens + 3) / 4), 1),
-                           dim3(256), 0, st, a);
+        const int sets = (a.h_q + a.row_heads - 1) / a.row_heads + (a.slots ? 2 : 1) * ((a.h_k + a.row_heads - 1) / a.row_heads);
+        const int waves = kRotaryWaves / (4 * groups);   // of every token's
+        const unsigned gy = static_cast<unsigned>(waves < 1 ? 1 : waves < sets ? waves : sets);
+        // one dimension of a grid holds less than 2^32 threads
+        const unsigned gx = static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20);
+        const unsigned gz = (static_cast<unsigned>(groups) + gx - 1) / gx;
+        hipLaunchKernelGGL((rotary_fwd_kernel<T, V, L, P, INTER>), dim3(gx, gy, gz), dim3(256), 0, st, a);
         return hipGetLastError();
     }
-    const int parts = rotary_parts(a.tokens);
-    hipLaunchKernelGGL((rotary_bwd_kernel<T, TG, V, L, P>), dim3(parts), dim3(256), 0, st, a);
+    const int most_parts = rotary_parts(a.tokens), parts = groups < 1 ? 1 : groups < most_parts ? groups : most_parts;
+    hipLaunchKernelGGL((rotary_bwd_kernel<T, TG, V, L, P, INTER>), dim3(parts), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !(a.q_weight || a.k_weight)) return e;
     hipLaunchKernelGGL(rotary_reduce_kernel, dim3((2 * a.d + 31) / 32), dim3(1024), 0, st, a, parts);
     return hipGetLastError();
 }
 
-template <typename T, typename TG, int V>
+template <typename T, typename TG, int V, bool INTER>
 hipError_t launch_rows(const RotaryArgs &a, bool backward, hipStream_t st) {
     const int units = a.d / (2 * V);
     if constexpr (V == 1) {
-        if (units <= 64) return launch<T, TG, 1, 16, 4>(a, backward, st);
-        return launch<T, TG, 1, 64, 4>(a, backward, st);
+        if (units <= 64) return launch<T, TG, 1, 16, 4, INTER>(a, backward, st);
+        return launch<T, TG, 1, 64, 4, INTER>(a, backward, st);
     } else {
-        if (units <= 4) return launch<T, TG, V, 4, 1>(a, backward, st);
-        if (units <= 8) return launch<T, TG, V, 8, 1>(a, backward, st);
-        if (units <= 16) return launch<T, TG, V, 16, 1>(a, backward, st);
-        if (units <= 32) return launch<T, TG, V, 32, 1>(a, backward, st);
-        return launch<T, TG, V, 64, 1>(a, backward, st);
+        if (units <= 4) return launch<T, TG, V, 4, 1, INTER>(a, backward, st);
+        if (units <= 8) return launch<T, TG, V, 8, 1, INTER>(a, backward, st);
+        if (units <= 16) return launch<T, TG, V, 16, 1, INTER>(a, backward, st);
+        if (units <= 32) return launch<T, TG, V, 32, 1, INTER>(a, backward, st);
+        return launch<T, TG, V, 64, 1, INTER>(a, backward, st);
     }
 }
 
@@ -359,14 +449,16 @@ bool whole(const RotaryArgs &a, int V) {
 template <typename T, typename TG>
 hipError_t launch_types(const RotaryArgs &a, bool backward, hipStream_t st) {
     constexpr int V = sizeof(T) == 2 ? 8 : 4;
-    return whole(a, V) ? launch_rows<T, TG, V>(a, backward, st) : launch_rows<T, TG, 1>(a, backward, st);
+    if (a.interleaved)
+        return whole(a, V) ? launch_rows<T, TG, V, true>(a, backward, st) : launch_rows<T, TG, 1, true>(a, backward, st);
+    return whole(a, V) ? launch_rows<T, TG, V, false>(a, backward, st) : launch_rows<T, TG, 1, false>(a, backward, st);
 }
 
 }  // namespace
 
 int rotary_parts(int tokens) {
     const int groups = tokens / 4 + (tokens % 4 != 0);
-    return groups < 1 ? 1 : groups < 1024 ? groups : 1024;
+    return groups < 1 ? 1 : groups < kRotaryGroups ? groups : kRotaryGroups;
 }
 
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st) {
