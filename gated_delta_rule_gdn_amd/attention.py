@@ -58,7 +58,6 @@ def declare(L: ctypes.CDLL) -> None:
 
 
 _MOST = (1 << 31) - 1             # what the C structs hold in 32 bits
-_CONTIGUOUS = torch.contiguous_format
 
 
 def _small(**sizes) -> None:
@@ -142,9 +141,12 @@ def _rotary_dims(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, e
                       ks, vs), ptrs
 
 
-def _like(t: torch.Tensor) -> torch.Tensor:
-    """A new contiguous tensor of t's shape and type."""
-    return torch.empty_like(t, memory_format=_CONTIGUOUS)
+def _output(name: str, given: Optional[torch.Tensor], like: torch.Tensor):
+    """A contiguous output of the shape and type of an input, new or given, and its pointer."""
+    if given is None:
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
+        return out, out.data_ptr()
+    return given, _whole(name, given, like.device, like.dtype, like.shape)
 
 
 def qk_rotary_fwd(q, k: Optional[torch.Tensor], cos_sin, positions: Optional[torch.Tensor] = None,
@@ -162,12 +164,10 @@ def qk_rotary_fwd(q, k: Optional[torch.Tensor], cos_sin, positions: Optional[tor
     may be contiguous q and k themselves."""
     d, ptrs = _rotary_dims(q, k, None, cos_sin, positions, q_weight, k_weight, interleaved, eps, 0)
     dev = q.device
-    qo = _like(q) if q_out is None else q_out
-    pq = _whole("q_out", qo, dev, q.dtype, q.shape)
+    qo, pq = _output("q_out", q_out, q)
     ko = pk = None
     if k is not None:
-        ko = _like(k) if k_out is None else k_out
-        pk = _whole("k_out", ko, dev, k.dtype, k.shape)
+        ko, pk = _output("k_out", k_out, k)
     elif k_out is not None:
         raise ValueError("k_out needs k")
     _call(dev, lib().gdn2_qk_rotary_fwd, *ptrs, pq, pk, ctypes.byref(d))
@@ -240,8 +240,7 @@ def qk_rotary_append(q, k, v, cos_sin, positions, k_pages, v_pages, slots,
     dev, dtype, shape = q.device, q.dtype, q.shape
     pages, size = _pages(k_pages, v_pages, dev, dtype, d.h_k, d.d)
     ps = _whole("slots", slots, dev, torch.int32, shape[:2])
-    qo = _like(q) if q_out is None else q_out
-    pq = _whole("q_out", qo, dev, dtype, shape)
+    qo, pq = _output("q_out", q_out, q)
     pq_in, pk, pcs, ppos, pqw, pkw = ptrs
     _call(dev, lib().gdn2_qk_rotary_append, pq_in, pk, v.data_ptr(), pcs, ppos, pqw, pkw, ps, pq,
           k_pages.data_ptr(), v_pages.data_ptr(), pages, size, ctypes.byref(d))
@@ -282,11 +281,12 @@ def paged_attention_step(q, k_pages, v_pages, page_table, seq_lens, scale: Optio
     pl = _whole("seq_lens", seq_lens, dev, torch.int32, (N,))
     dims = AttentionDims(N, T, hq, hk, d, pages, size, most, window, code,
                          d ** -0.5 if scale is None else scale, step)
-    o = _like(q) if out is None else out
-    po = _whole("out", o, dev, dtype, shape)
+    o, po = _output("out", out, q)
     if return_lse and lse is None:
         lse = torch.empty((N, T, hq), dtype=torch.float32, device=dev)
-    ple = _whole("lse", lse, dev, torch.float32, (N, T, hq))
+        ple = lse.data_ptr()
+    else:
+        ple = _whole("lse", lse, dev, torch.float32, (N, T, hq))
     need = lib().gdn2_paged_attention_step_workspace_bytes(ctypes.byref(dims))
     pw = nw = 0
     if workspace is not None or need:
@@ -327,14 +327,17 @@ def pool_copy(pools: Union[torch.Tensor, Sequence[torch.Tensor]], src, dst) -> N
     slots = pools[0].shape[0] if pools[0].dim() else -1
     if slots > _MOST or count > _MOST:
         _small(num_slots=slots, count=count)
-    ptrs, sizes = array("q"), array("q")
     for t in pools:
-        if t.get_device() != index or t.dim() < 1 or t.size(0) != slots or not t.is_contiguous():
-            if t.dim() >= 1:
+        if t.get_device() != index or not t.dim() or t.shape[0] != slots or not t.is_contiguous():
+            if t.dim():
                 _check("a pool", t, dev, t.dtype, (slots, *t.shape[1:]))
             raise ValueError("a pool must be a contiguous [num_slots,...]")
-        if t.nbytes:
-            ptrs.append(t.data_ptr())
-            sizes.append(t.nbytes // slots)
+    if slots == 0:
+        return
+    sizes = array("q", [t.nbytes // slots for t in pools])
+    if 0 in sizes:
+        pools = [t for t in pools if t.nbytes]
+        sizes = array("q", [n for n in sizes if n])
+    ptrs = array("q", [t.data_ptr() for t in pools])
     _call(dev, lib().gdn2_pool_copy, ptrs.buffer_info()[0], sizes.buffer_info()[0], len(ptrs), slots,
           ps, pd, count)

@@ -161,7 +161,7 @@ template <typename T> constexpr int tile_keys(int d) { return sizeof(T) == 2 && 
 
 // Waves per SIMD that the registers are held to.
 template <typename T, int D, int MT> constexpr int waves_per_simd() {
-    if (D == 64) return sizeof(T) == 2 && MT == 2 ? 3 : 4;
+    if (D == 64) return MT == 2 ? 3 : 4;
     return D == 128 ? (MT == 1 ? 3 : 2) : sizeof(T) == 4 ? 1 : 2;
 }
 
@@ -170,7 +170,8 @@ template <typename T> struct Ops;
 template <> struct Ops<bf16_t> {
     static constexpr int QW = 32;
     typedef u32x4 Frag;                          // 8 values of a q or k row
-    static __device__ __forceinline__ f32x4 qk(Frag k, Frag q, f32x4 c) { return mma_k32(k, q, c); }
+    static constexpr int CHAINS = 1;
+    static __device__ __forceinline__ void qk(Frag k, Frag q, f32x4 (&c)[1]) { c[0] = mma_k32(k, q, c[0]); }
     static __device__ __forceinline__ Frag each(const bf16_t *p) {      // value by value
         Frag f;
 #pragma unroll
@@ -181,7 +182,11 @@ template <> struct Ops<bf16_t> {
 template <> struct Ops<float> {
     static constexpr int QW = 16;
     typedef f32x4 Frag;
-    static __device__ __forceinline__ f32x4 qk(Frag k, Frag q, f32x4 c) { return mma_k16_f32(k, q, c); }
+    static constexpr int CHAINS = 4;
+    static __device__ __forceinline__ void qk(Frag k, Frag q, f32x4 (&c)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(k[i], q[i], c[i], 0, 0, 0);
+    }
     static __device__ __forceinline__ Frag each(const float *p) { return Frag{p[0], p[1], p[2], p[3]}; }
 };
 
@@ -356,32 +361,49 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
         id = id > 0 ? id : 0;
         return static_cast<uint32_t>((id * a.h_k + h) * a.page_size + (j - pg * a.page_size));
     };
+    // scale log2 e, and what fp32 leaves off it: it is multiplied with differences of up to hundreds
     const float to2 = a.scale * kLog2e;
+    const float to2_rest = fmaf(a.scale, kLog2e, -to2) + a.scale * 1.92596303e-8f;
     Frag k[ST][QF];
     V v;
     f32x4 s[MT][ST];
     typename V::Weights pb[MT];
 
+    // fp32: four chains of d / 16 instructions, joined at the end, in place of one of d / 4. A score's
+    // error goes into every weight, and it is the largest (1.1e-6 of o at 64 values with one chain).
+    constexpr int CH = Op::CHAINS;
     auto products = [&]() {
+        f32x4 part[MT][ST][CH];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int t = 0; t < ST; ++t) s[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) part[mt][t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int f = 0; f < QF; ++f)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const Frag q = s_q[(mt * QF + f) * 64 + lane];
 #pragma unroll
-                for (int t = 0; t < ST; ++t) s[mt][t] = Op::qk(k[t][f], q, s[mt][t]);
+                for (int t = 0; t < ST; ++t) Op::qk(k[t][f], q, part[mt][t]);
             }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+                s[mt][t] = CH == 1 ? part[mt][t][0]
+                                   : (part[mt][t][0] + part[mt][t][1 % CH]) + (part[mt][t][2 % CH] + part[mt][t][3 % CH]);
     };
-    auto softmax = [&](int mt) {
+    // Of a tile's products, those that seen(t, i) says. A weight's exponent is one fused operation (in
+    // fp32 with the rest of the factor before it), so that it is off by its own rounding, not by that of
+    // the larger product.
+    auto softmax = [&](int mt, auto &&seen) {
         float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[mt][t][i]);
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, seen(t, i) ? s[mt][t][i] * to2 : -INFINITY);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         top = fmaxf(top, m[mt]);
@@ -391,7 +413,11 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][t][i] = __builtin_amdgcn_exp2f(s[mt][t][i] - at);
+            for (int i = 0; i < 4; ++i)
+            {
+                const float less = sizeof(T) == 4 ? fmaf(s[mt][t][i], to2_rest, -at) : -at;
+                s[mt][t][i] = seen(t, i) ? __builtin_amdgcn_exp2f(fmaf(s[mt][t][i], to2, less)) : 0.f;
+            }
         l[mt] *= keep;
 #pragma unroll
         for (int t = 0; t < ST; ++t) l[mt] += (s[mt][t].x + s[mt][t].y) + (s[mt][t].z + s[mt][t].w);
@@ -452,14 +478,10 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int first = max(lo, first_of(row_t[mt])), end = min(hi, end_of(row_t[mt]));
-#pragma unroll
-            for (int t = 0; t < ST; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = tile + t * 16 + 4 * lg + i;
-                    s[mt][t][i] = j >= first && j < end ? s[mt][t][i] * to2 : -INFINITY;
-                }
-            softmax(mt);
+            softmax(mt, [&](int t, int i) {
+                const int j = tile + t * 16 + 4 * lg + i;
+                return j >= first && j < end;
+            });
         }
         // Where rows see different keys of a tile, a weight of zero would still take in a value that
         // is not finite (0 * NaN): token by token then, without the values it does not see.
@@ -519,13 +541,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
         load_keys();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int t = 0; t < ST; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[mt][t][i] *= to2;
-            softmax(mt);
-        }
+        for (int mt = 0; mt < MT; ++mt) softmax(mt, [](int, int) { return true; });
         __builtin_amdgcn_sched_barrier(0);
         add_values();
     }

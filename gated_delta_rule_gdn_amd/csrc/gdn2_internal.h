@@ -280,8 +280,10 @@ constexpr int kCopyPools = 64;       // pools of one launch
 struct CopyArgs {
     void *pool[kCopyPools];
     int64_t bytes[kCopyPools];       // of a slot
+    int32_t first_piece[kCopyPools];     // of the workgroups that copy a pair: a pool's first one
     const int32_t *src, *dst;
     int num_pools, num_slots, count;
+    int same_pieces;                 // of every pool, or 0
 };
 hipError_t launch_pool_copy(const CopyArgs &a, hipStream_t st);
 

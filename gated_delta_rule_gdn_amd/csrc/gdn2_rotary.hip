@@ -14,6 +14,8 @@
 // values that are not rotated are cut into pairs in the same way. A wave takes a token's heads,
 // 64 / L at a time, with the token's cosines and sines and the weights in registers. Sums and
 // rotation are fp32, rounded once at the store.
+#include <initializer_list>
+
 #include "gdn2_internal.h"
 #include "gdn2_layer.h"
 
@@ -384,10 +386,13 @@ __global__ __launch_bounds__(1024) void rotary_reduce_kernel(RotaryArgs a, int p
     }
 }
 
-// Waves of a forward call up to which a token's sets of rows go to waves of their own.
+// Waves that fill the chip. A forward call of fewer gives the sets of a token's rows waves of their own
+// (64 tokens x 20 heads of 256 into pages 8.6 -> 3.9 us), and both directions put heads of several
+// tokens side by side only above that.
 constexpr int kRotaryWaves = 4096;
-// Workgroups of a backward call: three per CU.
-constexpr int kRotaryGroups = 768;
+// Most workgroups of a backward call: four per CU. (Accesses of eight values: three. With four, the last
+// quarter of 8,192 tokens x 32 heads of 128 runs alone, 47.9 us in place of 40.9.)
+constexpr int kRotaryGroups = 1024;
 
 int next_pow2(int x) {
     int p = 1;
@@ -395,10 +400,21 @@ int next_pow2(int x) {
     return p;
 }
 
+// Heads of a token that a wave takes at once, of the `rows` that it has room for. As many as there are
+// leaves places empty where the last set of q or of k is not full (16 and 4 heads in sets of 16); with
+// enough tokens for all workgroups, the number that leaves the fewest empty.
+int heads_at_once(const RotaryArgs &a, int rows, bool backward) {
+    const int most = next_pow2(a.h_q > a.h_k ? a.h_q : a.h_k);
+    int best = most < rows ? most : rows;
+    auto taken = [&](int n) { return (a.h_q + n - 1) / n * n + (a.h_k + n - 1) / n * n; };
+    for (int n = best / 2; n >= 1; n /= 2)
+        if (taken(n) < taken(best) && a.tokens / (rows / n) >= kRotaryWaves) best = n;
+    return best;
+}
+
 template <typename T, typename TG, int V, int L, int P, bool INTER>
 hipError_t launch(RotaryArgs a, bool backward, hipStream_t st) {
-    const int most = next_pow2(a.h_q > a.h_k ? a.h_q : a.h_k);
-    a.row_heads = most < 64 / L ? most : 64 / L;
+    a.row_heads = heads_at_once(a, 64 / L, backward);
     a.inv_d = 1.f / a.d;
     const int per = 4 * (64 / L / a.row_heads);          // tokens of a workgroup
     const int groups = a.tokens / per + (a.tokens % per != 0);
@@ -412,7 +428,9 @@ hipError_t launch(RotaryArgs a, bool backward, hipStream_t st) {
         hipLaunchKernelGGL((rotary_fwd_kernel<T, V, L, P, INTER>), dim3(gx, gy, gz), dim3(256), 0, st, a);
         return hipGetLastError();
     }
-    const int most_parts = rotary_parts(a.tokens), parts = groups < 1 ? 1 : groups < most_parts ? groups : most_parts;
+    // as many as run at once: instances of eight values per access have 161-168 registers, others 96-122
+    constexpr int AT_ONCE = V == 8 ? 3 * 256 : kRotaryGroups;
+    const int parts = groups < 1 ? 1 : groups < AT_ONCE ? groups : AT_ONCE;
     hipLaunchKernelGGL((rotary_bwd_kernel<T, TG, V, L, P, INTER>), dim3(parts), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !(a.q_weight || a.k_weight)) return e;
@@ -423,9 +441,9 @@ hipError_t launch(RotaryArgs a, bool backward, hipStream_t st) {
 template <typename T, typename TG, int V, bool INTER>
 hipError_t launch_rows(const RotaryArgs &a, bool backward, hipStream_t st) {
     const int units = a.d / (2 * V);
-    if constexpr (V == 1) {
-        if (units <= 64) return launch<T, TG, 1, 16, 4, INTER>(a, backward, st);
-        return launch<T, TG, 1, 64, 4, INTER>(a, backward, st);
+    if constexpr (V <= 2) {
+        if (units <= 64 / V) return launch<T, TG, V, 16, 4 / V, INTER>(a, backward, st);
+        return launch<T, TG, V, 64, 4 / V, INTER>(a, backward, st);
     } else {
         if (units <= 4) return launch<T, TG, V, 4, 1, INTER>(a, backward, st);
         if (units <= 8) return launch<T, TG, V, 8, 1, INTER>(a, backward, st);
@@ -435,23 +453,29 @@ hipError_t launch_rows(const RotaryArgs &a, bool backward, hipStream_t st) {
     }
 }
 
-bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Whether every run of V pairs' members can be taken in whole accesses.
+// Whether every run of V pairs' members can be taken in whole accesses, at most 16 bytes each.
 bool whole(const RotaryArgs &a, int V) {
     const int half = a.d_rot / 2, rest = (a.d - a.d_rot) / 2;
-    return half % V == 0 && rest % V == 0 && a.q_stride % V == 0 && a.k_stride % V == 0 &&
-           a.v_stride % V == 0 && al16(a.q) && al16(a.k) && al16(a.v) && al16(a.cos_sin) && al16(a.q_weight) &&
-           al16(a.k_weight) && al16(a.q_out) && al16(a.k_out) && al16(a.v_out) && al16(a.dq_out) &&
-           al16(a.dk_out) && al16(a.dq) && al16(a.dk);
+    uintptr_t low = 0;
+    for (const void *p : {a.q, a.k, a.v, static_cast<const void *>(a.cos_sin), static_cast<const void *>(a.q_weight),
+                          static_cast<const void *>(a.k_weight), static_cast<const void *>(a.q_out),
+                          static_cast<const void *>(a.k_out), static_cast<const void *>(a.v_out), a.dq_out, a.dk_out,
+                          static_cast<const void *>(a.dq), static_cast<const void *>(a.dk)})
+        low |= reinterpret_cast<uintptr_t>(p);
+    return half % V == 0 && rest % V == 0 && a.q_stride % V == 0 && a.k_stride % V == 0 && a.v_stride % V == 0 &&
+           low % (V == 2 ? 8 : 16) == 0;
+}
+
+template <typename T, typename TG, bool INTER>
+hipError_t launch_types(const RotaryArgs &a, bool backward, hipStream_t st) {
+    constexpr int V = sizeof(T) == 2 ? 8 : 4;
+    if (whole(a, V)) return launch_rows<T, TG, V, INTER>(a, backward, st);
+    return whole(a, 2) ? launch_rows<T, TG, 2, INTER>(a, backward, st) : launch_rows<T, TG, 1, INTER>(a, backward, st);
 }
 
 template <typename T, typename TG>
 hipError_t launch_types(const RotaryArgs &a, bool backward, hipStream_t st) {
-    constexpr int V = sizeof(T) == 2 ? 8 : 4;
-    if (a.interleaved)
-        return whole(a, V) ? launch_rows<T, TG, V, true>(a, backward, st) : launch_rows<T, TG, 1, true>(a, backward, st);
-    return whole(a, V) ? launch_rows<T, TG, V, false>(a, backward, st) : launch_rows<T, TG, 1, false>(a, backward, st);
+    return a.interleaved ? launch_types<T, TG, true>(a, backward, st) : launch_types<T, TG, false>(a, backward, st);
 }
 
 }  // namespace
