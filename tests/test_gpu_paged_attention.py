@@ -131,6 +131,16 @@ def test_more_sequences_than_a_wave_has_lanes():
         compare(make(n, lens, 1, 1, 2, 64, 16, BF16), only=[0, n // 2 - 1, n // 2, n // 2 + 1, n - 2, n - 1])
 
 
+@pytest.mark.parametrize("n,hk,d", [(300, 1, 64), (257, 2, 128), (1500, 1, 64), (520, 4, 128)])
+def test_hundreds_of_sequences(n, hk, d):
+    """More of them than are looked at together, fewer and more than run at once, two long ones among
+    them."""
+    rng = np.random.default_rng(n)
+    lens = [int(v) for v in rng.integers(0, 40, n)]
+    lens[3], lens[n - 2] = 5000, 1300
+    compare(make(n, lens, 1, hk, 2, d, 16, BF16), only=[0, 2, 3, 4, 63, 64, 255, 256, n - 3, n - 2, n - 1])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_garbage_behind_the_end_is_never_used(dtype):
     """NaN, infinities and the type's lowest value in the unused places give the same bits."""
