@@ -29,6 +29,10 @@ constexpr int kWaves = 4;           // of a workgroup: as many as an output tile
 // into.
 constexpr int kWholeSteps = 4;
 constexpr int kLeastSteps = 1;
+// Shares of all steps, in parts that run at once, that a part is held to where sequences outnumber those
+// (256 sequences of 32,768 tokens together, 8 key heads of 128: 44.8 us with 2, 47.8 with 1, 56.4 with 8;
+// 300 of 150,000: 125, 132, 148).
+constexpr int kTurns = 2;
 
 // Inclusive sum over the lanes of a wave, by the rows of 16 that DPP shifts in and across them.
 __device__ __forceinline__ int lane_sums(int x) {
@@ -78,14 +82,20 @@ struct Part {
 // its heads, end together if no part is longer than another's and none has to wait, so the steps of a
 // part are the fewest that give at most `budget` parts, or near them. More sequences than that run
 // in turn, and only those longer than a share of the whole are cut. (64 sequences of 262,144 tokens
-// together, 4 key heads of 128: 103 us with at most 768 parts for 768 places, 106 with about 1,024.)
+// together, 4 key heads of 128: 103 us with at most 768 workgroups for 768 places, 106 with about 1,024.)
 // Every workgroup works this out by itself, in loops: what is not repeated has its code fetched
 // first, which takes longer than running it (four tries side by side: 0.6 us more than in turn).
 template <int KT>
-__device__ __forceinline__ Part find_part(const AttentionArgs &a, int id) {
+__device__ __forceinline__ Part find_part(const AttentionArgs &a, int id, int (&s_steps)[64 * kWaves]) {
     const int lane = threadIdx.x & 63;
-    auto steps_of = [&](int n) { return n < a.num_seqs ? seq_steps<KT>(a, seq_len(a, n)) : 0; };
-    const int mine = steps_of(lane);
+    auto load = [&](int n) { return n < a.num_seqs ? seq_steps<KT>(a, seq_len(a, n)) : 0; };
+    // up to 64 sequences are in registers, up to 256 in LDS, a load per wave
+    const int mine = load(a.num_seqs <= 64 ? lane : threadIdx.x);
+    if (a.num_seqs > 64) {
+        s_steps[threadIdx.x] = mine;
+        __syncthreads();
+    }
+    auto steps_of = [&](int n) { return a.num_seqs <= 64 ? mine : n < 64 * kWaves ? s_steps[n] : load(n); };
     const float shares = static_cast<float>(a.budget - a.num_seqs);
     int low = 0, per = 0, next = 0;
 #pragma unroll 1
@@ -95,7 +105,7 @@ __device__ __forceinline__ Part find_part(const AttentionArgs &a, int id) {
         int64_t sum = 0;
 #pragma unroll 1
         for (int base = 0; base < a.num_seqs; base += 64) {
-            const int steps = base == 0 ? mine : steps_of(base + lane);
+            const int steps = steps_of(base + lane);
             sum += last_lane(lane_sums(next == 0 ? steps : base + lane < a.num_seqs ? p.of(steps) : 0));
         }
         if (next == 0) {
@@ -106,7 +116,7 @@ __device__ __forceinline__ Part find_part(const AttentionArgs &a, int id) {
                 const float x = all * __builtin_amdgcn_rcpf(among);
                 return x < 0x1p24f ? static_cast<int>(x * (1.f + 0x1p-20f)) : 1 << 24;
             };
-            low = share(static_cast<float>(a.budget));
+            low = share(static_cast<float>(shares > 0.f ? a.budget : kTurns * a.budget));
             low = low > kLeastSteps ? low : kLeastSteps;
             per = shares > 0.f ? share(shares) + 1 : low + 1;
             if (shares <= 0.f || a.num_seqs > 256) break;
@@ -122,7 +132,7 @@ __device__ __forceinline__ Part find_part(const AttentionArgs &a, int id) {
     int before = 0;
 #pragma unroll 1
     for (int base = 0; base < a.num_seqs; base += 64) {
-        const int steps = base == 0 ? mine : steps_of(base + lane);
+        const int steps = steps_of(base + lane);
         const int parts = base + lane < a.num_seqs ? p.of(steps) : 0;
         const int sum = lane_sums(parts);
         const uint64_t hit = __ballot(parts > 0 && id < before + sum);
@@ -273,6 +283,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
     constexpr int QB = MT * QF * 64 * sizeof(Frag), OB = kWaves * 4 * V::S * V::VE * 64 * sizeof(float);
     __shared__ __align__(16) char s_mem[QB > OB ? QB : OB];
     __shared__ float s_ml[kWaves][2][ROWS];
+    __shared__ int s_steps[64 * kWaves];
     Frag *const s_q = reinterpret_cast<Frag *>(s_mem);
     float *const s_o = reinterpret_cast<float *>(s_mem);
     const int lane = threadIdx.x & 63, lg = lane >> 4, li = lane & 15;
@@ -288,7 +299,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
     if (a.budget == 0) {
         if (id >= a.num_seqs) return;
     } else {
-        part = find_part<KT>(a, id);
+        part = find_part<KT>(a, id, s_steps);
         if (part.n < 0) return;
         if (part.part == 0 && h == 0 && rb == 0 && threadIdx.x == 0) {
             a.part_info[2 * part.n] = part.before;
@@ -746,7 +757,7 @@ AttentionPlan attention_plan(const gdn2_attention_dims &d) {
     const int64_t heads = d.h_k * p.row_blocks, keys = static_cast<int64_t>(d.max_pages) * d.page_size;
     p.budget = keys > static_cast<int64_t>(kWholeSteps) * step_keys(d) ? places(d, p.row_tiles) / heads : 0;
     if (p.budget == 1 && d.num_seqs >= 1) p.budget = 0;      // every sequence whole
-    p.max_parts = p.budget > d.num_seqs ? p.budget : d.num_seqs + p.budget;
+    p.max_parts = p.budget > d.num_seqs ? p.budget : d.num_seqs + kTurns * p.budget;
     return p;
 }
 

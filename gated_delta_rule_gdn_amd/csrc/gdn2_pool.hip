@@ -1,8 +1,11 @@
 // gdn2_pool.hip -- slots of pools copied: dst[i] takes the bytes of src[i] in every pool.
 //
 // Bound by memory: every byte is read once and written once, from the registers, with no staging copy
-// between. The stores are non-temporal: written through the cache, 64 pages of 16 KB in 48 pools take
-// 31.1 us and 24 states of 3.3 MB 40.8; past it 18.9 (101 MB moved, 5.3 TB/s) and 25.7 (157 MB, 6.1).
+// between. The stores are non-temporal, straight to memory: 64 pages of 16 KB in 48 pools take 18.9 us
+// (101 MB moved, 5.3 TB/s) and 24 states of 3.3 MB 25.7 (157 MB, 6.1), in place of 31.1 and 40.8 through
+// the caches. What reads a copy next finds it in memory, though: a kernel that reads all of it at once
+// takes 9 us longer behind the first, 3 behind the second. A fork's pages are read layer by layer
+// between everything else that a layer moves, which would have put them out of the caches by then.
 #include "gdn2_internal.h"
 
 namespace gdn2 {
