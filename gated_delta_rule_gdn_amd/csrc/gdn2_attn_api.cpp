@@ -64,7 +64,7 @@ bool in_place_ok(const void *in, const void *out, int64_t stride, int64_t row) {
 }
 
 size_t rotary_bwd_bytes(const gdn2_rotary_dims *d) {
-    return static_cast<size_t>(gdn2::rotary_parts(d->batch * d->seqlen)) * 2 * d->d * sizeof(float);
+    return static_cast<size_t>(gdn2::kRotaryParts) * 2 * d->d * sizeof(float);
 }
 
 // ---- attention ---------------------------------------------------------------------------

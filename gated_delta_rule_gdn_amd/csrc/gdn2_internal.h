@@ -237,14 +237,16 @@ struct RotaryArgs {
     const void *dq_out = nullptr, *dk_out = nullptr;
     void *dq = nullptr, *dk = nullptr;
     float *dq_weight = nullptr, *dk_weight = nullptr;
-    float *partial = nullptr;        // [rotary_parts()][2][d] sums of a backward call
+    float *partial = nullptr;        // [kRotaryParts][2][d] sums of a backward call
     int64_t q_stride, k_stride, v_stride = 0;
     int tokens, seqlen, h_q, h_k, d, d_rot, num_positions;
     int row_heads = 0;               // heads of a token that a wave takes at once: a power of two
     float eps, inv_d = 0.f;
     bool interleaved, bf16, grad_bf16 = false;
 };
-int rotary_parts(int tokens);                 // most rows of the partial sums: workgroups of a backward call
+// Most rows of the partial sums: workgroups of a backward call, four per CU. (Three with accesses of eight
+// values, where the fourth would wait: 8,192 tokens x 32 heads of 128 47.9 us in place of 40.9.)
+constexpr int kRotaryParts = 1024;
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st);
 hipError_t launch_rotary_bwd(const RotaryArgs &a, hipStream_t st);
 

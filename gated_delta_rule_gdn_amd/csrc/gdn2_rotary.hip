@@ -246,8 +246,8 @@ __global__ __launch_bounds__(256) void rotary_fwd_kernel(RotaryArgs a) {
     }
 }
 
-// A wave takes its tokens, then those 4 gridDim.x waves on, with all their sets of rows one after the
-// other, the next set's rows under way while one is worked on. It keeps its columns' sums of the
+// A wave takes its tokens, then those 4 gridDim.x waves on, with every gridDim.y-th set of their rows one
+// after the other, the next set's rows under way while one is worked on. It keeps its columns' sums of the
 // weights' gradients in registers; a workgroup's leave as one row of a.partial, [2][d].
 template <typename T, typename TG, int V, int L, int P, bool INTER>
 __global__ __launch_bounds__(256, 3) void rotary_bwd_kernel(RotaryArgs a) {
@@ -278,14 +278,15 @@ __global__ __launch_bounds__(256, 3) void rotary_bwd_kernel(RotaryArgs a) {
             nx.load(static_cast<const T *>(kind ? a.k : a.q) + token * (kind ? a.k_stride : a.q_stride) +
                         static_cast<int64_t>(head) * a.d, k);
     };
+    const int set0 = blockIdx.y, sets_on = gridDim.y;
     int at = first < a.tokens ? position_of(a, static_cast<int>(first)) : -1;
     load_turn<V, L, P, INTER>(a.cos_sin + static_cast<int64_t>(at) * a.d_rot, k, at >= 0, turn);
-    fetch(first, at >= 0, 0);
+    fetch(first, at >= 0, set0);
     for (int64_t base = 0; first - rows.token + base < a.tokens; base += stride) {
         const int64_t token = first + base, next = token + stride;
         const bool real = token < a.tokens;
         const int next_at = next < a.tokens ? position_of(a, static_cast<int>(next)) : -1;
-        for (int set = 0; set < rows.sets; ++set) {
+        for (int set = set0; set < rows.sets; set += sets_on) {
             const int kind = set < rows.sets_q ? 0 : 1, heads = kind ? a.h_k : a.h_q;
             const int head = (set - (kind ? rows.sets_q : 0)) * a.row_heads + rows.head;
             const bool mine = real && head < heads, used = mine && at >= 0;
@@ -293,8 +294,8 @@ __global__ __launch_bounds__(256, 3) void rotary_bwd_kernel(RotaryArgs a) {
             Pairs<V, P> g, x;
             ng.get(k, used, g);
             if (weight) nx.get(k, used, x);
-            const bool last = set + 1 == rows.sets;
-            fetch(last ? next : token, last ? next_at >= 0 : at >= 0, last ? 0 : set + 1);
+            const bool last = set + sets_on >= rows.sets;
+            fetch(last ? next : token, last ? next_at >= 0 : at >= 0, last ? set0 : set + sets_on);
             if (last) load_turn<V, L, P, INTER>(a.cos_sin + static_cast<int64_t>(next_at) * a.d_rot, k, next_at >= 0, nturn);
 #pragma unroll
             for (int i = 0; i < P; ++i)
@@ -360,25 +361,33 @@ __global__ __launch_bounds__(256, 3) void rotary_bwd_kernel(RotaryArgs a) {
         for (int n = 0; n < 2; ++n) store_pairs<float, V, L, P, INTER>(s_sum[wave] + n * a.d, k, dw[n]);
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * a.d; c += 256)
-        a.partial[static_cast<int64_t>(blockIdx.x) * 2 * a.d + c] =
+        a.partial[(static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * a.d + c] =
             (s_sum[0][c] + s_sum[1][c]) + (s_sum[2][c] + s_sum[3][c]);
 }
 
-// The weights' gradients: the rows of a.partial added in a fixed order, 32 columns per workgroup,
-// whose 32 halves of waves each take every 32nd row.
+// The weights' gradients: the rows of a.partial added in a fixed order, 16 columns per workgroup. Lane
+// l of wave w takes rows 4 w + l / 16, 64 on and so forth of column l % 16; then the four rows of a wave
+// are added by exchanges, and the 16 waves in the first one.
+constexpr int kReduceCols = 16;
 __global__ __launch_bounds__(1024) void rotary_reduce_kernel(RotaryArgs a, int parts) {
-    __shared__ float s[32][33];
-    const int lane = threadIdx.x & 31, half = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
+    __shared__ float s[16][kReduceCols];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane % kReduceCols;
+    const int col = blockIdx.x * kReduceCols + c;
     float sum = 0.f;
     if (col < 2 * a.d)
 #pragma unroll 8
-        for (int i = half; i < parts; i += 32) sum += a.partial[static_cast<int64_t>(i) * 2 * a.d + col];
-    s[half][lane] = sum;
+        for (int i = threadIdx.x / kReduceCols; i < parts; i += 64) sum += a.partial[static_cast<int64_t>(i) * 2 * a.d + col];
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (lane < kReduceCols) s[wave][c] = sum;
     __syncthreads();
-    if (half != 0 || col >= 2 * a.d) return;
+    if (wave != 0) return;
+    sum = 0.f;
 #pragma unroll
-    for (int i = 1; i < 32; ++i) sum += s[i][lane];
+    for (int i = 0; i < 4; ++i) sum += s[lane / kReduceCols * 4 + i][c];
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (lane >= kReduceCols || col >= 2 * a.d) return;
     if (col < a.d) {
         if (a.q_weight) a.dq_weight[col] = sum;
     } else if (a.k_weight) {
@@ -386,13 +395,11 @@ __global__ __launch_bounds__(1024) void rotary_reduce_kernel(RotaryArgs a, int p
     }
 }
 
-// Waves that fill the chip. A forward call of fewer gives the sets of a token's rows waves of their own
-// (64 tokens x 20 heads of 256 into pages 8.6 -> 3.9 us), and both directions put heads of several
-// tokens side by side only above that.
+// Waves that fill the chip. A call of fewer gives the sets of a token's rows to waves of their own
+// (forward: 64 tokens x 20 heads of 256 into pages 8.6 -> 3.9 us; gradients of 584 x (66 + 11) fp32
+// heads of 256 48 -> 27), and heads of
+// several tokens go side by side only above that.
 constexpr int kRotaryWaves = 4096;
-// Most workgroups of a backward call: four per CU. (Accesses of eight values: three. With four, the last
-// quarter of 8,192 tokens x 32 heads of 128 runs alone, 47.9 us in place of 40.9.)
-constexpr int kRotaryGroups = 1024;
 
 int next_pow2(int x) {
     int p = 1;
@@ -418,23 +425,24 @@ hipError_t launch(RotaryArgs a, bool backward, hipStream_t st) {
     a.inv_d = 1.f / a.d;
     const int per = 4 * (64 / L / a.row_heads);          // tokens of a workgroup
     const int groups = a.tokens / per + (a.tokens % per != 0);
+    const int sets = (a.h_q + a.row_heads - 1) / a.row_heads + (a.slots ? 2 : 1) * ((a.h_k + a.row_heads - 1) / a.row_heads);
+    auto split = [&](int n) { return n < 1 ? 1 : n < sets ? n : sets; };
     if (!backward) {
-        const int sets = (a.h_q + a.row_heads - 1) / a.row_heads + (a.slots ? 2 : 1) * ((a.h_k + a.row_heads - 1) / a.row_heads);
-        const int waves = kRotaryWaves / (4 * groups);   // of every token's
-        const unsigned gy = static_cast<unsigned>(waves < 1 ? 1 : waves < sets ? waves : sets);
         // one dimension of a grid holds less than 2^32 threads
         const unsigned gx = static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20);
+        const unsigned gy = static_cast<unsigned>(split(kRotaryWaves / (4 * groups)));
         const unsigned gz = (static_cast<unsigned>(groups) + gx - 1) / gx;
         hipLaunchKernelGGL((rotary_fwd_kernel<T, V, L, P, INTER>), dim3(gx, gy, gz), dim3(256), 0, st, a);
         return hipGetLastError();
     }
     // as many as run at once: instances of eight values per access have 161-168 registers, others 96-122
-    constexpr int AT_ONCE = V == 8 ? 3 * 256 : kRotaryGroups;
-    const int parts = groups < 1 ? 1 : groups < AT_ONCE ? groups : AT_ONCE;
-    hipLaunchKernelGGL((rotary_bwd_kernel<T, TG, V, L, P, INTER>), dim3(parts), dim3(256), 0, st, a);
+    constexpr int AT_ONCE = V == 8 ? 3 * 256 : kRotaryParts;
+    const int gx = groups < 1 ? 1 : groups < AT_ONCE ? groups : AT_ONCE, gy = split(AT_ONCE / gx);
+    hipLaunchKernelGGL((rotary_bwd_kernel<T, TG, V, L, P, INTER>), dim3(gx, gy), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !(a.q_weight || a.k_weight)) return e;
-    hipLaunchKernelGGL(rotary_reduce_kernel, dim3((2 * a.d + 31) / 32), dim3(1024), 0, st, a, parts);
+    hipLaunchKernelGGL(rotary_reduce_kernel, dim3((2 * a.d + kReduceCols - 1) / kReduceCols), dim3(1024), 0, st, a,
+                       gx * gy);
     return hipGetLastError();
 }
 
@@ -479,11 +487,6 @@ hipError_t launch_types(const RotaryArgs &a, bool backward, hipStream_t st) {
 }
 
 }  // namespace
-
-int rotary_parts(int tokens) {
-    const int groups = tokens / 4 + (tokens % 4 != 0);
-    return groups < 1 ? 1 : groups < kRotaryGroups ? groups : kRotaryGroups;
-}
 
 hipError_t launch_rotary(const RotaryArgs &a, hipStream_t st) {
     return a.bf16 ? launch_types<bf16_t, bf16_t>(a, false, st) : launch_types<float, float>(a, false, st);
