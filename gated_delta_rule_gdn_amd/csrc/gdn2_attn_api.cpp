@@ -97,7 +97,7 @@ gdn2_status check_attention(const gdn2_attention_dims *d) {
     if (!take_stride(d->q_stride, static_cast<int64_t>(d->h_q) * d->d, tokens, &s))
         return report(GDN2_ERR_BAD_SHAPE, "q_stride is smaller than a token's heads or q too large");
     const gdn2::AttentionPlan p = gdn2::attention_plan(*d);
-    if (p.max_parts > (int64_t{1} << 23) || p.max_parts * d->h_k * p.row_blocks > (int64_t{1} << 23))
+    if (p.groups > (int64_t{1} << 23))
         return report(GDN2_ERR_BAD_SHAPE, "more than 2^23 workgroups: too many sequences, heads or new tokens");
     return GDN2_OK;
 }

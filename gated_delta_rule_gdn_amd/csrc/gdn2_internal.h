@@ -273,6 +273,7 @@ struct AttentionPlan {
     int64_t row_blocks;              // workgroups that share a (sequence, key head)'s rows
     int64_t budget;                  // parts of sequences that run at once; 0: no sequence is cut
     int64_t max_parts;               // most parts that all sequences together are cut into
+    int64_t groups;                  // workgroups: a part's key heads in eights, times row_blocks
 };
 AttentionPlan attention_plan(const gdn2_attention_dims &d);
 hipError_t launch_attention(const AttentionArgs &a, const AttentionPlan &p, hipStream_t st);
@@ -285,7 +286,7 @@ struct CopyArgs {
     int32_t first_piece[kCopyPools];     // of the workgroups that copy a pair: a pool's first one
     const int32_t *src, *dst;
     int num_pools, num_slots, count;
-    int same_pieces;                 // of every pool, or 0
+    int pieces, same_pieces;         // of all pools; of each, if they have the same, or 0
 };
 hipError_t launch_pool_copy(const CopyArgs &a, hipStream_t st);
 

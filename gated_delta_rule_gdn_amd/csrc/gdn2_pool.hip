@@ -19,36 +19,38 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kCopyThreads = 128;
 constexpr int kCopyUnits = 4;        // accesses that a thread has in flight
 
-// A workgroup copies a piece of a slot, kCopyThreads * kCopyUnits accesses: piece blockIdx.x of those of
-// all pools one after the other, of every gridDim.y-th pair.
+// A workgroup copies pieces of slots, kCopyThreads * kCopyUnits accesses each: every gridDim.x-th of all
+// pools' pieces one after the other, of every gridDim.y-th pair.
 template <typename W>
 __global__ __launch_bounds__(kCopyThreads) void pool_copy_kernel(CopyArgs a) {
-    int p = 0, piece = static_cast<int>(blockIdx.x);
-    if (a.same_pieces) {
-        p = piece / a.same_pieces;
-        piece -= p * a.same_pieces;
-    } else {
-        // the last pool whose pieces begin at or before this one
-        const int lane = threadIdx.x & 63;
-        const int begin = lane < a.num_pools ? a.first_piece[lane] : INT32_MAX;
-        p = __popcll(__ballot(begin <= piece)) - 1;
-        piece -= a.first_piece[p];
-    }
-    char *pool = static_cast<char *>(a.pool[p]);
-    const int64_t units = a.bytes[p] / static_cast<int64_t>(sizeof(W));
-    const int64_t first = static_cast<int64_t>(piece) * kCopyThreads * kCopyUnits + threadIdx.x;
-    for (int i = blockIdx.y; i < a.count; i += gridDim.y) {
-        const int from = a.src[i], to = a.dst[i];
-        if (from < 0 || from >= a.num_slots || to < 0 || to >= a.num_slots || from == to) continue;
-        const W *s = reinterpret_cast<const W *>(pool) + from * units;
-        W *t = reinterpret_cast<W *>(pool) + to * units;
-        W x[kCopyUnits];
+    for (int id = static_cast<int>(blockIdx.x); id < a.pieces; id += gridDim.x) {
+        int p, piece;
+        if (a.same_pieces) {
+            p = id / a.same_pieces;
+            piece = id - p * a.same_pieces;
+        } else {
+            // the last pool whose pieces begin at or before this one
+            const int lane = threadIdx.x & 63;
+            const int begin = lane < a.num_pools ? a.first_piece[lane] : INT32_MAX;
+            p = __popcll(__ballot(begin <= id)) - 1;
+            piece = id - a.first_piece[p];
+        }
+        char *pool = static_cast<char *>(a.pool[p]);
+        const int64_t units = a.bytes[p] / static_cast<int64_t>(sizeof(W));
+        const int64_t first = static_cast<int64_t>(piece) * kCopyThreads * kCopyUnits + threadIdx.x;
+        for (int i = blockIdx.y; i < a.count; i += gridDim.y) {
+            const int from = a.src[i], to = a.dst[i];
+            if (from < 0 || from >= a.num_slots || to < 0 || to >= a.num_slots || from == to) continue;
+            const W *s = reinterpret_cast<const W *>(pool) + from * units;
+            W *t = reinterpret_cast<W *>(pool) + to * units;
+            W x[kCopyUnits];
 #pragma unroll
-        for (int u = 0; u < kCopyUnits; ++u)
-            if (first + u * kCopyThreads < units) x[u] = s[first + u * kCopyThreads];
+            for (int u = 0; u < kCopyUnits; ++u)
+                if (first + u * kCopyThreads < units) x[u] = s[first + u * kCopyThreads];
 #pragma unroll
-        for (int u = 0; u < kCopyUnits; ++u)
-            if (first + u * kCopyThreads < units) __builtin_nontemporal_store(x[u], t + first + u * kCopyThreads);
+            for (int u = 0; u < kCopyUnits; ++u)
+                if (first + u * kCopyThreads < units) __builtin_nontemporal_store(x[u], t + first + u * kCopyThreads);
+        }
     }
 }
 
@@ -63,8 +65,11 @@ hipError_t launch(CopyArgs a, hipStream_t st) {
         a.first_piece[p] = static_cast<int>(pieces);
         pieces += n;
     }
-    const unsigned rows = static_cast<unsigned>(a.count < 32768 ? a.count : 32768);
-    hipLaunchKernelGGL((pool_copy_kernel<W>), dim3(static_cast<unsigned>(pieces), rows), dim3(kCopyThreads), 0, st, a);
+    a.pieces = static_cast<int>(pieces);       // 64 slots of 2^32 bytes, one by one: 2^29
+    // one dimension of a grid holds less than 2^32 threads
+    const unsigned gx = static_cast<unsigned>(pieces < (1 << 20) ? pieces : 1 << 20);
+    const unsigned gy = static_cast<unsigned>(a.count < 32768 ? a.count : 32768);
+    hipLaunchKernelGGL((pool_copy_kernel<W>), dim3(gx, gy), dim3(kCopyThreads), 0, st, a);
     return hipGetLastError();
 }
 

@@ -802,7 +802,8 @@ size_t gdn2_paged_attention_step_workspace_bytes(const gdn2_attention_dims *dims
  *                [0, max_pages * page_size]
  *   o            device [N, T, h_q, d], contiguous, 16-byte aligned
  *   lse          device fp32 [N, T, h_q], or NULL
- *   workspace    at least gdn2_paged_attention_step_workspace_bytes() bytes, 256-byte aligned
+ *   workspace    at least gdn2_paged_attention_step_workspace_bytes() bytes, 256-byte aligned; nothing
+ *                is kept in it from one call to the next, but two calls at once need one each
  */
 gdn2_status gdn2_paged_attention_step(const void *q, const void *k_pages, const void *v_pages,
                                       const int32_t *page_table, const int32_t *seq_lens, void *o,

@@ -135,6 +135,8 @@ def test_attention_refusals(L):
     assert attn(L, h_q=1 << 14) == SHAPE
     assert attn(L, num_seqs=1 << 20, new_tokens=1 << 11) == SHAPE
     assert attn(L, num_seqs=1 << 23) == SHAPE                        # workgroups
+    assert attn(L, num_seqs=1, new_tokens=1 << 26, h_q=1, h_k=1) == SHAPE
+    assert attn(L, num_seqs=1, new_tokens=1 << 20, h_q=16, h_k=1) == SHAPE
     assert attn(L, num_pages=-1) == SHAPE and attn(L, page_size=0) == SHAPE and attn(L, max_pages=-1) == SHAPE
     assert attn(L, num_pages=1 << 26) == SHAPE                       # 2^31 rows
     assert attn(L, page_size=(1 << 31) - 1) == SHAPE

@@ -86,6 +86,17 @@ def test_slots_beyond_four_gigabytes():
     assert torch.equal(pool[3], pool[4]) and not pool[:3].any()
 
 
+def test_more_pieces_than_a_grid_dimension_takes():
+    """A slot of 2^20 workgroups and a few, byte by byte, in a pool beside a small one."""
+    n = (1 << 29) + 1539
+    pool = torch.zeros(2, n, dtype=torch.uint8, device="cuda")
+    pool[0, :1000], pool[0, -1000:], pool[0, 1 << 28] = 3, 5, 7
+    small = torch.tensor([[1, 2, 3], [4, 5, 6]], dtype=torch.uint8, device="cuda")
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    g.pool_copy([pool, small], i(0), i(1))
+    assert torch.equal(pool[1], pool[0]) and torch.equal(small[1], small[0])
+
+
 def test_nothing_to_do():
     gen = torch.Generator().manual_seed(6)
     pool = bytes_of(gen, 3, 16)

@@ -234,6 +234,27 @@ def test_append_to_pages(page, d, hk, dtype):
     assert torch.equal(got, q) and torch.equal(kp, want[0]) and torch.equal(vp, want[1])
 
 
+def test_append_in_place_of_dense_prompts():
+    """Three prompts of 11 tokens, q in place; keys and values of a padded batch's end are left out."""
+    v = make(17, 3, 11, 4, 2, 64, 64, BF16)
+    q, k = v["q"].contiguous(), v["k"].contiguous()
+    kp = torch.zeros(9, 2, 8, 64, dtype=BF16, device="cuda")
+    vp = torch.zeros_like(kp)
+    slots = torch.arange(33, dtype=torch.int32).view(3, 11)
+    slots[1, 8:] = -1
+    want_q, want_k = g.qk_rotary_fwd(q, k, v["cs"], v["pos"], v["qw"], v["kw"], eps=EPS)
+    got = g.qk_rotary_append(q, k, v["v"], v["cs"], v["pos"], kp, vp, slots.cuda(), v["qw"], v["kw"], eps=EPS, q_out=q)
+    assert got is q and torch.equal(q, want_q)
+    for pool, src in ((kp, want_k), (vp, v["v"])):
+        rows = pool.transpose(1, 2).flatten(0, 1)
+        for b in range(3):
+            for t in range(11):
+                s = int(slots[b, t])
+                if s >= 0:
+                    assert torch.equal(rows[s], src[b, t])
+        assert not rows[33:].any() and not rows[19:22].any()
+
+
 def test_append_far_into_a_large_pool():
     """Places whose elements lie beyond 2^32."""
     pages, hk, page, d = 1100, 16, 1024, 256          # 4.6e9 values of bf16, 9.2 GB
