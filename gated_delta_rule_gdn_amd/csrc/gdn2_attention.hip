@@ -424,8 +424,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-            {
+            for (int i = 0; i < 4; ++i) {
                 const float less = sizeof(T) == 4 ? fmaf(s[mt][t][i], to2_rest, -at) : -at;
                 s[mt][t][i] = seen(t, i) ? __builtin_amdgcn_exp2f(fmaf(s[mt][t][i], to2, less)) : 0.f;
             }
@@ -757,6 +756,12 @@ AttentionPlan attention_plan(const gdn2_attention_dims &d) {
     p.row_blocks = row_blocks(rows);
     const int64_t heads = d.h_k * p.row_blocks, keys = static_cast<int64_t>(d.max_pages) * d.page_size;
     p.budget = keys > static_cast<int64_t>(kWholeSteps) * step_keys(d) ? places(d, p.row_tiles) / heads : 0;
+    // Two tiles of rows: the sums of a part are so large (32 KB at 256 values, for 256 KB of keys and
+    // values where the chip is just filled) that one workgroup per CU does better, as long as that
+    // leaves four parts per sequence (32 sequences x 4 new tokens, 65,536 keys of 2 x 8 heads of 256:
+    // 43.4 -> 40.3 us, one of 200,000 97 -> 91; with two per sequence, 64 of 200,000 together 101 -> 105).
+    if (p.budget > 0 && p.row_tiles == 2 && kSimds / 4 / heads >= 4 * static_cast<int64_t>(d.num_seqs))
+        p.budget = kSimds / 4 / heads;
     if (p.budget == 1 && d.num_seqs >= 1) p.budget = 0;      // every sequence whole
     p.max_parts = p.budget > d.num_seqs ? p.budget : d.num_seqs + kTurns * p.budget;
     p.groups = (p.max_parts * d.h_k + 7) / 8 * 8 * p.row_blocks;
