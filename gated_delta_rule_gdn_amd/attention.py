@@ -299,6 +299,7 @@ def paged_attention_step(q, k_pages, v_pages, page_table, seq_lens, scale: Optio
 
 def paged_attention_step_workspace_bytes(num_seqs: int, new_tokens: int, h_q: int, h_k: int, d: int,
                                          page_size: int, max_pages: int, dtype: torch.dtype) -> int:
+    """Bytes that are enough for these sizes with any window, and with fewer sequences."""
     n = AttentionDims(num_seqs, new_tokens, h_q, h_k, d, 0, page_size, max_pages, 0,
                       _dtype_code(dtype), 1.0, 0)
     return int(lib().gdn2_paged_attention_step_workspace_bytes(ctypes.byref(n)))

@@ -25,9 +25,13 @@ namespace {
 
 constexpr int kWaves = 4;           // of a workgroup: as many as an output tile has rows in a lane
 
-// Steps (a tile per wave) of a call that is never cut, and of the shortest part that a sequence is cut
-// into.
+// Steps (a tile per wave) of a call that is never cut, of one with a window, whose sequences are about
+// as long as each other, that is not if every CU has a sequence then, and of the shortest part that a
+// sequence is cut into. The second launch takes 4 us, a step 1 to 2. (64 sequences, 4 key heads of 128, a
+// window of 512 keys: 15 us whole, 22 cut; of 1,024 24.4 and 28.7; 1,500 32.1 and 37.3; two sequences of
+// 768 14.2 and 11.3.)
 constexpr int kWholeSteps = 4;
+constexpr int kWindowSteps = 12;
 constexpr int kLeastSteps = 1;
 // Shares of all steps, in parts that run at once, that a part is held to where sequences outnumber those
 // (256 sequences of 32,768 tokens together, 8 key heads of 128: 44.8 us with 2, 47.8 with 1, 56.4 with 8;
@@ -755,7 +759,15 @@ AttentionPlan attention_plan(const gdn2_attention_dims &d) {
     p.row_tiles = row_tiles(rows);
     p.row_blocks = row_blocks(rows);
     const int64_t heads = d.h_k * p.row_blocks, keys = static_cast<int64_t>(d.max_pages) * d.page_size;
-    p.budget = keys > static_cast<int64_t>(kWholeSteps) * step_keys(d) ? places(d, p.row_tiles) / heads : 0;
+    const int64_t seen = static_cast<int64_t>(d.window) + d.new_tokens - 1;
+    const bool short_window = d.window > 0 && seen < keys;
+    int whole = kWholeSteps;
+    // Steps of 3 us: fp32 of 256 values, and two tiles of rows of them in pages that are not whole sixteens
+    // (32 sequences x 2 key heads, a window of 200: 23 us cut, 26 whole; 1 x 7, 7 new tokens, 248: 18, 23).
+    if (d.d == 256 && (d.dtype == GDN2_F32 || (p.row_tiles == 2 && d.page_size % 16 != 0))) whole /= 2;
+    if (short_window && d.num_seqs * heads >= kSimds / 4) whole = kWindowSteps;
+    const bool cut = (short_window ? seen : keys) > static_cast<int64_t>(whole) * step_keys(d);
+    p.budget = cut ? places(d, p.row_tiles) / heads : 0;
     // Two tiles of rows: the sums of a part are so large (32 KB at 256 values, for 256 KB of keys and
     // values where the chip is just filled) that one workgroup per CU does better, as long as that
     // leaves four parts per sequence (32 sequences x 4 new tokens, 65,536 keys of 2 x 8 heads of 256:

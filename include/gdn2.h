@@ -782,7 +782,8 @@ typedef struct gdn2_attention_dims {
 
 /*
  * Bytes of device workspace gdn2_paged_attention_step needs for these dims (0 too where it needs
- * none, and if the dims are invalid). They do not depend on the lengths.
+ * none, and if the dims are invalid). They do not depend on the lengths. With window = 0 they grow with
+ * num_seqs and are enough for any window; with a window more sequences may need less than fewer.
  */
 size_t gdn2_paged_attention_step_workspace_bytes(const gdn2_attention_dims *dims);
 

@@ -168,6 +168,22 @@ def test_attention_workspace(L):
     assert g.paged_attention_step_workspace_bytes(4, 1, 8, 2, 128, 16, 200, torch.bfloat16) == need
 
 
+def test_attention_workspace_of_any_call(L):
+    """The size without a window is enough for any window and for fewer sequences."""
+    size = lambda **kw: L.gdn2_paged_attention_step_workspace_bytes(dims(AttentionDims, ATTN, **kw))  # noqa: E731
+    for d in (64, 128, 256):
+        for dtype in (0, 1):
+            for T in (1, 4, 40):
+                last = 0
+                for n in (1, 2, 7, 31, 32, 33, 64, 100, 128, 129, 300, 1000, 5000):
+                    whole = size(num_seqs=n, new_tokens=T, d=d, dtype=dtype)
+                    assert whole >= last > -1
+                    last = whole
+                    for w in (1, 64, 250, 500, 1000, 2000, 100000):
+                        assert size(num_seqs=n, new_tokens=T, d=d, dtype=dtype, window=w) <= whole
+    assert size(num_seqs=200, h_q=8, h_k=4, window=1000) == 0 < size(num_seqs=2, h_q=8, h_k=4, window=1000)
+
+
 def copy(L, pools=(0x1000, 0x2000), sizes=(64, 64), slots=10, src=P(8), dst=P(9), count=4, n=None):
     n = len(pools) if n is None else n
     return L.gdn2_pool_copy((ctypes.c_void_p * len(pools))(*pools), (ctypes.c_int64 * len(sizes))(*sizes), n, slots,

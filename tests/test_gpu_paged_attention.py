@@ -102,6 +102,22 @@ def test_windows(window, T, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,d,page", [(1, 64, 16), (3, 128, 24)])
+@pytest.mark.parametrize("N,window", [(31, 500), (32, 500), (33, 150), (40, 1200), (40, 2500)])
+def test_windows_of_sequences_for_every_cu(N, window, T, d, page, dtype):
+    """Where every CU has a sequence and the window is short, no sequence is cut; next to that, and
+    behind a longer window, they are."""
+    rng = np.random.default_rng(N + window)
+    lens = [int(n) for n in rng.integers(0, 1700, N - 3)] + [window, window + T, 2600]
+    x = make(window + T + N, lens, T, 8, 1, d, page, dtype)
+    compare(x, window=window, only=[0, 7, 19, N - 3, N - 2, N - 1])
+    for i in (3, 11, N - 1):                    # alone they are cut
+        y = {**x, "q": x["q"][i:i + 1], "table": x["table"][i:i + 1], "lens": x["lens"][i:i + 1],
+             "k": x["k"][i:i + 1], "v": x["v"][i:i + 1]}
+        compare(y, window=window)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_window_leaves_pages_behind(dtype):
     """Pages that lie before the window may be given away: their entries point nowhere, or at pages
     full of NaN."""
