@@ -195,6 +195,23 @@ def test_values_that_are_not_finite_stay_with_the_tokens_that_see_them(bad, dtyp
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32), (128, 24), (256, 16)])
+@pytest.mark.parametrize("N", [1, 34])
+def test_a_value_that_is_not_finite_at_the_beginning_of_a_window(N, d, page, dtype):
+    """Seen by token 0 of 3 alone, with several tiles behind it: the other tokens have the bits they had."""
+    window = 700
+    x = make(d + N, [1450] * N, 3, 8, 1, d, page, dtype)
+    want = call(x, window=window)
+    y = dict(x, vp=x["vp"].clone())
+    at = 1450 - 3 - window + 1
+    y["vp"][x["table"][N - 1, at // page], 3, at % page, d - 1] = float("nan")
+    o, lse = call(y, window=window)
+    assert torch.isnan(o[N - 1, 0, 3, d - 1])
+    o[N - 1, 0, 3, d - 1] = want[0][N - 1, 0, 3, d - 1]
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_large_and_small_scores(dtype):
     """Scores of hundreds (one key takes all), differences far below the type's range, scales of zero
     and below."""
