@@ -792,11 +792,15 @@ AttentionPlan attention_plan(const gdn2_attention_dims &d) {
     if (short_window && d.num_seqs * heads >= kSimds / 4) whole = kWindowSteps;
     const bool cut = (short_window ? seen : keys) > static_cast<int64_t>(whole) * step_keys(d);
     p.budget = cut ? places(d, p.row_tiles) / heads : 0;
-    // Two tiles of rows: the sums of a part are so large (32 KB at 256 values, for 256 KB of keys and
-    // values where the chip is just filled) that one workgroup per CU does better, as long as that
+    // Two tiles of rows in bf16: the sums of a part are so large (32 KB at 256 values, for 256 KB of keys
+    // and values where the chip is just filled) that one workgroup per CU does better, as long as that
     // leaves four parts per sequence (32 sequences x 4 new tokens, 65,536 keys of 2 x 8 heads of 256:
-    // 43.4 -> 40.3 us, one of 200,000 97 -> 91; with two per sequence, 64 of 200,000 together 101 -> 105).
-    if (p.budget > 0 && p.row_tiles == 2 && kSimds / 4 / heads >= 4 * static_cast<int64_t>(d.num_seqs))
+    // 42.3 -> 40.3 us, one of 200,000 97 -> 91; with two per sequence, 64 of 200,000 together 101 -> 105).
+    // It does worse where its one wave per SIMD is busy rather than waiting: workgroups that share keys
+    // (32 x 8 new tokens, 200,000 keys of 4 x 8 heads of 128: 112 -> 126), 64 values (42 -> 45), fp32
+    // (32 x 8 new tokens, 4 x 8 heads of 128: 109 -> 120).
+    if (p.budget > 0 && p.row_tiles == 2 && p.row_blocks == 1 && d.dtype == GDN2_BF16 && d.d > 64 &&
+        kSimds / 4 / heads >= 4 * static_cast<int64_t>(d.num_seqs))
         p.budget = kSimds / 4 / heads;
     if (p.budget == 1 && d.num_seqs >= 1) p.budget = 0;      // every sequence whole
     p.max_parts = p.budget > d.num_seqs ? p.budget : d.num_seqs + kTurns * p.budget;
