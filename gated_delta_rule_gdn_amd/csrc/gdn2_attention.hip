@@ -288,7 +288,10 @@ template <int D> struct VRows<float, D> {
     }
 };
 
-template <typename T, int D, int MT>
+// PB: 8 for pages of whole eights that are not of whole sixteens, 16 for those and any others. (Pages of 8,
+// 32 sequences x 4 new tokens, 65,536 keys of 2 x 8 heads of 256: 44 us, as any others 58; 16 sequences
+// of 65,536, 4 key heads of 256 in fp32: 115 and 182.)
+template <typename T, int D, int MT, int PB>
 __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void paged_attention_kernel(AttentionArgs a, int row_blocks) {
     using Op = Ops<T>;
     using V = VRows<T, D>;
@@ -465,26 +468,35 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
                 for (int mt = 0; mt < MT; ++mt) o[mt][c][j] = v.pv(c, j, pb[mt], o[mt][c][j]);
     };
 
-    // Pages of whole sixteens: each 16 keys lie in one page, so their rows are the same for all lanes but
-    // for a fixed offset. A sixteen outside [lo, hi) (a tile has one inside) is that one instead.
-    const int k_at = li * D + lg * LV, v_at = 4 * lg * D + li * V::VE;
-    uint32_t row[ST];
-    auto find_rows = [&](int tile, uint32_t (&to)[ST]) {
+    // Pages of whole PB: each PB keys lie in one page, so their rows follow the first, whose row is the same
+    // for all lanes. PB keys outside [lo, hi) (a tile has some inside) are the nearest ones inside instead.
+    constexpr int NB = KT / PB, OF = 16 / PB;            // blocks of a tile, and of sixteen keys
+    const int k_at = li % PB * D + lg * LV, v_at = 4 * lg % PB * D + li * V::VE;
+    uint32_t row[NB];
+    auto find_rows = [&](int tile, uint32_t (&to)[NB]) {
 #pragma unroll
-        for (int t = 0; t < ST; ++t) to[t] = __builtin_amdgcn_readfirstlane(pool_row(ST == 1 ? tile : t == 0 ? max(tile, lo & ~15) : min(tile + 16, (hi - 1) & ~15)));
+        for (int b = 0; b < NB; ++b) {
+            int at = tile + PB * b;
+            if (b > 0) at = min(at, (hi - 1) / PB * PB);
+            if (b + 1 < NB) at = max(at, lo / PB * PB);
+            to[b] = __builtin_amdgcn_readfirstlane(pool_row(at));
+        }
     };
     auto load_keys = [&]() {
 #pragma unroll
         for (int t = 0; t < ST; ++t) {
-            const T *p = kp + static_cast<int64_t>(row[t]) * D;
+            const uint32_t mine = li < PB ? row[OF * t] : row[OF * t + OF - 1];
+            const T *p = kp + static_cast<int64_t>(mine) * D;
 #pragma unroll
             for (int f = 0; f < QF; ++f) k[t][f] = *reinterpret_cast<const Frag *>(p + k_at + f * Op::QW);
         }
     };
     auto load_values = [&]() {
 #pragma unroll
-        for (int r = 0; r < V::VR; ++r)
-            v.load(r, vp + static_cast<int64_t>(row[r / 4]) * D + v_at + r % 4 * D, 0);
+        for (int r = 0; r < V::VR; ++r) {
+            const uint32_t mine = 4 * lg < PB ? row[OF * (r / 4)] : row[OF * (r / 4) + OF - 1];
+            v.load(r, vp + static_cast<int64_t>(mine) * D + v_at + r % 4 * D, 0);
+        }
     };
     // Other pages. Keys outside [lo, hi) take the nearest one inside, which is read instead and masked.
     auto edge = [&](int tile) {
@@ -541,7 +553,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
     constexpr int NEXT = kWaves * KT;
     const int first = lo < hi ? lo / KT * KT + wave * KT : hi;
     const int full_lo = max(lo, lo_all), full_hi = min(hi, hi_all);
-    const int piped = a.page_size % 16 == 0 ? hi : first;
+    const int piped = a.page_size % PB == 0 ? hi : first;
     if (first < piped) {
         find_rows(first, row);
         load_keys();
@@ -557,7 +569,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
     // tokens together, now 7.9; 32 x 4 new tokens with a window 42 and 40.5).
     int tile = first;
     for (; tile < piped; tile += NEXT) {
-        uint32_t ahead[ST];
+        uint32_t ahead[NB];
         find_rows(tile + NEXT < hi ? tile + NEXT : tile, ahead);
         load_values();
         __builtin_amdgcn_sched_barrier(0);
@@ -572,7 +584,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
             if (t0 < t1 && !__all(v.finite())) break;      // it and what follows: as other pages
         }
 #pragma unroll
-        for (int t = 0; t < ST; ++t) row[t] = ahead[t];
+        for (int b = 0; b < NB; ++b) row[b] = ahead[b];
         load_keys();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -732,8 +744,9 @@ constexpr int kJoinRows = 2048;      // most rows that take a workgroup each
 template <typename T, int D, int MT>
 hipError_t launch(const AttentionArgs &a, const AttentionPlan &p, hipStream_t st) {
     const int blocks_of_rows = static_cast<int>(p.row_blocks);
-    hipLaunchKernelGGL((paged_attention_kernel<T, D, MT>), dim3(static_cast<unsigned>(p.groups)), dim3(64 * kWaves), 0, st,
-                       a, blocks_of_rows);
+    const dim3 groups(static_cast<unsigned>(p.groups)), threads(64 * kWaves);
+    if (a.page_size % 16 == 8) hipLaunchKernelGGL((paged_attention_kernel<T, D, MT, 8>), groups, threads, 0, st, a, blocks_of_rows);
+    else hipLaunchKernelGGL((paged_attention_kernel<T, D, MT, 16>), groups, threads, 0, st, a, blocks_of_rows);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.budget == 0) return e;
     const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.new_tokens * a.h_q;
@@ -786,9 +799,10 @@ AttentionPlan attention_plan(const gdn2_attention_dims &d) {
     const int64_t seen = static_cast<int64_t>(d.window) + d.new_tokens - 1;
     const bool short_window = d.window > 0 && seen < keys;
     int whole = kWholeSteps;
-    // Steps of 3 us: fp32 of 256 values, and two tiles of rows of them in pages that are not whole sixteens
-    // (32 sequences x 2 key heads, a window of 200: 23 us cut, 26 whole; 1 x 7, 7 new tokens, 248: 18, 23).
-    if (d.d == 256 && (d.dtype == GDN2_F32 || (p.row_tiles == 2 && d.page_size % 16 != 0))) whole /= 2;
+    // Steps of 3 us: fp32 of 256 values, and two tiles of rows of them in pages whose rows are looked up
+    // lane by lane (32 sequences x 2 key heads, a window of 200: 23 us cut, 26 whole; 1 x 7, 7 new tokens,
+    // 248: 18, 23).
+    if (d.d == 256 && (d.dtype == GDN2_F32 || (p.row_tiles == 2 && d.page_size % 8 != 0))) whole /= 2;
     if (short_window && d.num_seqs * heads >= kSimds / 4) whole = kWindowSteps;
     const bool cut = (short_window ? seen : keys) > static_cast<int64_t>(whole) * step_keys(d);
     p.budget = cut ? places(d, p.row_tiles) / heads : 0;

@@ -80,6 +80,16 @@ def test_page_sizes(page, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T,window", [(1, 0), (1, 37), (3, 0), (3, 150)])
+@pytest.mark.parametrize("page", [4, 8, 12, 24, 40])
+def test_pages_that_end_inside_a_tile(page, T, window, d, dtype):
+    """Every other number of eights, and none: ends and windows that begin at every place of a page."""
+    lens = [T - 1, page, 2 * page + 1, 130, 131, 135, 137, 141, 144, 500, 1029]
+    compare(make(page * d + T, lens, T, 1, 8, d, page, dtype), window=window)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("hk,G", [(1, 1), (3, 1), (2, 8), (1, 16), (1, 17), (2, 32), (1, 40), (5, 2)])
 def test_heads(hk, G, dtype):
     compare(make(hk * 50 + G, [130, 40, 601], 1, hk, G, 128, 32, dtype))
