@@ -261,7 +261,7 @@ def paged_attention_step(q, k_pages, v_pages, page_table, seq_lens, scale: Optio
     Token t stands at place seq_lens[n] - T + t and sees the places up to its own, with a window > 0
     the last `window` of them. scale: of the products (None: d^-1/2). Returns o [N,T,h_q,d], or
     (o, lse fp32 [N,T,h_q]) with return_lse: lse = log sum exp of a row's scaled products. A token
-    that sees nothing gives zeros, and an lse of -inf."""
+    that sees nothing, or nothing but products of -inf, gives zeros, and an lse of -inf."""
     dev, dtype = _gpu_of("q", q), q.dtype
     if q.dim() != 4:
         raise ValueError("q must be [N,T,h_q,d]")

@@ -4,7 +4,11 @@
 // token r / G. For a row at place p and the keys j that it sees,
 //     o = sum_j e^(s_j - m) v_j / l,   m = max_j s_j,   l = sum_j e^(s_j - m),   s_j = scale q . k_j
 // in one pass over the keys: m, l and the unnormalised o are kept and rescaled when m grows, and
-// parts of a sequence (m, l, o) join the same way. Exponentials are taken to base 2.
+// parts of a sequence (m, l, o) join the same way. Exponentials are taken to base 2, of differences of
+// the products as they are (m is one of them): (q . k_j - m) times to_base2 is 0 for the largest and -inf
+// for a product of -inf, whatever their size, and off by its own roundings only. (A scaled product less a
+// rounded scaled maximum is off by the rounding of the larger one: 2^100 at the lowest value of bf16.) For
+// a scale below 0 the queries change their sign, so that the largest product has the largest weight.
 //
 // Bound by memory: every key and value is read once for all rows of its head. Each of the two
 // products is made on the matrix cores, 16 rows at a time, with the cache in registers only:
@@ -49,6 +53,16 @@ __device__ __forceinline__ int lane_sums(int x) {
     return x;
 }
 __device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, 63); }
+
+// The factor of differences of products: |scale| log2 e, but held inside the range of fp32, so that neither
+// 0 nor -inf makes NaN with it. (A scale of 0 gives weights that are equal to 1e-6 at least.)
+__device__ __forceinline__ float to_base2(const AttentionArgs &a) {
+    return fminf(fmaxf(fabsf(a.scale) * kLog2e, 0x1p-149f), 0x1.fffffep127f);
+}
+// The log-sum-exp of a row whose largest product is `top`.
+__device__ __forceinline__ float row_lse(const AttentionArgs &a, float top, float sum) {
+    return sum == 0.f ? -INFINITY : fmaf(top, fabsf(a.scale), log2f(sum) * (1.f / kLog2e));
+}
 
 __device__ __forceinline__ int seq_len(const AttentionArgs &a, int n) {
     const int most = a.max_pages * a.page_size, len = a.seq_lens[n];
@@ -186,6 +200,7 @@ template <> struct Ops<bf16_t> {
     typedef u32x4 Frag;                          // 8 values of a q or k row
     static constexpr int CHAINS = 1;
     static __device__ __forceinline__ void qk(Frag k, Frag q, f32x4 (&c)[1]) { c[0] = mma_k32(k, q, c[0]); }
+    static __device__ __forceinline__ Frag turned(Frag f) { return f ^ 0x80008000u; }
     static __device__ __forceinline__ Frag each(const bf16_t *p) {      // value by value
         Frag f;
 #pragma unroll
@@ -201,6 +216,7 @@ template <> struct Ops<float> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(k[i], q[i], c[i], 0, 0, 0);
     }
+    static __device__ __forceinline__ Frag turned(Frag f) { return -f; }
     static __device__ __forceinline__ Frag each(const float *p) { return Frag{p[0], p[1], p[2], p[3]}; }
 };
 
@@ -367,6 +383,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
                      (static_cast<int64_t>(part.n) * a.new_tokens + t) * a.q_stride +
                      static_cast<int64_t>(h * G + (r < R ? r : R - 1) - t * G) * D + f % QF * Op::QW + lg * LV;
         q[i] = a.q_whole ? *reinterpret_cast<const Frag *>(p) : Op::each(p);
+        if (a.scale < 0.f) q[i] = Op::turned(q[i]);
     }
 
     f32x4 o[MT][V::S][V::VE];
@@ -391,9 +408,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
         id = id > 0 ? id : 0;
         return static_cast<uint32_t>((id * a.h_k + h) * a.page_size + (j - pg * a.page_size));
     };
-    // scale log2 e, and what fp32 leaves off it: it is multiplied with differences of up to hundreds
-    const float to2 = a.scale * kLog2e;
-    const float to2_rest = fmaf(a.scale, kLog2e, -to2) + a.scale * 1.92596303e-8f;
+    const float to2 = to_base2(a);
     Frag k[ST][QF];
     V v;
     f32x4 s[MT][ST];
@@ -425,28 +440,26 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
                 s[mt][t] = CH == 1 ? part[mt][t][0]
                                    : (part[mt][t][0] + part[mt][t][1 % CH]) + (part[mt][t][2 % CH] + part[mt][t][3 % CH]);
     };
-    // Of a tile's products, those that seen(t, i) says. A weight's exponent is one fused operation (in
-    // fp32 with the rest of the factor before it), so that it is off by its own rounding, not by that of
-    // the larger product.
+    // Of a tile's products, those that seen(t, i) says.
     auto softmax = [&](int mt, auto &&seen) {
         float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, seen(t, i) ? s[mt][t][i] * to2 : -INFINITY);
+            for (int i = 0; i < 4; ++i) {
+                s[mt][t][i] = seen(t, i) ? s[mt][t][i] : -INFINITY;
+                top = fmaxf(top, s[mt][t][i]);
+            }
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         top = fmaxf(top, m[mt]);
         const float at = top == -INFINITY ? 0.f : top;      // nothing seen so far: all weights 0
-        const float keep = __builtin_amdgcn_exp2f(m[mt] - at);
+        const float keep = __builtin_amdgcn_exp2f((m[mt] - at) * to2);
         m[mt] = top;
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float less = sizeof(T) == 4 ? fmaf(s[mt][t][i], to2_rest, -at) : -at;
-                s[mt][t][i] = seen(t, i) ? __builtin_amdgcn_exp2f(fmaf(s[mt][t][i], to2, less)) : 0.f;
-            }
+            for (int i = 0; i < 4; ++i) s[mt][t][i] = __builtin_amdgcn_exp2f((s[mt][t][i] - at) * to2);
         l[mt] *= keep;
 #pragma unroll
         for (int t = 0; t < ST; ++t) l[mt] += (s[mt][t].x + s[mt][t].y) + (s[mt][t].z + s[mt][t].w);
@@ -618,8 +631,8 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
         const float at = top == -INFINITY ? 0.f : top;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
-            sum += s_ml[w][1][mt * 16 + li] * __builtin_amdgcn_exp2f(s_ml[w][0][mt * 16 + li] - at);
-        const float keep = __builtin_amdgcn_exp2f(m[mt] - at);
+            sum += s_ml[w][1][mt * 16 + li] * __builtin_amdgcn_exp2f((s_ml[w][0][mt * 16 + li] - at) * to2);
+        const float keep = __builtin_amdgcn_exp2f((m[mt] - at) * to2);
 #pragma unroll
         for (int c = 0; c < V::S; ++c)
 #pragma unroll
@@ -651,7 +664,7 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
         }
         if (r < R && lg == 0 && wave == 0) {
             if (cut) *reinterpret_cast<float2 *>(a.part_ml + 2 * part_at) = float2{top, sum};
-            else if (a.lse) a.lse[row_at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * (1.f / kLog2e);
+            else if (a.lse) a.lse[row_at] = row_lse(a, top, sum);
         }
     }
 }
@@ -665,6 +678,7 @@ __global__ __launch_bounds__(256) void paged_attention_join_kernel(AttentionArgs
     __shared__ f32x4 s_o[PER][JW][LANES];
     __shared__ float2 s_ml[PER][JW];
     const int G = a.h_q / a.h_k, heads = a.h_k * row_blocks;
+    const float to2 = to_base2(a);
     const int slot = threadIdx.x / THREADS, thread = threadIdx.x % THREADS;
     const int64_t at = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * PER + slot;
     const bool mine = at < static_cast<int64_t>(a.num_seqs) * a.new_tokens * a.h_q;
@@ -700,13 +714,13 @@ __global__ __launch_bounds__(256) void paged_attention_join_kernel(AttentionArgs
                 if (p + u * JW >= parts) ml[u].x = -INFINITY;
                 high = fmaxf(high, ml[u].x);
             }
-            const float ref = high == -INFINITY ? 0.f : high, keep = __builtin_amdgcn_exp2f(top - ref);
+            const float ref = high == -INFINITY ? 0.f : high, keep = __builtin_amdgcn_exp2f((top - ref) * to2);
             top = high;
             l *= keep;
             o *= keep;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float w = __builtin_amdgcn_exp2f(ml[u].x - ref);
+                const float w = __builtin_amdgcn_exp2f((ml[u].x - ref) * to2);
                 l = fmaf(w, ml[u].y, l);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = fmaf(w, x[u][e], o[e]);
@@ -721,13 +735,13 @@ __global__ __launch_bounds__(256) void paged_attention_join_kernel(AttentionArgs
         float high = top;
 #pragma unroll
         for (int x = 1; x < JW; ++x) high = fmaxf(high, s_ml[slot][x].x);
-        const float ref = high == -INFINITY ? 0.f : high, keep = __builtin_amdgcn_exp2f(top - ref);
+        const float ref = high == -INFINITY ? 0.f : high, keep = __builtin_amdgcn_exp2f((top - ref) * to2);
         top = high;
         l *= keep;
         o *= keep;
 #pragma unroll
         for (int x = 1; x < JW; ++x) {
-            const float w = __builtin_amdgcn_exp2f(s_ml[slot][x].x - ref);
+            const float w = __builtin_amdgcn_exp2f((s_ml[slot][x].x - ref) * to2);
             l = fmaf(w, s_ml[slot][x].y, l);
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = fmaf(w, s_o[slot][x][c][e], o[e]);
@@ -736,7 +750,7 @@ __global__ __launch_bounds__(256) void paged_attention_join_kernel(AttentionArgs
     if (!cut) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     io<T>::st4(static_cast<T *>(a.o) + at * D + 4 * c, o * inv);
-    if (a.lse && c == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * (1.f / kLog2e);
+    if (a.lse && c == 0) a.lse[at] = row_lse(a, top, l);
 }
 
 constexpr int kJoinRows = 2048;      // most rows that take a workgroup each

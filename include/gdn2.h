@@ -793,8 +793,10 @@ size_t gdn2_paged_attention_step_workspace_bytes(const gdn2_attention_dims *dims
  * p = seq_lens[n] - T + t and sees the places j <= p, with a window those with j > p - window:
  *     s_j = scale q . k_j,   o = sum_j softmax(s)_j v_j,   lse = log sum_j e^(s_j)
  * A token that sees nothing (an empty sequence; more new tokens than the sequence has) gives o = 0
- * and lse = -inf. What lies in the pages at places that a token does not see is not used for it, NaN
- * included; of those that it sees, an infinite value gives inf or NaN in its element of o.
+ * and lse = -inf, and so does one all of whose products are -inf. A key whose scaled product is -inf
+ * takes no part beside others, whatever the scale's sign. What lies in the pages at places that a
+ * token does not see is not used for it, NaN included; of those that it sees, an infinite value gives
+ * inf or NaN in its element of o.
  *   q            device [N, T, h_q, d]
  *   k_pages, v_pages   device [num_pages][h_k][page_size][d], 16-byte aligned
  *   page_table   device int32 [N][max_pages]: the page of each page_size tokens of a sequence. Only
