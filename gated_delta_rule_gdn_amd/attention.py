@@ -181,11 +181,9 @@ def qk_rotary_bwd(q, k: Optional[torch.Tensor], cos_sin, dq_out,
                   workspace: Optional[torch.Tensor] = None) -> dict:
     """Gradients of qk_rotary_fwd given dq_out = dL/dq_out and dk_out = dL/dk_out (both in q's dtype
     or both in fp32). Returns dq (and dk) in that dtype, and dq_weight, dk_weight fp32 [d] for the
-    weights given."""
+    weights given (zeros for k_weight without keys)."""
     if (dk_out is None) != (k is None):
         raise ValueError("k and dk_out go together")
-    if k is None:
-        k_weight = None
     gt = dq_out.dtype
     d, ptrs = _rotary_dims(q, k, None, cos_sin, positions, q_weight, k_weight, interleaved, eps,
                            _grad_code("dq_out", dq_out, q.dtype))

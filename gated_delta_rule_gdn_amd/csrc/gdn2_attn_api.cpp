@@ -46,7 +46,7 @@ gdn2::RotaryArgs rotary_args(const gdn2_rotary_dims *d, const void *q, const voi
                              const int32_t *positions, const float *q_weight, const float *k_weight) {
     gdn2::RotaryArgs a;
     a.q = q; a.k = k; a.cos_sin = cos_sin; a.positions = positions;
-    a.q_weight = q_weight; a.k_weight = d->h_k > 0 ? k_weight : nullptr;
+    a.q_weight = q_weight; a.k_weight = k_weight;
     a.tokens = d->batch * d->seqlen; a.seqlen = d->seqlen;
     a.h_q = d->h_q; a.h_k = d->h_k; a.d = d->d; a.d_rot = d->d_rot; a.num_positions = d->num_positions;
     a.q_stride = d->q_stride ? d->q_stride : static_cast<int64_t>(d->h_q) * d->d;
@@ -138,7 +138,7 @@ gdn2_status gdn2_qk_rotary_fwd(const void *q, const void *k, const float *cos_si
         return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input or the other output");
     if (!in_place_ok(q, q_out, dims->q_stride, qrow) || !in_place_ok(k, kout, dims->k_stride, krow))
         return report(GDN2_ERR_BAD_SHAPE, "only a contiguous input may be its own output");
-    gdn2::RotaryArgs a = rotary_args(dims, q, k, cos_sin, positions, q_weight, k_weight);
+    gdn2::RotaryArgs a = rotary_args(dims, q, k, cos_sin, positions, q_weight, keys ? k_weight : nullptr);
     a.q_out = q_out; a.k_out = k_out;
     return done(gdn2::launch_rotary(a, static_cast<hipStream_t>(stream)), "gdn2_qk_rotary_fwd launch");
 }
@@ -155,7 +155,7 @@ gdn2_status gdn2_qk_rotary_bwd(const void *q, const void *k, const float *cos_si
     gdn2_status st = check_rotary(dims, true);
     if (st != GDN2_OK) return st;
     const bool tokens = dims->batch > 0 && dims->seqlen > 0, keys = dims->h_k > 0;
-    if (!keys) k_weight = nullptr;
+    if (!keys && !dk_weight) k_weight = nullptr;
     if (tokens && (!q || !dq_out || !dq || (keys && (!k || !dk_out || !dk)) || (dims->d_rot > 0 && !cos_sin)))
         return report(GDN2_ERR_NULL_ARG, "q, k, cos_sin, the incoming gradients, dq and dk are required");
     if ((q_weight && !dq_weight) || (k_weight && !dk_weight))

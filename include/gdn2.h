@@ -738,7 +738,8 @@ size_t gdn2_qk_rotary_bwd_workspace_bytes(const gdn2_rotary_dims *dims);
  *   dq_out, dk_out   device, contiguous (grad_dtype): dL/dq_out, dL/dk_out
  *   dq, dk           device, contiguous (grad_dtype); rows of padding tokens come out zero, and give
  *                    nothing to the weights' gradients
- *   dq_weight, dk_weight   device fp32 [d], each required with its weight
+ *   dq_weight, dk_weight   device fp32 [d], each required with its weight. With h_k = 0, dk_weight is
+ *                    zeros, or may be NULL
  *   workspace        at least gdn2_qk_rotary_bwd_workspace_bytes() bytes, 256-byte aligned; not
  *                    needed without weights
  */
