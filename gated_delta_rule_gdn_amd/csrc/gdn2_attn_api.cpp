@@ -136,7 +136,7 @@ gdn2_status gdn2_qk_rotary_fwd(const void *q, const void *k, const float *cos_si
     const void *kouts[] = {kout}, *kins[] = {q, cos_sin, positions, q_weight, k_weight};
     if (aliases(qouts, qins) || aliases(kouts, kins))
         return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input or the other output");
-    if (!in_place_ok(q, q_out, dims->q_stride, qrow) || !in_place_ok(k, kout, dims->k_stride, krow))
+    if (!in_place_ok(q, q_out, dims->q_stride, qrow) || (keys && !in_place_ok(k, kout, dims->k_stride, krow)))
         return report(GDN2_ERR_BAD_SHAPE, "only a contiguous input may be its own output");
     gdn2::RotaryArgs a = rotary_args(dims, q, k, cos_sin, positions, q_weight, keys ? k_weight : nullptr);
     a.q_out = q_out; a.k_out = k_out;

@@ -1,4 +1,5 @@
-"""Gradients of queries alone, with a weight for keys that are not there: nothing to add up, so zeros."""
+"""Queries alone, with keys of no heads or a weight for keys that are not there: the queries' outputs and
+gradients are what they are without, and the weight's gradient is zeros."""
 import ctypes
 
 import pytest
@@ -56,3 +57,16 @@ def test_every_output_is_written_whatever_the_workspace_holds():
         want = g.qk_rotary_bwd(q, None, v["cs"], dq, positions=v["pos"], q_weight=v["qw"], eps=EPS)
         assert torch.equal(dqo, want["dq"]) and torch.equal(dqw, want["dq_weight"])
         assert torch.equal(dkw, torch.zeros_like(dkw)) if asked else torch.isnan(dkw).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T", [(1, 1), (2, 37)])
+def test_forward_with_keys_of_no_heads(B, T, dtype):
+    v = make(T, B, T, 3, 1, 64, 32, dtype)
+    want, _ = g.qk_rotary_fwd(v["q"], None, v["cs"], v["pos"], v["qw"], eps=EPS)
+    nothing = torch.empty(B, T, 0, 64, dtype=dtype, device="cuda")
+    for kw in (None, v["kw"]):
+        q, k = g.qk_rotary_fwd(v["q"], nothing, v["cs"], v["pos"], v["qw"], kw, eps=EPS)
+        assert torch.equal(q, want) and k.shape == nothing.shape
+    q = v["q"].contiguous()
+    assert g.qk_rotary_fwd(q, nothing, v["cs"], v["pos"], v["qw"], eps=EPS, q_out=q)[0] is q and torch.equal(q, want)
