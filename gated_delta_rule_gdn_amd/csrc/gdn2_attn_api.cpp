@@ -58,9 +58,9 @@ gdn2::RotaryArgs rotary_args(const gdn2_rotary_dims *d, const void *q, const voi
     return a;
 }
 
-// An input that its own output may replace: then it has to be contiguous.
-bool in_place_ok(const void *in, const void *out, int64_t stride, int64_t row) {
-    return in != out || stride == 0 || stride == row;
+// An input that its own output may replace: then it has to be contiguous, which one token always is.
+bool in_place_ok(const gdn2_rotary_dims *d, const void *in, const void *out, int64_t stride, int64_t row) {
+    return in != out || stride == 0 || stride == row || (d->batch == 1 && d->seqlen == 1);
 }
 
 size_t rotary_bwd_bytes(const gdn2_rotary_dims *d) {
@@ -136,7 +136,7 @@ gdn2_status gdn2_qk_rotary_fwd(const void *q, const void *k, const float *cos_si
     const void *kouts[] = {kout}, *kins[] = {q, cos_sin, positions, q_weight, k_weight};
     if (aliases(qouts, qins) || aliases(kouts, kins))
         return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input or the other output");
-    if (!in_place_ok(q, q_out, dims->q_stride, qrow) || (keys && !in_place_ok(k, kout, dims->k_stride, krow)))
+    if (!in_place_ok(dims, q, q_out, dims->q_stride, qrow) || (keys && !in_place_ok(dims, k, kout, dims->k_stride, krow)))
         return report(GDN2_ERR_BAD_SHAPE, "only a contiguous input may be its own output");
     gdn2::RotaryArgs a = rotary_args(dims, q, k, cos_sin, positions, q_weight, keys ? k_weight : nullptr);
     a.q_out = q_out; a.k_out = k_out;
@@ -196,7 +196,7 @@ gdn2_status gdn2_qk_rotary_append(const void *q, const void *k, const void *v, c
     const void *pouts[] = {k_pages, v_pages}, *pins[] = {q, k, v, cos_sin, positions, q_weight, k_weight, slots};
     if (aliases(qouts, qins) || aliases(pouts, pins))
         return report(GDN2_ERR_BAD_SHAPE, "an output aliases an input or another output");
-    if (!in_place_ok(q, q_out, dims->q_stride, static_cast<int64_t>(dims->h_q) * dims->d))
+    if (!in_place_ok(dims, q, q_out, dims->q_stride, static_cast<int64_t>(dims->h_q) * dims->d))
         return report(GDN2_ERR_BAD_SHAPE, "only a contiguous input may be its own output");
     gdn2::RotaryArgs a = rotary_args(dims, q, k, cos_sin, positions, q_weight, k_weight);
     a.v = v; a.v_stride = dims->v_stride ? dims->v_stride : krow;
