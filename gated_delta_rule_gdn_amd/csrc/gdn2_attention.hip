@@ -324,7 +324,8 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
     const int lane = threadIdx.x & 63, lg = lane >> 4, li = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // The blocks of rows that share keys are 8 apart: workgroups go round the 8 XCDs, so they find them in
-    // one XCD's cache. `group` is the workgroup's number without that.
+    // one XCD's cache. (Fewer than 8 pairs of a part and a key head leave the other XCDs without work: a prompt
+    // of 4,096 tokens runs at 393 TFLOP/s with 8 key heads of 128, at 105 with 2.) `group` is the workgroup's number without that.
     const int eight = static_cast<int>(blockIdx.x) / (8 * row_blocks), among = static_cast<int>(blockIdx.x) % (8 * row_blocks);
     const int rb = among / 8, pair = 8 * eight + among % 8, group = pair * row_blocks + rb;
     const int h = pair % a.h_k;
@@ -578,8 +579,8 @@ __global__ __launch_bounds__(64 * kWaves, (waves_per_simd<T, D, MT>())) void pag
     // The next tile's keys are under way while this one's weights and values are worked on, its values
     // while its products are. (The last tile loads its own keys again instead: a load that is not
     // always made would have to be waited for at once.) Places that no row sees are in the pool too, and
-    // masked: tiles with such places took the loop of other pages before (8.5 us for 4 sequences of 611
-    // tokens together, now 7.9; 32 x 4 new tokens with a window 42 and 40.5).
+    // masked: in the loop of other pages, tiles with such places take longer (both kernels of 4 sequences of
+    // 611 tokens together 8.5 us in place of 8.0, of 32 x 4 new tokens with a window 42 in place of 40.7).
     int tile = first;
     for (; tile < piped; tile += NEXT) {
         uint32_t ahead[NB];

@@ -75,6 +75,8 @@ hipError_t launch(CopyArgs a, hipStream_t st) {
 
 }  // namespace
 
+// The widest access that suits all pools of the launch. (64 pages of 16 KB in 48 pools, the same ones again:
+// 15.4 us; with a pool of slots of 4 bytes beside them 18.5, of 6 32, of one 66.)
 hipError_t launch_pool_copy(const CopyArgs &a, hipStream_t st) {
     uint64_t low = 0;                // bits of every address and size: their common alignment
     for (int p = 0; p < a.num_pools; ++p)

@@ -8,8 +8,9 @@
 // back by the same angles (a rotation's transpose):
 //     dw = sum over tokens and heads of g x r,     dx = r (g w - x r^2 mean(g w x)).
 //
-// Bound by memory: every value is read once and written once. A head's row lives in the registers
-// of L lanes. A lane holds P units of 2 V values, the two members of V pairs (V neighbours each, so
+// Bound by memory (every value is read once and written once), the forward as much by the vector unit:
+// at 4,096 x 20 bf16 heads of 128 that issues in 83 % of the busy cycles, 11 us. A head's row lives in
+// the registers of L lanes. A lane holds P units of 2 V values, the two members of V pairs (V neighbours each, so
 // a unit is two accesses of up to 16 bytes), and the rotation needs no exchange between lanes; the
 // values that are not rotated are cut into pairs in the same way. A wave takes a token's heads,
 // 64 / L at a time, with the token's cosines and sines and the weights in registers. Sums and
