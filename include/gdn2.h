@@ -797,7 +797,8 @@ size_t gdn2_paged_attention_step_workspace_bytes(const gdn2_attention_dims *dims
  * and lse = -inf, and so does one all of whose products are -inf. A key whose scaled product is -inf
  * takes no part beside others, whatever the scale's sign. What lies in the pages at places that a
  * token does not see is not used for it, NaN included; of those that it sees, an infinite value gives
- * inf or NaN in its element of o.
+ * inf or NaN in its element of o. Weights (1 for the largest) and values are summed in fp32 and divided
+ * at the end, so finite values whose sum leaves fp32 give inf.
  *   q            device [N, T, h_q, d]
  *   k_pages, v_pages   device [num_pages][h_k][page_size][d], 16-byte aligned
  *   page_table   device int32 [N][max_pages]: the page of each page_size tokens of a sequence. Only
